@@ -107,10 +107,12 @@ def _matrices(text):
 
 
 def _products(rows, cols):
-    """Operations that the Newton-Schulz steps of one matrix cannot do without: with m <= n its sides, half of each of
-    the two symmetric products X X^T and A A, and all of B X."""
+    """Operations that the Newton-Schulz steps of one matrix cannot do without, with m <= n its sides. X moves only by
+    polynomials of its Gram matrix, so the steps can be composed: half of the symmetric product X X^T, in each step the
+    half of A A, for each further step three more symmetric products (the next A from this one, the polynomials'
+    product), and all of B X once."""
     m, n = min(rows, cols), max(rows, cols)
-    return STEPS * (m * m * n + m * m * m + 2 * m * m * n)
+    return 3 * m * m * n + (4 * STEPS - 3) * m * m * m
 
 
 def _size(kind):
