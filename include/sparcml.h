@@ -12,6 +12,12 @@
  *              (sparcml_sparse_reduce; sparcml_sparse_reduce_qsgd takes
  *               quantized values; sparcml_qsgd_dense_result quantizes a
  *               dense result)
+ * and the parts of a training step on either side of it:
+ *   - layer norm and its gradients, reduced per node  (sparcml_layer_norm,
+ *               sparcml_layer_norm_backward)
+ *   - momentum from a reduction's result            (sparcml_momentum_step)
+ *   - orthogonalised updates by Newton-Schulz steps  (sparcml_orthogonalize,
+ *               sparcml_orthogonal_step)
  *
  * Sources, cited by page title and section: "SparCML: High-Performance Sparse
  * Communication for Machine Learning" (paperlayer.ai digest of arXiv
@@ -466,6 +472,145 @@ sparcml_status sparcml_qsgd_dense_result(uint32_t bits, uint64_t N, uint32_t buc
                                          uint32_t step, uint32_t node,
                                          const sparcml_reduce_result* d_result, const float* val,
                                          uint8_t* codes, float* scales, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Element types of the dense operators below. Where a call names a type, the
+ * arrays marked "typed" hold elements of it; sums and statistics are fp32 or
+ * wider, and a 16-bit result is rounded once, to nearest even.
+ * ---------------------------------------------------------------------- */
+#define SPARCML_F32 0u
+#define SPARCML_BF16 1u
+#define SPARCML_F16 2u
+
+/* ------------------------------------------------------------------------
+ * Layer norm over rows of `cols` elements.
+ *
+ *   v    = x, or x + residual rounded to the type (returned as `total`)
+ *   mean = sum(v) / cols,  rstd = 1 / sqrt(sum((v - mean)^2) / cols + eps)
+ *   y    = (v - mean) * rstd * weight + bias
+ *
+ *   rows       any number (0: nothing is done), rows * cols < 2^39
+ *   cols       1 <= cols < 2^31
+ *   x          device, typed, read only; row r starts at x + r * x_stride
+ *              (elements; any stride, 0 for one row repeated)
+ *   residual   device, typed, read only, rows r_stride apart; or NULL
+ *   weight, bias  device, [cols] fp32; NULL: ones, zeros
+ *   eps        finite, >= 0
+ *   y          device, typed, [rows][cols]
+ *   total      device, typed, [rows][cols]; NULL exactly when residual is
+ *   mean, rstd device, [rows] fp32
+ * Arrays need the alignment of their elements only; where rows start on
+ * 16-byte borders they are read and written 16 bytes at a time. The outputs
+ * must not overlap each other or the inputs. A NaN or an infinity in a row
+ * makes that row's outputs NaN and touches no other row.
+ * ---------------------------------------------------------------------- */
+sparcml_status sparcml_layer_norm(uint32_t type, uint64_t rows, uint32_t cols, const void* x, uint64_t x_stride,
+                                  const void* residual, uint64_t r_stride, const float* weight, const float* bias,
+                                  float eps, void* y, void* total, float* mean, float* rstd, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Gradients of sparcml_layer_norm for `nodes` nodes of `rows` rows each
+ * (row p * rows + r is row r of node p), with h = (x - mean) * rstd and
+ * g = dy * weight, x being the values that were normed (`total` where there
+ * was a residual):
+ *   dx        = rstd * (g - sum(g) / cols - h * sum(g * h) / cols) [+ dresidual]
+ *   dweight_p = sum over node p's rows of dy * h
+ *   dbias_p   = sum over node p's rows of dy
+ * With a residual, dx (dresidual given: the gradient that reaches `total`
+ * from elsewhere) is the gradient of x and of residual alike. The sums over
+ * rows are added in an order that depends on the sizes alone, so a call
+ * repeated gives the same bits.
+ *
+ *   nodes      1 <= nodes <= 65535, nodes * rows * cols < 2^39
+ *   rows       any number (0: dweight and dbias become 0)
+ *   dy, x      device, typed, read only, rows dy_stride / x_stride apart
+ *   dresidual  device, typed, read only, rows dres_stride apart; or NULL
+ *   weight     device, [cols] fp32; NULL: ones
+ *   mean, rstd device, [nodes * rows] fp32, as sparcml_layer_norm wrote them
+ *   dx         device, typed, [nodes * rows][cols]
+ *   dweight    device, fp32, node p's at dweight + p * dw_stride (dw_stride >=
+ *              cols): for instance columns of the [P][N] gradients that
+ *              sparcml_topk_ef takes, with dw_stride = N; NULL: not wanted
+ *   dbias      the same
+ *   ws         device workspace of sparcml_layer_norm_backward_workspace(nodes,
+ *              rows, cols) bytes, 256-byte aligned; content does not matter
+ * ---------------------------------------------------------------------- */
+size_t sparcml_layer_norm_backward_workspace(uint32_t nodes, uint64_t rows, uint32_t cols);
+
+sparcml_status sparcml_layer_norm_backward(uint32_t type, uint32_t nodes, uint64_t rows, uint32_t cols,
+                                           const void* dy, uint64_t dy_stride, const void* x, uint64_t x_stride,
+                                           const void* dresidual, uint64_t dres_stride, const float* weight,
+                                           const float* mean, const float* rstd, void* dx, float* dweight,
+                                           uint64_t dw_stride, float* dbias, uint64_t db_stride, void* ws,
+                                           size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Momentum from a reduction's result. With g the sum that the reduction
+ * left, sparse or dense as d_result says on the device (no host wait):
+ *   m      = mu * m + scale * g              (in place)
+ *   update = m, or scale * g + mu * m (the new m) with nesterov
+ * at every position; where the result is sparse, g is 0 outside its pairs.
+ *
+ *   N         1 <= N < 2^32, as in the reduction
+ *   d_result  device, the reduction's record, in stream order after it
+ *   idx, val  device, the reduction's out_idx (idx_cap entries; may be NULL
+ *             when idx_cap == 0) and out_val ([N])
+ *   momentum  device, [N] fp32, read and overwritten
+ *   update_type, update  device, typed, [N]; NULL: not wanted
+ * Indices are expected as a reduction writes them (strictly ascending, < N);
+ * others give unspecified values, and no read or write leaves the arrays.
+ * ---------------------------------------------------------------------- */
+sparcml_status sparcml_momentum_step(uint64_t N, const sparcml_reduce_result* d_result, const uint32_t* idx,
+                                     uint64_t idx_cap, const float* val, float* momentum, float mu, float scale,
+                                     uint32_t nesterov, uint32_t update_type, void* update, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Orthogonalised updates. Each matrix G of a flat update goes through
+ *   X = G / (|G|_F + eps), turned so that it is not taller than wide
+ *   X <- a X + (b A + c A A) X,  A = X X^T             `steps` times
+ * which takes its singular values towards 1 for suitable a, b, c.
+ *
+ * sparcml_orthogonalize writes X (turned back) to the matrix's place in
+ * `out`; sparcml_orthogonal_step moves the weights there instead:
+ *   w = (1 - lr * decay) * w - lr * sqrt(max(1, rows / cols)) * X
+ *
+ *   N         length of the flat arrays
+ *   count     matrices; h_offsets, h_rows, h_cols host, [count]: matrix k is
+ *             rows[k] * cols[k] elements, row-major, from offsets[k] on. They
+ *             follow each other (offsets[k] + rows[k] * cols[k] <=
+ *             offsets[k + 1], and <= N at the end); a matrix with no rows or
+ *             columns is passed over. The shorter side is at most 2^16, the
+ *             longer at most 2^24, a matrix at most 2^32 elements, and with
+ *             sides rounded up to 64 all of them hold less than 2^36.
+ *   steps     0 <= steps <= 64 (0: the normalised update)
+ *   eps       finite, >= 0
+ *   update    device, typed (update_type), [N], read only
+ *   out       device, typed (out_type), [N]; only the matrices' elements are
+ *             written
+ *   weight    device, typed (weight_type), [N], read and overwritten
+ *   ws        device workspace of sparcml_orthogonalize_workspace(...) bytes,
+ *             256-byte aligned; content does not matter
+ * sparcml_orthogonalize_workspace returns 0 for arguments the calls reject.
+ *
+ * The products run on the matrix cores, two fp16 parts to a value and fp32
+ * sums: the result is as near to the formula as with fp32 products. The
+ * iterates are held in parts of a power of two of their size, which leaves
+ * room for entries of X up to 15 (they stay below 1.3 with the usual
+ * coefficients 3.4445, -4.7750, 2.0315); beyond it the matrix becomes NaN. A
+ * NaN or an infinity in G makes that matrix NaN and touches no other.
+ * ---------------------------------------------------------------------- */
+size_t sparcml_orthogonalize_workspace(uint64_t N, uint32_t count, const uint64_t* h_offsets, const uint32_t* h_rows,
+                                       const uint32_t* h_cols);
+
+sparcml_status sparcml_orthogonalize(uint64_t N, uint32_t count, const uint64_t* h_offsets, const uint32_t* h_rows,
+                                     const uint32_t* h_cols, uint32_t steps, float a, float b, float c, float eps,
+                                     uint32_t update_type, const void* update, uint32_t out_type, void* out,
+                                     void* ws, size_t ws_bytes, hipStream_t stream);
+
+sparcml_status sparcml_orthogonal_step(uint64_t N, uint32_t count, const uint64_t* h_offsets, const uint32_t* h_rows,
+                                       const uint32_t* h_cols, uint32_t steps, float a, float b, float c, float eps,
+                                       uint32_t update_type, const void* update, uint32_t weight_type, void* weight,
+                                       double lr, double decay, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* Uniform-model estimate of K used when no hint is given (Appendix B.1):
  * N * (1 - prod_p (1 - nnz_p / N)), capped by sum_p nnz_p. Host only. */

@@ -1,5 +1,7 @@
 """MI355X (gfx950) SparCML hot path: error-feedback Top-k, 2/4/8-bit stochastic
-quantization and sparse reduction with the dense switch.
+quantization and sparse reduction with the dense switch; and around it, layer
+norm with per-node gradients, momentum from a reduction's result and
+orthogonalised updates.
 
 Thin ctypes binding over the C ABI in include/sparcml.h: it checks tensor
 dtype/device/contiguity, allocates outputs and workspaces with torch, and
@@ -88,6 +90,23 @@ def _load():
     L.sparcml_sparse_reduce_sums.restype = st
     L.sparcml_sparse_reduce_noalloc.argtypes = [u32, u64, f64, vp, vp, vp, u64, vp, vp, vp, vp]
     L.sparcml_sparse_reduce_noalloc.restype = st
+    f32 = ctypes.c_float
+    L.sparcml_layer_norm.argtypes = [u32, u64, u32, vp, u64, vp, u64, vp, vp, f32, vp, vp, vp, vp, vp]
+    L.sparcml_layer_norm.restype = st
+    L.sparcml_layer_norm_backward_workspace.argtypes = [u32, u64, u32]
+    L.sparcml_layer_norm_backward_workspace.restype = sz
+    L.sparcml_layer_norm_backward.argtypes = [u32, u32, u64, u32, vp, u64, vp, u64, vp, u64, vp, vp, vp, vp, vp, u64,
+                                              vp, u64, vp, sz, vp]
+    L.sparcml_layer_norm_backward.restype = st
+    L.sparcml_momentum_step.argtypes = [u64, vp, vp, u64, vp, vp, f32, f32, u32, u32, vp, vp]
+    L.sparcml_momentum_step.restype = st
+    L.sparcml_orthogonalize_workspace.argtypes = [u64, u32, vp, vp, vp]
+    L.sparcml_orthogonalize_workspace.restype = sz
+    L.sparcml_orthogonalize.argtypes = [u64, u32, vp, vp, vp, u32, f32, f32, f32, f32, u32, vp, u32, vp, vp, sz, vp]
+    L.sparcml_orthogonalize.restype = st
+    L.sparcml_orthogonal_step.argtypes = [u64, u32, vp, vp, vp, u32, f32, f32, f32, f32, u32, vp, u32, vp, f64, f64,
+                                          vp, sz, vp]
+    L.sparcml_orthogonal_step.restype = st
     L.sparcml_estimate_nnz.argtypes = [u32, u64, vp]
     L.sparcml_estimate_nnz.restype = f64
     ev = ctypes.POINTER(BenchEvents)
@@ -625,3 +644,239 @@ def sparse_reduce_noalloc(offsets, idx: torch.Tensor, val: torch.Tensor, N: int,
                                                _ptr(result), ctypes.c_void_p(_stream(dev)))
     _raise(st, "sparcml_sparse_reduce_noalloc")
     return ReduceOutput(result, out_idx, out_val, N)
+
+
+# ---------------------------------------------------------------------------
+_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # SPARCML_F32, SPARCML_BF16, SPARCML_F16
+
+
+def _type(dtype, name: str) -> int:
+    t = _TYPES.get(dtype)
+    if t is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, not {dtype}")
+    return t
+
+
+def _row_stride(t: torch.Tensor, like: torch.Tensor, name: str) -> int:
+    """Elements from one row to the next of `t`, a GPU tensor of `like`'s shape
+    and type whose rows (the last dimension) are contiguous and evenly spaced."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != like.dtype or t.shape != like.shape:
+        raise TypeError(f"{name} must be a {like.dtype} tensor of shape {tuple(like.shape)} on a GPU")
+    if t.is_contiguous():
+        return t.shape[-1]
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    step, size = None, 1  # of the dimensions from the inside out
+    for d in range(t.dim() - 2, -1, -1):
+        n = t.shape[d]
+        if n == 1:
+            continue
+        if step is None:
+            step = t.stride(d)
+        elif t.stride(d) != step * size:
+            raise ValueError(f"{name}'s rows must be evenly spaced")
+        size *= n
+    return t.shape[-1] if step is None else step
+
+
+def _vector(t: Optional[torch.Tensor], n: int, name: str):
+    if t is not None:
+        _check_dev(t, torch.float32, name)
+        if t.numel() != n:
+            raise ValueError(f"{name} must have {n} elements")
+
+
+def _given(t: Optional[torch.Tensor], shape, dtype, dev, name: str) -> torch.Tensor:
+    """The caller's output, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _check_dev(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    return t
+
+
+def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               eps: float = 1e-5, residual: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+               mean: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None,
+               total: Optional[torch.Tensor] = None):
+    """Layer norm over the last dimension of `x` (fp32, bf16 or fp16; rows may
+    be slices of a wider buffer), with fp32 `weight` and `bias`. Returns (y,
+    mean, rstd), mean and rstd fp32 of x.shape[:-1]; with `residual`, x +
+    residual is what is normed, and (y, mean, rstd, total) come back with that sum."""
+    if not isinstance(x, torch.Tensor) or x.dim() == 0:
+        raise TypeError("x must be a tensor of rows")
+    t = _type(x.dtype, "x")
+    xs = _row_stride(x, x, "x")
+    shape = x.shape
+    cols = shape[-1]
+    rows = x.numel() // cols if cols else 0
+    rs = 0 if residual is None else _row_stride(residual, x, "residual")
+    _vector(weight, cols, "weight")
+    _vector(bias, cols, "bias")
+    dev = x.device
+    y = _given(y, shape, x.dtype, dev, "y")
+    mean = _given(mean, shape[:-1], torch.float32, dev, "mean")
+    rstd = _given(rstd, shape[:-1], torch.float32, dev, "rstd")
+    if residual is not None:
+        total = _given(total, shape, x.dtype, dev, "total")
+    elif total is not None:
+        raise ValueError("total needs a residual")
+    st = _load().sparcml_layer_norm(t, rows, cols, _ptr(x), xs, _ptr(residual), rs, _ptr(weight), _ptr(bias), eps,
+                                    _ptr(y), _ptr(total), _ptr(mean), _ptr(rstd), _stream(dev))
+    _raise(st, "sparcml_layer_norm")
+    return (y, mean, rstd) if residual is None else (y, mean, rstd, total)
+
+
+def layer_norm_backward_workspace_bytes(nodes: int, rows: int, cols: int) -> int:
+    return int(_load().sparcml_layer_norm_backward_workspace(nodes, rows, cols))
+
+
+def _node_rows(t: Optional[torch.Tensor], nodes: int, cols: int, dev, name: str):
+    """A per-node gradient's tensor and the elements from one node to the next."""
+    if t is None:
+        return torch.empty((nodes, cols), dtype=torch.float32, device=dev), cols
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_cuda:
+        raise TypeError(f"{name} must be a float32 tensor on a GPU")
+    if tuple(t.shape) != (nodes, cols) or (cols > 1 and t.stride(1) != 1) or (nodes > 1 and t.stride(0) < cols):
+        raise ValueError(f"{name} must be [{nodes}, {cols}] with contiguous rows that do not overlap")
+    return t, max(t.stride(0), cols)
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor], mean: torch.Tensor,
+                        rstd: torch.Tensor, nodes: int = 1, dresidual: Optional[torch.Tensor] = None,
+                        dx: Optional[torch.Tensor] = None, dweight: Optional[torch.Tensor] = None,
+                        dbias: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """Gradients of layer_norm: (dx like x, dweight [nodes, D], dbias [nodes, D],
+    both fp32). `x` is what was normed (`total` where there was a residual); its
+    rows belong to `nodes` nodes in equal parts, one after the other.
+    `dresidual`, the gradient that reaches the residual stream from elsewhere,
+    is added to dx. dweight and dbias may be columns of the [P, N] gradients."""
+    if not isinstance(x, torch.Tensor) or x.dim() == 0:
+        raise TypeError("x must be a tensor of rows")
+    t = _type(x.dtype, "x")
+    xs = _row_stride(x, x, "x")
+    ds = _row_stride(dy, x, "dy")
+    rs = 0 if dresidual is None else _row_stride(dresidual, x, "dresidual")
+    cols = x.shape[-1]
+    if cols == 0:
+        raise ValueError("x's rows are empty")
+    rows = x.numel() // cols
+    if nodes < 1 or rows % nodes:
+        raise ValueError(f"{rows} rows do not belong to {nodes} nodes in equal parts")
+    _vector(weight, cols, "weight")
+    _check_dev(mean, torch.float32, "mean")
+    _check_dev(rstd, torch.float32, "rstd")
+    if mean.numel() != rows or rstd.numel() != rows:
+        raise ValueError(f"mean and rstd must have {rows} elements")
+    dev = x.device
+    dx = _given(dx, x.shape, x.dtype, dev, "dx")
+    dweight, ws = _node_rows(dweight, nodes, cols, dev, "dweight")
+    dbias, bs = _node_rows(dbias, nodes, cols, dev, "dbias")
+    L = _load()
+    if workspace is None:
+        need = L.sparcml_layer_norm_backward_workspace(nodes, rows // nodes, cols)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    st = L.sparcml_layer_norm_backward(t, nodes, rows // nodes, cols, _ptr(dy), ds, _ptr(x), xs, _ptr(dresidual), rs,
+                                       _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(dweight), ws,
+                                       _ptr(dbias), bs, _ptr(workspace), workspace.numel(), _stream(dev))
+    _raise(st, "sparcml_layer_norm_backward")
+    return dx, dweight, dbias
+
+
+# ---------------------------------------------------------------------------
+def momentum_step(reduced: "ReduceOutput", momentum: torch.Tensor, mu: float, scale: float = 1.0,
+                  nesterov: bool = False, dtype: torch.dtype = torch.float32,
+                  update: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """momentum = mu * momentum + scale * g in place, g the reduction's result
+    (sparse or dense, as the device knows). Returns the update in `dtype`: the
+    momentum, or scale * g + mu * momentum with `nesterov`."""
+    _check_dev(momentum, torch.float32, "momentum")
+    _check_dev(reduced.result, torch.uint8, "result")
+    _check_dev(reduced.out_idx, torch.int32, "out_idx")
+    _check_dev(reduced.out_val, torch.float32, "out_val")
+    N = reduced.N
+    if momentum.numel() != N or reduced.out_val.numel() < N or reduced.result.numel() < 16:
+        raise ValueError(f"momentum and the reduction's result must hold {N} positions")
+    dev = momentum.device
+    if update is None:
+        update = torch.empty(N, dtype=dtype, device=dev)
+    else:
+        _check_dev(update, update.dtype, "update")
+        if update.numel() != N:
+            raise ValueError(f"update must hold {N} positions")
+    st = _load().sparcml_momentum_step(N, _ptr(reduced.result), _ptr(reduced.out_idx), reduced.out_idx.numel(),
+                                       _ptr(reduced.out_val), _ptr(momentum), mu, scale, int(nesterov),
+                                       _type(update.dtype, "update"), _ptr(update), _stream(dev))
+    _raise(st, "sparcml_momentum_step")
+    return update
+
+
+# ---------------------------------------------------------------------------
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)  # quintic whose iterates take (0, 1] to about 0.7 .. 1.2
+
+
+def _matrices(matrices):
+    """Host arrays of [(position, rows, cols)], in ascending order."""
+    n = len(matrices)
+    at, rows, cols = zip(*matrices) if n else ((), (), ())
+    return n, (ctypes.c_uint64 * n)(*at), (ctypes.c_uint32 * n)(*rows), (ctypes.c_uint32 * n)(*cols)
+
+
+def orthogonalize_workspace_bytes(N: int, matrices) -> int:
+    """Bytes of the workspace that orthogonalize and orthogonal_step need."""
+    return int(_load().sparcml_orthogonalize_workspace(N, *_matrices(matrices)))
+
+
+def _flat(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous tensor on a GPU")
+    return _type(t.dtype, name)
+
+
+def orthogonalize(update: torch.Tensor, matrices, dtype: Optional[torch.dtype] = None, steps: int = 5,
+                  coefficients=NEWTON_SCHULZ, eps: float = 1e-7, out: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Orthogonalises every matrix of the flat `update` by Newton-Schulz steps.
+    `matrices` is [(position, rows, cols)], ascending and disjoint, row-major.
+    Returns `out`, like `update` in `dtype` (default: its own), written at the
+    matrices' positions only (a new one is 0 elsewhere)."""
+    kind = _flat(update, "update")
+    N = update.numel()
+    dev = update.device
+    args = _matrices(matrices)
+    L = _load()
+    need = L.sparcml_orthogonalize_workspace(N, *args)
+    if out is None:
+        whole = sum(m[1] * m[2] for m in matrices) == N
+        out = (torch.empty if whole else torch.zeros)(update.shape, dtype=dtype or update.dtype, device=dev)
+    okind = _flat(out, "out")
+    if out.numel() != N or (dtype is not None and out.dtype != dtype):
+        raise ValueError(f"out must hold {N} elements of the dtype asked for")
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    st = L.sparcml_orthogonalize(N, *args, steps, *coefficients, eps, kind, _ptr(update), okind, _ptr(out),
+                                 _ptr(workspace), workspace.numel(), _stream(dev))
+    _raise(st, "sparcml_orthogonalize")
+    return out
+
+
+def orthogonal_step(weight: torch.Tensor, update: torch.Tensor, matrices, lr: float, weight_decay: float = 0.0,
+                    steps: int = 5, coefficients=NEWTON_SCHULZ, eps: float = 1e-7,
+                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Moves the flat `weight` at every matrix's place, in place:
+    w = (1 - lr * weight_decay) * w - lr * sqrt(max(1, rows / cols)) * o, o the
+    orthogonalised matrix of `update` (see orthogonalize). Returns `weight`."""
+    kind, wkind = _flat(update, "update"), _flat(weight, "weight")
+    N = update.numel()
+    if weight.numel() != N:
+        raise ValueError(f"weight must hold {N} elements")
+    args = _matrices(matrices)
+    L = _load()
+    if workspace is None:
+        need = L.sparcml_orthogonalize_workspace(N, *args)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=weight.device)
+    st = L.sparcml_orthogonal_step(N, *args, steps, *coefficients, eps, kind, _ptr(update), wkind, _ptr(weight), lr,
+                                   weight_decay, _ptr(workspace), workspace.numel(), _stream(weight.device))
+    _raise(st, "sparcml_orthogonal_step")
+    return weight

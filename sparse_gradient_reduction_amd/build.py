@@ -16,7 +16,8 @@ LIB = os.path.join(PKG, "libsparcml.so")
 BENCH_LIB = os.path.join(PKG, "libsparcml_bench.so")
 OBJDIR = os.path.join(PKG, "_build")
 
-SOURCES = ["api.hip", "topk_ef.hip", "topk_row.hip", "topk_bucketed.hip", "qsgd.hip", "sparse_reduce.hip"]
+SOURCES = ["api.hip", "topk_ef.hip", "topk_row.hip", "topk_bucketed.hip", "qsgd.hip", "sparse_reduce.hip",
+           "layer_norm.hip", "momentum.hip", "orthogonal.hip"]
 BENCH_SOURCES = ["reference_stream.hip"]
 
 ARCH = "gfx950"

@@ -377,6 +377,124 @@ sparcml_status sparcml_sparse_reduce_qsgd_runs(uint32_t bits, uint32_t bucket, u
 // --------------------------------------------------------------------------
 // Measurement entry points: the calls above with caller-owned events
 // attached to their kernel dispatches.
+// --------------------------------------------------------------------------
+static bool type_ok(uint32_t type) { return type <= SPARCML_F16; }
+static bool typed_ok(const void* p, uint32_t type) {
+  return p && (reinterpret_cast<uintptr_t>(p) & (type == SPARCML_F32 ? 3u : 1u)) == 0;
+}
+static bool f32_ok(const float* p) { return typed_ok(p, SPARCML_F32); }
+
+sparcml_status sparcml_layer_norm(uint32_t type, uint64_t rows, uint32_t cols, const void* x, uint64_t x_stride,
+                                  const void* residual, uint64_t r_stride, const float* weight, const float* bias,
+                                  float eps, void* y, void* total, float* mean, float* rstd, hipStream_t stream) {
+  if (!type_ok(type) || cols == 0 || cols > 0x7FFFFFFFu || !std::isfinite(eps) || eps < 0.0f)
+    return SPARCML_ERR_INVALID_ARG;
+  if (rows >= (1ull << 40) / cols || (residual == nullptr) != (total == nullptr)) return SPARCML_ERR_INVALID_ARG;
+  if (rows == 0) return SPARCML_OK;
+  if (!typed_ok(x, type) || !typed_ok(y, type) || !f32_ok(mean) || !f32_ok(rstd)) return SPARCML_ERR_INVALID_ARG;
+  if (residual && (!typed_ok(residual, type) || !typed_ok(total, type))) return SPARCML_ERR_INVALID_ARG;
+  if ((weight && !f32_ok(weight)) || (bias && !f32_ok(bias))) return SPARCML_ERR_INVALID_ARG;
+  return from_hip(sparcml::layer_norm_launch(type, rows, cols, x, x_stride, residual, r_stride, weight, bias, eps, y,
+                                             total, mean, rstd, stream));
+}
+
+static bool layer_norm_backward_sizes_ok(uint32_t nodes, uint64_t rows, uint32_t cols) {
+  if (nodes == 0 || nodes > 65535u || cols == 0 || cols > 0x7FFFFFFFu) return false;
+  return rows < (1ull << 40) / cols / nodes;
+}
+
+size_t sparcml_layer_norm_backward_workspace(uint32_t nodes, uint64_t rows, uint32_t cols) {
+  if (!layer_norm_backward_sizes_ok(nodes, rows, cols)) return 0;
+  return sparcml::layer_norm_backward_workspace_bytes(nodes, rows, cols);
+}
+
+sparcml_status sparcml_layer_norm_backward(uint32_t type, uint32_t nodes, uint64_t rows, uint32_t cols,
+                                           const void* dy, uint64_t dy_stride, const void* x, uint64_t x_stride,
+                                           const void* dresidual, uint64_t dres_stride, const float* weight,
+                                           const float* mean, const float* rstd, void* dx, float* dweight,
+                                           uint64_t dw_stride, float* dbias, uint64_t db_stride, void* ws,
+                                           size_t ws_bytes, hipStream_t stream) {
+  if (!type_ok(type) || !layer_norm_backward_sizes_ok(nodes, rows, cols)) return SPARCML_ERR_INVALID_ARG;
+  if (rows > 0 && (!typed_ok(dy, type) || !typed_ok(x, type) || !typed_ok(dx, type) || !f32_ok(mean) || !f32_ok(rstd)))
+    return SPARCML_ERR_INVALID_ARG;
+  if ((dresidual && !typed_ok(dresidual, type)) || (weight && !f32_ok(weight))) return SPARCML_ERR_INVALID_ARG;
+  if ((dweight && (!f32_ok(dweight) || dw_stride < cols)) || (dbias && (!f32_ok(dbias) || db_stride < cols)))
+    return SPARCML_ERR_INVALID_ARG;
+  if (!ws || !aligned256(ws) || ws_bytes < sparcml::layer_norm_backward_workspace_bytes(nodes, rows, cols))
+    return SPARCML_ERR_WORKSPACE;
+  return from_hip(sparcml::layer_norm_backward_launch(type, nodes, rows, cols, dy, dy_stride, x, x_stride, dresidual,
+                                                      dres_stride, weight, mean, rstd, dx, dweight, dw_stride, dbias,
+                                                      db_stride, ws, stream));
+}
+
+// --------------------------------------------------------------------------
+sparcml_status sparcml_momentum_step(uint64_t N, const sparcml_reduce_result* d_result, const uint32_t* idx,
+                                     uint64_t idx_cap, const float* val, float* momentum, float mu, float scale,
+                                     uint32_t nesterov, uint32_t update_type, void* update, hipStream_t stream) {
+  if (N == 0 || N > kMaxN || !type_ok(update_type)) return SPARCML_ERR_INVALID_ARG;
+  if (!d_result || (reinterpret_cast<uintptr_t>(d_result) & 7u) || !f32_ok(val) || !f32_ok(momentum))
+    return SPARCML_ERR_INVALID_ARG;
+  if (idx_cap > 0 && (!idx || (reinterpret_cast<uintptr_t>(idx) & 3u))) return SPARCML_ERR_INVALID_ARG;
+  if (update && !typed_ok(update, update_type)) return SPARCML_ERR_INVALID_ARG;
+  return from_hip(sparcml::momentum_launch(N, reinterpret_cast<const sparcml::ReduceResultDev*>(d_result), idx,
+                                           idx_cap, val, momentum, mu, scale, nesterov != 0, update_type, update,
+                                           stream));
+}
+
+// --------------------------------------------------------------------------
+// the matrices follow each other inside the N elements, and their tiles fit one launch
+static bool matrices_ok(uint64_t N, const sparcml::OrthoMatrices& ms) {
+  if (N >= (1ull << 40) || (ms.count > 0 && (!ms.offsets || !ms.rows || !ms.cols))) return false;
+  uint64_t end = 0, tiles = 0;
+  for (uint32_t k = 0; k < ms.count; ++k) {
+    const uint64_t rows = ms.rows[k], cols = ms.cols[k];
+    if (ms.offsets[k] < end || ms.offsets[k] > N || rows * cols > N - ms.offsets[k]) return false;
+    end = ms.offsets[k] + rows * cols;
+    if (rows == 0 || cols == 0) continue;
+    const uint64_t t = sparcml::ortho_tiles(rows, cols);
+    tiles += t;
+    if (t == 0 || tiles >= (1ull << 24)) return false;
+  }
+  return true;
+}
+
+size_t sparcml_orthogonalize_workspace(uint64_t N, uint32_t count, const uint64_t* h_offsets, const uint32_t* h_rows,
+                                       const uint32_t* h_cols) {
+  const sparcml::OrthoMatrices ms{count, h_offsets, h_rows, h_cols};
+  return matrices_ok(N, ms) ? sparcml::ortho_workspace_bytes(ms) : 0;
+}
+
+static sparcml_status ortho_common(uint64_t N, const sparcml::OrthoMatrices& ms, const sparcml::OrthoSteps& s,
+                                   uint32_t update_type, const void* update, uint32_t out_type, void* out,
+                                   bool is_weight, float keep, float move, void* ws, size_t ws_bytes,
+                                   hipStream_t stream) {
+  if (!type_ok(update_type) || !type_ok(out_type) || !matrices_ok(N, ms)) return SPARCML_ERR_INVALID_ARG;
+  if (s.steps > 64 || !std::isfinite(s.a) || !std::isfinite(s.b) || !std::isfinite(s.c) || !std::isfinite(s.eps) ||
+      s.eps < 0.0f)
+    return SPARCML_ERR_INVALID_ARG;
+  if (!std::isfinite(keep) || !std::isfinite(move)) return SPARCML_ERR_INVALID_ARG;
+  if (ms.count == 0 || N == 0) return SPARCML_OK;
+  if (!typed_ok(update, update_type) || !typed_ok(out, out_type)) return SPARCML_ERR_INVALID_ARG;
+  if (!ws || !aligned256(ws) || ws_bytes < sparcml::ortho_workspace_bytes(ms)) return SPARCML_ERR_WORKSPACE;
+  return from_hip(sparcml::ortho_launch(ms, s, update_type, update, out_type, out, is_weight, keep, move, ws, stream));
+}
+
+sparcml_status sparcml_orthogonalize(uint64_t N, uint32_t count, const uint64_t* h_offsets, const uint32_t* h_rows,
+                                     const uint32_t* h_cols, uint32_t steps, float a, float b, float c, float eps,
+                                     uint32_t update_type, const void* update, uint32_t out_type, void* out,
+                                     void* ws, size_t ws_bytes, hipStream_t stream) {
+  return ortho_common(N, {count, h_offsets, h_rows, h_cols}, {steps, a, b, c, eps}, update_type, update, out_type,
+                      out, false, 0.0f, 0.0f, ws, ws_bytes, stream);
+}
+
+sparcml_status sparcml_orthogonal_step(uint64_t N, uint32_t count, const uint64_t* h_offsets, const uint32_t* h_rows,
+                                       const uint32_t* h_cols, uint32_t steps, float a, float b, float c, float eps,
+                                       uint32_t update_type, const void* update, uint32_t weight_type, void* weight,
+                                       double lr, double decay, void* ws, size_t ws_bytes, hipStream_t stream) {
+  return ortho_common(N, {count, h_offsets, h_rows, h_cols}, {steps, a, b, c, eps}, update_type, update, weight_type,
+                      weight, true, (float)(1.0 - lr * decay), (float)lr, ws, ws_bytes, stream);
+}
+
 static sparcml::OpEvents op_events(const sparcml_bench_events* ev) {
   sparcml::OpEvents e;
   if (ev) {

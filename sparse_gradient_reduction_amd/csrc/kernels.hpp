@@ -123,4 +123,40 @@ hipError_t sparse_reduce_launch(uint32_t P, uint64_t N, uint64_t T, const uint64
                                 uint64_t out_idx_cap, float* out_val, ReduceResultDev* d_result, void* ws,
                                 hipStream_t stream, const OpEvents* ev = nullptr, int phase = kReduceBoth);
 
+
+// ---- layer norm (type: SPARCML_F32, _BF16 or _F16; strides in elements) -----
+hipError_t layer_norm_launch(uint32_t type, uint64_t rows, uint32_t cols, const void* x, uint64_t x_stride,
+                             const void* residual, uint64_t r_stride, const float* weight, const float* bias,
+                             float eps, void* y, void* total, float* mean, float* rstd, hipStream_t stream);
+size_t layer_norm_backward_workspace_bytes(uint32_t nodes, uint64_t rows, uint32_t cols);
+hipError_t layer_norm_backward_launch(uint32_t type, uint32_t nodes, uint64_t rows, uint32_t cols, const void* dy,
+                                      uint64_t dy_stride, const void* x, uint64_t x_stride, const void* dresidual,
+                                      uint64_t dres_stride, const float* weight, const float* mean, const float* rstd,
+                                      void* dx, float* dweight, uint64_t dw_stride, float* dbias, uint64_t db_stride,
+                                      void* ws, hipStream_t stream);
+
+// ---- momentum from a reduction's result (update: null if not wanted) --------
+hipError_t momentum_launch(uint64_t N, const ReduceResultDev* result, const uint32_t* idx, uint64_t idx_cap,
+                           const float* val, float* momentum, float mu, float scale, bool nesterov,
+                           uint32_t update_type, void* update, hipStream_t stream);
+
+// ---- orthogonalised updates ---------------------------------------------------
+struct OrthoMatrices {
+  uint32_t count;
+  const uint64_t* offsets;
+  const uint32_t* rows;
+  const uint32_t* cols;
+};
+struct OrthoSteps {
+  uint32_t steps;
+  float a, b, c, eps;
+};
+// 64 x 64 tiles of the matrix with its sides rounded up; 0 if it is too large
+uint64_t ortho_tiles(uint64_t rows, uint64_t cols);
+size_t ortho_workspace_bytes(const OrthoMatrices& ms);
+// is_weight: out = keep * out - move * sqrt(max(1, rows / cols)) * X, else out = X
+hipError_t ortho_launch(const OrthoMatrices& ms, const OrthoSteps& steps, uint32_t update_type, const void* update,
+                        uint32_t out_type, void* out, bool is_weight, float keep, float move, void* ws,
+                        hipStream_t stream);
+
 }  // namespace sparcml
