@@ -164,7 +164,8 @@ def bench_lib():
 
 
 def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    # the handle that torch.cuda.current_stream(device).cuda_stream holds, without the Stream object (3 us)
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _check_dev(t: torch.Tensor, dtype, name: str):
@@ -173,7 +174,7 @@ def _check_dev(t: torch.Tensor, dtype, name: str):
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None or t.numel() == 0 else ctypes.c_void_p(t.data_ptr())
+    return None if t is None or t.numel() == 0 else t.data_ptr()
 
 
 def _raise(status: int, what: str):
@@ -686,10 +687,15 @@ def _vector(t: Optional[torch.Tensor], n: int, name: str):
             raise ValueError(f"{name} must have {n} elements")
 
 
-def _given(t: Optional[torch.Tensor], shape, dtype, dev, name: str) -> torch.Tensor:
-    """The caller's output, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+def _given(t: Optional[torch.Tensor], like: torch.Tensor, name: str, shape=None, dtype=None) -> torch.Tensor:
+    """The caller's output, or a new one, contiguous, on `like`'s device; of
+    its shape and type where none are given."""
+    if shape is None:
+        if t is None:
+            return torch.empty_like(like, memory_format=torch.contiguous_format)
+        shape, dtype = like.shape, like.dtype
+    elif t is None:
+        return like.new_empty(shape, dtype=dtype)
     _check_dev(t, dtype, name)
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}")
@@ -708,18 +714,17 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
         raise TypeError("x must be a tensor of rows")
     t = _type(x.dtype, "x")
     xs = _row_stride(x, x, "x")
-    shape = x.shape
-    cols = shape[-1]
+    cols = x.shape[-1]
     rows = x.numel() // cols if cols else 0
     rs = 0 if residual is None else _row_stride(residual, x, "residual")
     _vector(weight, cols, "weight")
     _vector(bias, cols, "bias")
     dev = x.device
-    y = _given(y, shape, x.dtype, dev, "y")
-    mean = _given(mean, shape[:-1], torch.float32, dev, "mean")
-    rstd = _given(rstd, shape[:-1], torch.float32, dev, "rstd")
+    y = _given(y, x, "y")
+    mean = _given(mean, x, "mean", x.shape[:-1], torch.float32)
+    rstd = _given(rstd, x, "rstd", x.shape[:-1], torch.float32)
     if residual is not None:
-        total = _given(total, shape, x.dtype, dev, "total")
+        total = _given(total, x, "total")
     elif total is not None:
         raise ValueError("total needs a residual")
     st = _load().sparcml_layer_norm(t, rows, cols, _ptr(x), xs, _ptr(residual), rs, _ptr(weight), _ptr(bias), eps,
@@ -732,10 +737,10 @@ def layer_norm_backward_workspace_bytes(nodes: int, rows: int, cols: int) -> int
     return int(_load().sparcml_layer_norm_backward_workspace(nodes, rows, cols))
 
 
-def _node_rows(t: Optional[torch.Tensor], nodes: int, cols: int, dev, name: str):
+def _node_rows(t: Optional[torch.Tensor], nodes: int, cols: int, like: torch.Tensor, name: str):
     """A per-node gradient's tensor and the elements from one node to the next."""
     if t is None:
-        return torch.empty((nodes, cols), dtype=torch.float32, device=dev), cols
+        return like.new_empty((nodes, cols), dtype=torch.float32), cols
     if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_cuda:
         raise TypeError(f"{name} must be a float32 tensor on a GPU")
     if tuple(t.shape) != (nodes, cols) or (cols > 1 and t.stride(1) != 1) or (nodes > 1 and t.stride(0) < cols):
@@ -770,13 +775,13 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
     if mean.numel() != rows or rstd.numel() != rows:
         raise ValueError(f"mean and rstd must have {rows} elements")
     dev = x.device
-    dx = _given(dx, x.shape, x.dtype, dev, "dx")
-    dweight, ws = _node_rows(dweight, nodes, cols, dev, "dweight")
-    dbias, bs = _node_rows(dbias, nodes, cols, dev, "dbias")
+    dx = _given(dx, x, "dx")
+    dweight, ws = _node_rows(dweight, nodes, cols, x, "dweight")
+    dbias, bs = _node_rows(dbias, nodes, cols, x, "dbias")
     L = _load()
     if workspace is None:
         need = L.sparcml_layer_norm_backward_workspace(nodes, rows // nodes, cols)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        workspace = x.new_empty(need, dtype=torch.uint8)
     st = L.sparcml_layer_norm_backward(t, nodes, rows // nodes, cols, _ptr(dy), ds, _ptr(x), xs, _ptr(dresidual), rs,
                                        _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(dweight), ws,
                                        _ptr(dbias), bs, _ptr(workspace), workspace.numel(), _stream(dev))
@@ -800,7 +805,7 @@ def momentum_step(reduced: "ReduceOutput", momentum: torch.Tensor, mu: float, sc
         raise ValueError(f"momentum and the reduction's result must hold {N} positions")
     dev = momentum.device
     if update is None:
-        update = torch.empty(N, dtype=dtype, device=dev)
+        update = momentum.new_empty(N, dtype=dtype)
     else:
         _check_dev(update, update.dtype, "update")
         if update.numel() != N:
@@ -849,12 +854,12 @@ def orthogonalize(update: torch.Tensor, matrices, dtype: Optional[torch.dtype] =
     need = L.sparcml_orthogonalize_workspace(N, *args)
     if out is None:
         whole = sum(m[1] * m[2] for m in matrices) == N
-        out = (torch.empty if whole else torch.zeros)(update.shape, dtype=dtype or update.dtype, device=dev)
+        out = (torch.empty_like if whole else torch.zeros_like)(update, dtype=dtype)
     okind = _flat(out, "out")
     if out.numel() != N or (dtype is not None and out.dtype != dtype):
         raise ValueError(f"out must hold {N} elements of the dtype asked for")
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        workspace = update.new_empty(need, dtype=torch.uint8)
     st = L.sparcml_orthogonalize(N, *args, steps, *coefficients, eps, kind, _ptr(update), okind, _ptr(out),
                                  _ptr(workspace), workspace.numel(), _stream(dev))
     _raise(st, "sparcml_orthogonalize")
@@ -875,7 +880,7 @@ def orthogonal_step(weight: torch.Tensor, update: torch.Tensor, matrices, lr: fl
     L = _load()
     if workspace is None:
         need = L.sparcml_orthogonalize_workspace(N, *args)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=weight.device)
+        workspace = weight.new_empty(need, dtype=torch.uint8)
     st = L.sparcml_orthogonal_step(N, *args, steps, *coefficients, eps, kind, _ptr(update), wkind, _ptr(weight), lr,
                                    weight_decay, _ptr(workspace), workspace.numel(), _stream(weight.device))
     _raise(st, "sparcml_orthogonal_step")

@@ -37,7 +37,7 @@ def _check(out, g, m0, m, u, mu, scale, nesterov):
 
 
 CASES = [(1, 1.0), (1, 0.0), (2, 0.5), (63, 0.3), (255, 1.0), (4095, 0.24), (4096, 0.5), (4097, 0.01), (8193, 0.3),
-         (100003, 0.001), (272474, 0.24), (1 << 20, 0.27), (1000003, 0.0)]
+         (100003, 0.001), (272474, 0.24), (1 << 20, 0.27), (1000003, 0.0), ((1 << 22) + 4099, 0.01), (1 << 22, 0.3)]
 
 
 @pytest.mark.parametrize("nesterov", [False, True])
@@ -58,9 +58,9 @@ def test_momentum(dev, N, density, t, nesterov):
         _check(out, g, m0, m, u, 0.95, 1 / 16, nesterov)
 
 
+@pytest.mark.parametrize("N", [3 * 4096 + 1001, (1 << 22) + 1001])
 @pytest.mark.parametrize("where", ["first", "last", "cluster", "all in one tile", "every 4096th"])
-def test_momentum_of_uneven_pairs(dev, where):
-    N = 3 * 4096 + 1001
+def test_momentum_of_uneven_pairs(dev, where, N):
     keep = {"first": [0], "last": [N - 1], "cluster": list(range(5000, 5600)), "all in one tile": list(range(4096, 8192)),
             "every 4096th": list(range(0, N, 4096))}[where]
     val = torch.randn(len(keep))
@@ -72,9 +72,10 @@ def test_momentum_of_uneven_pairs(dev, where):
     _check(None, g, m0, m, u, 0.9, 1.0, True)
 
 
-def test_momentum_on_slices(dev):
+@pytest.mark.parametrize("N", [5000, 1 << 22])
+def test_momentum_on_slices(dev, N):
     """Arrays off their 16-byte borders."""
-    N = 5000
+    N = N + 5
     keep = list(range(0, N, 3))
     val = torch.randn(len(keep))
     g = torch.zeros(N, dtype=torch.float64)
