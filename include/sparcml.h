@@ -580,7 +580,7 @@ sparcml_status sparcml_momentum_step(uint64_t N, const sparcml_reduce_result* d_
  *             follow each other (offsets[k] + rows[k] * cols[k] <=
  *             offsets[k + 1], and <= N at the end); a matrix with no rows or
  *             columns is passed over. The shorter side is at most 2^16, the
- *             longer at most 2^24, a matrix at most 2^32 elements, and with
+ *             longer at most 2^21, a matrix at most 2^32 elements, and with
  *             sides rounded up to 64 all of them hold less than 2^36.
  *   steps     0 <= steps <= 64 (0: the normalised update)
  *   eps       finite, >= 0

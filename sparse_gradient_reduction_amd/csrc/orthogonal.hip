@@ -29,8 +29,6 @@ namespace sparcml {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr uint32_t kTile = 128;      // rows and columns of one workgroup's tile of a product
-constexpr uint32_t kDepth = 32;      // summed index per pass through LDS
 constexpr uint32_t kPad = 64;        // sides are padded with zeros to this
 constexpr uint32_t kGroups = 24;     // groups of equal matrices in one set of launches
 constexpr uint32_t kParts = 256;     // partial sums of squares of one matrix, at most
@@ -60,36 +58,38 @@ struct Groups {
 };
 
 // A matrix's buffers: partial sums, then X, X^T, the next X and X^T, A and M.
-// Each buffer is a plane of hi and a plane of lo.
+// A row of `ld` values is stored as their hi parts, then their lo parts.
 enum Buffer : uint32_t { kX0, kXT0, kX1, kXT1, kA, kM, kBuffers };
 
-struct Planes {
-  f16* hi;
-  f16* lo;
+struct Plane {
+  f16* p;
   uint32_t ld;
+  __device__ __forceinline__ f16* hi(uint64_t row) const { return p + row * 2 * ld; }
+  __device__ __forceinline__ f16* lo(uint64_t row) const { return p + row * 2 * ld + ld; }
 };
 __host__ __device__ __forceinline__ uint64_t buffers_bytes(uint32_t m, uint32_t n) {
   return kParts * sizeof(double) + 4ull * (4ull * m * n + (uint64_t)(kBuffers - kA) * m * m);
 }
-__device__ __forceinline__ Planes planes(unsigned char* base, uint32_t m, uint32_t n, uint32_t b) {
+__device__ __forceinline__ Plane plane(unsigned char* base, uint32_t m, uint32_t n, uint32_t b) {
   f16* p = reinterpret_cast<f16*>(base + kParts * sizeof(double));
-  const uint64_t x = (uint64_t)m * n, s = (uint64_t)m * m;
-  if (b < kA) return Planes{p + 2 * x * b, p + 2 * x * b + x, (b & 1) ? m : n};
-  p += 2 * x * kA + 2 * s * (b - kA);
-  return Planes{p, p + s, m};
+  const uint64_t x = 2ull * m * n, s = 2ull * m * m;
+  return b < kA ? Plane{p + x * b, (b & 1) ? m : n} : Plane{p + x * kA + s * (b - kA), m};
 }
 
-// This workgroup's item among the groups' `tiles` per matrix: the group, the
-// matrix in it and the tile in the matrix.
+// Workgroups of a launch come in groups of `count * tiles`, rounded up to 8 so
+// that the workgroups of one group spread over the XCDs alike and each XCD
+// walks neighbouring tiles. k may be past the last matrix: nothing to do.
 struct Item {
   uint32_t g, k, tile;
 };
+__host__ __device__ __forceinline__ uint32_t items_of(const Group& g) { return up(g.count * g.tiles, kXcds); }
 __device__ __forceinline__ Item item_of(const Groups& gs, uint32_t b) {
   uint32_t g = 0;
-  while (g + 1 < gs.count && b >= gs.g[g].count * gs.g[g].tiles) {
-    b -= gs.g[g].count * gs.g[g].tiles;
+  while (g + 1 < gs.count && b >= items_of(gs.g[g])) {
+    b -= items_of(gs.g[g]);
     ++g;
   }
+  b = xcd_contiguous(b, items_of(gs.g[g]));
   return Item{g, b / gs.g[g].tiles, b % gs.g[g].tiles};
 }
 
@@ -104,6 +104,7 @@ __global__ __launch_bounds__(kThreads) void k_squares(Groups gs, const T* update
   __shared__ double scratch[kThreads / kWave];
   const Item it = item_of(gs, blockIdx.x);
   const Group& g = gs.g[it.g];
+  if (it.k >= g.count) return;
   const uint64_t size = (uint64_t)g.rows * g.cols, each = (size + g.tiles - 1) / g.tiles;
   const T* x = update + g.at + it.k * size;
   const uint64_t begin = it.tile * each, end = min(begin + each, size);
@@ -123,34 +124,34 @@ __global__ __launch_bounds__(kThreads) void k_split(Groups gs, const T* update, 
   __shared__ double scratch[kThreads / kWave];
   const Item it = item_of(gs, blockIdx.x);
   const Group& g = gs.g[it.g];
+  if (it.k >= g.count) return;
   unsigned char* base = ws + g.ws + it.k * g.ws_of;
   const uint64_t size = (uint64_t)g.rows * g.cols;
   const uint32_t parts = parts_of(size);
   const double* part = reinterpret_cast<const double*>(base);
   const double sum = block_sum_f64<kThreads>(threadIdx.x < parts ? part[threadIdx.x] : 0.0, scratch);
   const double by = (double)kScaleX / (sqrt(sum) + (double)eps);
-  const uint32_t pr = up(g.rows, kPad), pc = up(g.cols, kPad);
+  const uint32_t pc = up(g.cols, kPad);
   const uint32_t r0 = it.tile / (pc / 64) * 64, c0 = it.tile % (pc / 64) * 64;
   const T* x = update + g.at + it.k * size;
   const uint32_t tx = threadIdx.x % 64, ty = threadIdx.x / 64;
   // as stored: the wide X if rows <= cols, else X^T
-  const Planes same = planes(base, g.m(), g.n(), g.tall() ? kXT0 : kX0);
-  const Planes turned = planes(base, g.m(), g.n(), g.tall() ? kX0 : kXT0);
+  const Plane same = plane(base, g.m(), g.n(), g.tall() ? kXT0 : kX0);
+  const Plane turned = plane(base, g.m(), g.n(), g.tall() ? kX0 : kXT0);
   for (uint32_t y = ty; y < 64; y += 4) {
     const uint32_t r = r0 + y, c = c0 + tx;
     const float v = r < g.rows && c < g.cols ? (float)((double)to_f32(x[(uint64_t)r * g.cols + c]) * by) : 0.0f;
     t[y][tx] = v;
     const f16 hi = (f16)v;
-    same.hi[(uint64_t)r * pc + c] = hi;
-    same.lo[(uint64_t)r * pc + c] = (f16)(v - (float)hi);
+    same.hi(r)[c] = hi;
+    same.lo(r)[c] = (f16)(v - (float)hi);
   }
   __syncthreads();
   for (uint32_t y = ty; y < 64; y += 4) {
     const float v = t[tx][y];
     const f16 hi = (f16)v;
-    const uint64_t at = (uint64_t)(c0 + y) * pr + r0 + tx;
-    turned.hi[at] = hi;
-    turned.lo[at] = (f16)(v - (float)hi);
+    turned.hi(c0 + y)[r0 + tx] = hi;
+    turned.lo(c0 + y)[r0 + tx] = (f16)(v - (float)hi);
   }
 }
 
@@ -165,119 +166,232 @@ struct Product {
 };
 enum Out { kPlanes, kResult, kWeight };
 
-// (i, j), j <= i, of the t-th tile on and below the diagonal
-__device__ __forceinline__ void lower_tile(uint32_t t, uint32_t& i, uint32_t& j) {
-  i = (uint32_t)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
-  while ((uint64_t)i * (i + 1) / 2 > t) --i;
-  while ((uint64_t)(i + 1) * (i + 2) / 2 <= t) ++i;
-  j = t - (uint32_t)((uint64_t)i * (i + 1) / 2);
-}
-
 // Scale of the result for the weights: w = keep * w - move * s * X.
 struct Move {
   float keep, move;
 };
 
-template <int OUT, class T>
-__global__ __launch_bounds__(kThreads) void k_product(Groups gs, Product p, unsigned char* ws, T* out, Move mv) {
-  __shared__ f16x8 lds[4][kTile * kDepth / 8];  // A hi, A lo, B hi, B lo
+// Tiles are taken in blocks of 4 x 4 (on and below the diagonal where the
+// result is symmetric), so that the neighbouring ones that share an XCD's L2
+// read few rows of A and B. A slot may lie outside the result.
+constexpr uint32_t kBlock = 4;
+__host__ __device__ __forceinline__ uint32_t tile_slots(uint32_t i, uint32_t j, bool sym) {
+  const uint32_t bi = (i + kBlock - 1) / kBlock, bj = (j + kBlock - 1) / kBlock;
+  return (sym ? bi * (bi + 1) / 2 : bi * bj) * kBlock * kBlock;
+}
+__device__ __forceinline__ void tile_at(uint32_t slot, uint32_t j, bool sym, uint32_t& ti, uint32_t& tj) {
+  const uint32_t b = slot / (kBlock * kBlock), in = slot % (kBlock * kBlock);
+  uint32_t bi, bj;
+  if (sym) {  // the b-th (bi, bj), bj <= bi
+    bi = (uint32_t)((sqrtf(8.0f * (float)b + 1.0f) - 1.0f) * 0.5f);
+    while ((uint64_t)bi * (bi + 1) / 2 > b) --bi;
+    while ((uint64_t)(bi + 1) * (bi + 2) / 2 <= b) ++bi;
+    bj = b - (uint32_t)((uint64_t)bi * (bi + 1) / 2);
+  } else {
+    const uint32_t across = (j + kBlock - 1) / kBlock;
+    bi = b / across;
+    bj = b % across;
+  }
+  ti = bi * kBlock + in % kBlock;
+  tj = bj * kBlock + in / kBlock;
+}
+
+// 16 bytes a lane from memory straight into LDS, at `to` + 16 * lane.
+__device__ __forceinline__ void load_to_lds(const f16* from, f16x8* to) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                   (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+}
+
+// Orders the wave's LDS accesses, whose lanes read what other lanes wrote; the
+// hardware runs them in order.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// The shape of a workgroup's tile: WI x WJ waves, each TI x TJ blocks of
+// 32 x 32, and the parts of its operands: PARTS = 2 multiplies hi and lo
+// (three products), 1 hi alone.
+template <int WI_, int WJ_, int TI_, int TJ_, int PARTS_>
+struct Shape {
+  static constexpr int WI = WI_, WJ = WJ_, TI = TI_, TJ = TJ_, PARTS = PARTS_;
+  static constexpr int W = WI * WJ, NT = W * kWave, I = WI * TI * 32, J = WJ * TJ * 32;
+  static constexpr int DEPTH = 64 / PARTS;  // summed index of a pass: rows of 128 bytes in LDS
+};
+
+// A workgroup multiplies I x J tiles. Two LDS buffers of (I + J) rows of 128
+// bytes (64 of hi, or 32 of hi and 32 of lo): while the waves multiply from
+// one, the next pass's rows go from memory straight into the other, so a pass
+// waits once. A row's eight 16-byte chunks are stored in an order that differs
+// by row (chunk c at c ^ (row % 8)): eight lanes that read the same chunk of
+// eight rows then read eight different bank groups.
+template <class S, int OUT, class T>
+__global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups gs, Product p, unsigned char* ws,
+                                                                        T* out, Move mv) {
+  __shared__ f16x8 lds0[(S::I + S::J) * 8], lds1[(S::I + S::J) * 8];
   const Item it = item_of(gs, blockIdx.x);
   const Group& g = gs.g[it.g];
+  if (it.k >= g.count) return;
   const uint32_t m = g.m(), n = g.n();
-  unsigned char* base = ws + g.ws + it.k * g.ws_of;
-  const Planes a = planes(base, m, n, p.a), b = planes(base, m, n, p.b);
-  const uint32_t J = p.sym ? m : n, K = a.ld;
+  const uint32_t J = p.sym ? m : n;
   uint32_t ti, tj;
-  if (p.sym) {
-    lower_tile(it.tile, ti, tj);
-  } else {
-    const uint32_t across = up(J, kTile) / kTile;
-    ti = it.tile / across;
-    tj = it.tile % across;
-  }
-  const uint32_t lane = lane_id(), wid = threadIdx.x / kWave;
-  const uint32_t wi = wid / 2 * 64, wj = wid % 2 * 64;
-  const bool on = ti * kTile + wi < m && tj * kTile + wj < J;  // this wave's 64 x 64 is inside
+  tile_at(it.tile, (J + S::J - 1) / S::J, p.sym, ti, tj);
+  const uint32_t i0 = ti * S::I, j0 = tj * S::J;
+  if (i0 >= m || j0 >= J || (p.sym && tj > ti)) return;
+  unsigned char* base = ws + g.ws + it.k * g.ws_of;
+  const Plane a = plane(base, m, n, p.a), b = plane(base, m, n, p.b);
+  const uint32_t K = a.ld;
+  const uint32_t lane = lane_id(), wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const uint32_t wi = wid / S::WJ * (S::TI * 32), wj = wid % S::WJ * (S::TJ * 32);
 
-  f32x16 acc[2][2] = {};
-  for (uint32_t k0 = 0; k0 < K; k0 += kDepth) {
-    __syncthreads();
+  // this lane's part of 8 rows of a pass: row lane / 8, stored chunk lane % 8
+  const uint32_t chunk = lane % 8 ^ lane / 8;
+  const uint32_t from = S::PARTS == 2 ? chunk / 4 * K + chunk % 4 * 8 : chunk * 8;
+  constexpr int LA = S::I / 8 / S::W, LB = S::J / 8 / S::W;
+  const f16 *pa = a.hi(i0), *pb = b.hi(j0);
+  uint32_t src[LA + LB];  // elements from there; at most 256 rows of 2 * 2^21
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t chunk = threadIdx.x + h * kThreads, row = chunk / 4, c = chunk % 4;
-      const uint32_t slot = row * 4 + (c ^ (row >> 1 & 3));  // 8 rows of one chunk fall into 8 bank groups
-      const uint64_t ra = (uint64_t)min(ti * kTile + row, m - 1) * K + k0 + c * 8;
-      const uint64_t rb = (uint64_t)min(tj * kTile + row, J - 1) * K + k0 + c * 8;
-      lds[0][slot] = *reinterpret_cast<const f16x8*>(a.hi + ra);
-      lds[1][slot] = *reinterpret_cast<const f16x8*>(a.lo + ra);
-      lds[2][slot] = *reinterpret_cast<const f16x8*>(b.hi + rb);
-      lds[3][slot] = *reinterpret_cast<const f16x8*>(b.lo + rb);
-    }
-    __syncthreads();
-    if (on) {
-#pragma unroll
-      for (uint32_t ks = 0; ks < kDepth / 16; ++ks) {
-        f16x8 f[4][2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const uint32_t ra = wi + q * 32 + lane % 32, rb = wj + q * 32 + lane % 32, c = ks * 2 + lane / 32;
-          f[0][q] = lds[0][ra * 4 + (c ^ (ra >> 1 & 3))];
-          f[1][q] = lds[1][ra * 4 + (c ^ (ra >> 1 & 3))];
-          f[2][q] = lds[2][rb * 4 + (c ^ (rb >> 1 & 3))];
-          f[3][q] = lds[3][rb * 4 + (c ^ (rb >> 1 & 3))];
-        }
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[0][x], f[2][y], acc[x][y], 0, 0, 0);
-            acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[0][x], f[3][y], acc[x][y], 0, 0, 0);
-            acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[1][x], f[2][y], acc[x][y], 0, 0, 0);
-          }
-      }
-    }
+  for (int t = 0; t < LA + LB; ++t) {
+    const uint32_t r = (t < LA ? t : t - LA) * S::W * 8 + wid * 8 + lane / 8;
+    src[t] = min(r, (t < LA ? m - i0 : J - j0) - 1) * 2 * K + from;
   }
-  if (!on) return;
-  const Planes c = planes(base, m, n, p.c_ji), dij = planes(base, m, n, p.d_ij), dji = planes(base, m, n, p.d_ji);
+  const auto load = [&](f16x8* lds) {
+#pragma unroll
+    for (int t = 0; t < LA + LB; ++t) {
+      load_to_lds((t < LA ? pa : pb) + src[t], lds + (t * S::W + wid) * 64);
+    }
+    pa += S::DEPTH;
+    pb += S::DEPTH;
+  };
+
+  f32x16 acc[S::TI][S::TJ] = {};
+  const auto multiply = [&](const f16x8* lds) {
+#pragma unroll
+    for (int ks = 0; ks < S::DEPTH / 16; ++ks) {
+      f16x8 fa[S::PARTS][S::TI], fb[S::PARTS][S::TJ];
+#pragma unroll
+      for (int h = 0; h < S::PARTS; ++h) {
+        const uint32_t c = (ks * 2 + h * 4 + lane / 32) ^ lane % 8;  // h: only with DEPTH 32, chunks 4 .. 7
+#pragma unroll
+        for (int q = 0; q < S::TI; ++q) fa[h][q] = lds[(wi + q * 32 + lane % 32) * 8 + c];
+#pragma unroll
+        for (int q = 0; q < S::TJ; ++q) fb[h][q] = lds[(S::I + wj + q * 32 + lane % 32) * 8 + c];
+      }
+#pragma unroll
+      for (int x = 0; x < S::TI; ++x)
+#pragma unroll
+        for (int y = 0; y < S::TJ; ++y) {
+          acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[0][x], fb[0][y], acc[x][y], 0, 0, 0);
+          if constexpr (S::PARTS == 2) {
+            acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[0][x], fb[1][y], acc[x][y], 0, 0, 0);
+            acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[1][x], fb[0][y], acc[x][y], 0, 0, 0);
+          }
+        }
+      __builtin_amdgcn_sched_barrier(0);  // one part's operands at a time: the accumulators leave no room for more
+    }
+  };
+
+  const uint32_t passes = K / S::DEPTH;
+  load(lds0);
+  for (uint32_t k = 0; k < passes; k += 2) {
+    __syncthreads();  // buffer 0 is filled, buffer 1 no longer read
+    if (k + 1 < passes) load(lds1);
+    multiply(lds0);
+    if (k + 1 == passes) break;
+    __syncthreads();
+    if (k + 2 < passes) load(lds0);
+    multiply(lds1);
+  }
+
+  // A wave turns its blocks of 32 x 32 through LDS: lane l finishes row l / 2,
+  // half l % 2, of the block's 32 rows of 32, and so moves 32 bytes at a time.
+  __syncthreads();
+  uint32_t* turn = reinterpret_cast<uint32_t*>(lds0) + wid * 32 * 33;
+  const Plane c = plane(base, m, n, p.c_ji), dij = plane(base, m, n, p.d_ij), dji = plane(base, m, n, p.d_ji);
   const float move = mv.move * sqrtf(fmaxf(1.0f, (float)g.rows / (float)g.cols));
   T* o = out + g.at + it.k * (uint64_t)g.rows * g.cols;
+  const uint32_t row = lane / 2, half = lane % 2 * 16;
 #pragma unroll
-  for (int x = 0; x < 2; ++x)
+  for (int x = 0; x < S::TI; ++x)
 #pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      const uint32_t j = tj * kTile + wj + y * 32 + lane % 32;
+    for (int y = 0; y < S::TJ; ++y) {
+      const uint32_t ix = i0 + wi + x * 32, jx = j0 + wj + y * 32;
+      if (ix >= m || jx >= J) continue;  // blocks of 32 lie inside or outside
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {  // 4 consecutive i
-        const uint32_t i = ti * kTile + wi + x * 32 + q * 8 + lane / 32 * 4;
-        f16x4 ch = {}, cl = {};
-        if (p.beta != 0.0f) {
-          ch = *reinterpret_cast<const f16x4*>(c.hi + (uint64_t)j * c.ld + i);
-          cl = *reinterpret_cast<const f16x4*>(c.lo + (uint64_t)j * c.ld + i);
-        }
-        f16x4 dh, dl;
+      for (int e = 0; e < 16; ++e)
+        turn[lane % 32 * 33 + e / 4 * 8 + lane / 32 * 4 + e % 4] = __float_as_uint(acc[x][y][e]);
+      wave_fence();
+      const uint32_t j = jx + row, i = ix + half;
+      float v[16];
+      f16x8 ch[2] = {}, cl[2] = {};
+      if (p.beta != 0.0f) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float v = fmaf(p.alpha, acc[x][y][q * 4 + e], p.beta * ((float)ch[e] + (float)cl[e]));
-          if (OUT == kPlanes) {
-            dh[e] = (f16)v;
-            dl[e] = (f16)(v - (float)dh[e]);
-            if (!(p.sym && ti == tj)) {
-              dij.hi[(uint64_t)(i + e) * dij.ld + j] = dh[e];
-              dij.lo[(uint64_t)(i + e) * dij.ld + j] = dl[e];
-            }
-          } else {
-            const uint32_t r = g.tall() ? j : i + e, col = g.tall() ? i + e : j;
-            if (r < g.rows && col < g.cols) {
-              const uint64_t at = (uint64_t)r * g.cols + col;
-              o[at] = from_f32<T>(OUT == kWeight ? fmaf(mv.keep, to_f32(o[at]), -move * v) : v);
-            }
-          }
-        }
-        if (OUT == kPlanes) {
-          *reinterpret_cast<f16x4*>(dji.hi + (uint64_t)j * dji.ld + i) = dh;
-          *reinterpret_cast<f16x4*>(dji.lo + (uint64_t)j * dji.ld + i) = dl;
+        for (int q = 0; q < 2; ++q) {
+          ch[q] = reinterpret_cast<const f16x8*>(c.hi(j) + i)[q];
+          cl[q] = reinterpret_cast<const f16x8*>(c.lo(j) + i)[q];
         }
       }
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        v[e] = fmaf(p.alpha, __uint_as_float(turn[row * 33 + half + e]),
+                    p.beta * ((float)ch[e / 8][e % 8] + (float)cl[e / 8][e % 8]));
+      if constexpr (OUT == kPlanes) {
+        f16x8 dh[2], dl[2];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const f16 h = (f16)v[e], l = (f16)(v[e] - (float)h);
+          dh[e / 8][e % 8] = h;
+          dl[e / 8][e % 8] = l;
+          turn[row * 33 + half + e] = (uint32_t)__builtin_bit_cast(uint16_t, h) |
+                                      (uint32_t)__builtin_bit_cast(uint16_t, l) << 16;
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          reinterpret_cast<f16x8*>(dji.hi(j) + i)[q] = dh[q];
+          reinterpret_cast<f16x8*>(dji.lo(j) + i)[q] = dl[q];
+        }
+        if (!(p.sym && ti == tj)) {
+          wave_fence();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const uint32_t w = turn[(half + e) * 33 + row];
+            dh[e / 8][e % 8] = __builtin_bit_cast(f16, (uint16_t)w);
+            dl[e / 8][e % 8] = __builtin_bit_cast(f16, (uint16_t)(w >> 16));
+          }
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            reinterpret_cast<f16x8*>(dij.hi(ix + row) + jx + half)[q] = dh[q];
+            reinterpret_cast<f16x8*>(dij.lo(ix + row) + jx + half)[q] = dl[q];
+          }
+        }
+      } else {
+        uint32_t r = j, col = i;  // tall: the result's rows are j
+        if (!g.tall()) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) turn[row * 33 + half + e] = __float_as_uint(v[e]);
+          wave_fence();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(turn[(half + e) * 33 + row]);
+          r = ix + row;
+          col = jx + half;
+        }
+        if (r < g.rows) {
+          constexpr int N = Pack<T>::N;
+#pragma unroll
+          for (int q = 0; q < 16 / N; ++q) {
+            const int64_t room = (int64_t)g.cols - col - q * N;
+            if (room <= 0) break;
+            T* at = o + (uint64_t)r * g.cols + col + q * N;
+            typename Pack<T>::V w = {};
+            if (OUT == kWeight) w = load_pack(at, room);
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+              w[e] = from_f32<T>(OUT == kWeight ? fmaf(mv.keep, to_f32((T)w[e]), -move * v[q * N + e]) : v[q * N + e]);
+            store_pack(w, at, room);
+          }
+        }
+      }
+      wave_fence();  // before the next block's values
     }
 }
 
@@ -288,6 +402,7 @@ __global__ __launch_bounds__(kThreads) void k_normalised(Groups gs, const S* upd
   __shared__ double scratch[kThreads / kWave];
   const Item it = item_of(gs, blockIdx.x);
   const Group& g = gs.g[it.g];
+  if (it.k >= g.count) return;
   const uint64_t size = (uint64_t)g.rows * g.cols, each = (size + g.tiles - 1) / g.tiles;
   const double* part = reinterpret_cast<const double*>(ws + g.ws + it.k * g.ws_of);
   const double sum = block_sum_f64<kThreads>(threadIdx.x < g.tiles ? part[threadIdx.x] : 0.0, scratch);
@@ -336,7 +451,7 @@ uint32_t tiled(Groups& gs, F&& of) {
   uint64_t all = 0;
   for (uint32_t k = 0; k < gs.count; ++k) {
     gs.g[k].tiles = of(gs.g[k]);
-    all += (uint64_t)gs.g[k].tiles * gs.g[k].count;
+    all += items_of(gs.g[k]);
   }
   return (uint32_t)all;
 }
@@ -344,13 +459,32 @@ uint32_t parts_of_host(const Group& g) {
   return (uint32_t)std::min<uint64_t>(((uint64_t)g.rows * g.cols + 8191) / 8192, kParts);
 }
 
-template <int OUT, class T>
-hipError_t launch_product(Groups& gs, const Product& p, unsigned char* ws, T* out, Move mv, hipStream_t stream) {
-  const uint32_t blocks = tiled(gs, [&](const Group& g) {
-    const uint32_t i = up(g.m(), kTile) / kTile, j = up(g.n(), kTile) / kTile;
-    return p.sym ? i * (i + 1) / 2 : i * j;
+template <class S>
+uint32_t product_blocks(Groups& gs, const Product& p) {
+  return tiled(gs, [&](const Group& g) {
+    return tile_slots((g.m() + S::I - 1) / S::I, ((p.sym ? g.m() : g.n()) + S::J - 1) / S::J, p.sym);
   });
-  hipLaunchKernelGGL((k_product<OUT, T>), dim3(blocks), dim3(kThreads), 0, stream, gs, p, ws, out, mv);
+}
+template <class S>
+uint64_t product_tiles(const Groups& gs, const Product& p) {
+  uint64_t all = 0;
+  for (uint32_t k = 0; k < gs.count; ++k) {
+    const uint64_t i = (gs.g[k].m() + S::I - 1) / S::I, j = ((p.sym ? gs.g[k].m() : gs.g[k].n()) + S::J - 1) / S::J;
+    all += gs.g[k].count * (p.sym ? i * (i + 1) / 2 : i * j);
+  }
+  return all;
+}
+
+template <int PARTS, int OUT, class T>
+hipError_t launch_product(Groups& gs, const Product& p, unsigned char* ws, T* out, Move mv, hipStream_t stream) {
+  using Large = Shape<2, 4, 4, 2, PARTS>;  // 256 x 256, 8 waves
+  using Small = Shape<2, 2, 2, 2, PARTS>;  // 128 x 128, 4 waves
+  if (product_tiles<Large>(gs, p) >= 256)
+    hipLaunchKernelGGL((k_product<Large, OUT, T>), dim3(product_blocks<Large>(gs, p)), dim3(Large::NT), 0, stream, gs,
+                       p, ws, out, mv);
+  else
+    hipLaunchKernelGGL((k_product<Small, OUT, T>), dim3(product_blocks<Small>(gs, p)), dim3(Small::NT), 0, stream, gs,
+                       p, ws, out, mv);
   return hipGetLastError();
 }
 
@@ -371,9 +505,9 @@ hipError_t run(Groups& gs, const OrthoSteps& s, const S* update, T* out, Move mv
   e = hipGetLastError();
   for (uint32_t k = 0; k < s.steps && e == hipSuccess; ++k) {
     const uint32_t x = k % 2 ? kX1 : kX0, y = k % 2 ? kX0 : kX1;  // the step's X and the next
-    e = launch_product<kPlanes, T>(gs, Product{x, x, x, kA, kA, 1, 1.0f / kScaleX, 0.0f}, ws, nullptr, mv, stream);
+    e = launch_product<2, kPlanes, T>(gs, Product{x, x, x, kA, kA, 1, 1.0f / kScaleX, 0.0f}, ws, nullptr, mv, stream);
     if (e != hipSuccess) break;
-    e = launch_product<kPlanes, T>(gs,
+    e = launch_product<2, kPlanes, T>(gs,
                                    Product{kA, kA, kA, kM, kM, 1, s.c * kScaleM / (kScaleX * kScaleX),
                                            s.b * kScaleM / kScaleX},
                                    ws, nullptr, mv, stream);
@@ -381,8 +515,8 @@ hipError_t run(Groups& gs, const OrthoSteps& s, const S* update, T* out, Move mv
     const bool last = k + 1 == s.steps;
     const float unit = last ? 1.0f / kScaleX : 1.0f;
     const Product px{kM, x + 1, x + 1, y, y + 1, 0, unit / kScaleM, unit * s.a};
-    e = last ? launch_product<OUT, T>(gs, px, ws, out, mv, stream)
-             : launch_product<kPlanes, T>(gs, px, ws, nullptr, mv, stream);
+    e = last ? launch_product<2, OUT, T>(gs, px, ws, out, mv, stream)
+             : launch_product<2, kPlanes, T>(gs, px, ws, nullptr, mv, stream);
   }
   return e;
 }
@@ -391,7 +525,7 @@ hipError_t run(Groups& gs, const OrthoSteps& s, const S* update, T* out, Move mv
 
 uint64_t ortho_tiles(uint64_t rows, uint64_t cols) {
   const uint64_t m = std::min(rows, cols), n = std::max(rows, cols);
-  if (m > (1u << 16) || n > (1u << 24) || m * n > (1ull << 32)) return 0;
+  if (m > (1u << 16) || n > (1u << 21) || m * n > (1ull << 32)) return 0;
   return (m + 63) / 64 * ((n + 63) / 64);
 }
 

@@ -77,9 +77,9 @@ def test_orthogonalize_refuses():
     need = L.sparcml_orthogonalize_workspace(96, *_ms(good))
     assert need > 0
     for ms, N in ((good, 95), ([(0, 4, 8), (31, 8, 8)], 96), ([(32, 8, 8), (0, 4, 8)], 96),
-                  ([(0, 65537, 65537)], (1 << 40) - 1), ([(0, 1, (1 << 24) + 1)], 1 << 30), ([(97, 0, 0)], 96),
+                  ([(0, 65537, 65537)], (1 << 40) - 1), ([(0, 1, (1 << 21) + 1)], 1 << 30), ([(97, 0, 0)], 96),
                   ([(0, 1 << 16, (1 << 16) + 1)], 1 << 39), ([(0, 1, 1)], 1 << 40),
-                  ([(k << 24, 1, 1 << 24) for k in range(64)], 1 << 30)):
+                  ([(k << 21, 1, 1 << 21) for k in range(512)], 1 << 30)):
         assert L.sparcml_orthogonalize_workspace(N, *_ms(ms)) == 0, ms[:3]
         assert L.sparcml_orthogonalize(N, *_ms(ms), 5, 1, 1, 1, 0, 0, A, 0, A, A, 1 << 40, None) == BAD
     assert L.sparcml_orthogonalize_workspace(96, 2, None, None, None) == 0
