@@ -31,6 +31,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr uint32_t kPad = 64;        // sides are padded with zeros to this
 constexpr uint32_t kGroups = 24;     // groups of equal matrices in one set of launches
+constexpr uint32_t kMaxSteps = 64;
 constexpr uint32_t kParts = 256;     // partial sums of squares of one matrix, at most
 constexpr float kScaleX = 4096.0f;   // of X, X^T, A
 constexpr float kScaleM = 256.0f;    // of M
@@ -57,9 +58,10 @@ struct Groups {
   uint32_t count;
 };
 
-// A matrix's buffers: partial sums, then X, X^T, the next X and X^T, A and M.
+// A matrix's buffers: partial sums, then X, X^T, the next X and X^T, and the
+// square ones: A, the step's M, Q A, and the product of the steps' Q (two).
 // A row of `ld` values is stored as their hi parts, then their lo parts.
-enum Buffer : uint32_t { kX0, kXT0, kX1, kXT1, kA, kM, kBuffers };
+enum Buffer : uint32_t { kX0, kXT0, kX1, kXT1, kA, kM, kT, kP, kP2, kBuffers };
 
 struct Plane {
   f16* p;
@@ -155,14 +157,14 @@ __global__ __launch_bounds__(kThreads) void k_split(Groups gs, const T* update, 
   }
 }
 
-// One product of every matrix: D = alpha * A B^T + beta * C in stored units.
+// One product of every matrix: D = alpha * A B^T + beta * C + gamma * C2 in stored units.
 // i runs over A's rows (m of them), j over B's.
 struct Product {
   uint32_t a, b;        // operands, rows along the summed index
-  uint32_t c_ji;        // C, stored [j][i]
+  uint32_t c_ji, c2;    // C, stored [j][i]; C2, symmetric
   uint32_t d_ij, d_ji;  // D in both orders (planes only)
   uint32_t sym;         // D symmetric: a == b's rows, tiles j <= i
-  float alpha, beta;
+  float alpha, beta, gamma;
 };
 enum Out { kPlanes, kResult, kWeight };
 
@@ -307,7 +309,7 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
   // half l % 2, of the block's 32 rows of 32, and so moves 32 bytes at a time.
   __syncthreads();
   uint32_t* turn = reinterpret_cast<uint32_t*>(lds0) + wid * 32 * 33;
-  const Plane c = plane(base, m, n, p.c_ji), dij = plane(base, m, n, p.d_ij), dji = plane(base, m, n, p.d_ji);
+  const Plane c = plane(base, m, n, p.c_ji), c2 = plane(base, m, n, p.c2), dij = plane(base, m, n, p.d_ij), dji = plane(base, m, n, p.d_ji);
   const float move = mv.move * sqrtf(fmaxf(1.0f, (float)g.rows / (float)g.cols));
   T* o = out + g.at + it.k * (uint64_t)g.rows * g.cols;
   const uint32_t row = lane / 2, half = lane % 2 * 16;
@@ -335,6 +337,15 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
       for (int e = 0; e < 16; ++e)
         v[e] = fmaf(p.alpha, __uint_as_float(turn[row * 33 + half + e]),
                     p.beta * ((float)ch[e / 8][e % 8] + (float)cl[e / 8][e % 8]));
+      if (p.gamma != 0.0f) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          ch[q] = reinterpret_cast<const f16x8*>(c2.hi(j) + i)[q];
+          cl[q] = reinterpret_cast<const f16x8*>(c2.lo(j) + i)[q];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[q * 8 + e] = fmaf(p.gamma, (float)ch[q][e] + (float)cl[q][e], v[q * 8 + e]);
+        }
+      }
       if constexpr (OUT == kPlanes) {
         f16x8 dh[2], dl[2];
 #pragma unroll
@@ -415,16 +426,19 @@ __global__ __launch_bounds__(kThreads) void k_normalised(Groups gs, const S* upd
   }
 }
 
-// Cuts the matrices into groups of equal ones that follow each other, and
-// lays their buffers out in the workspace. Calls f(groups) for every kGroups
-// of them; returns the bytes used.
+// The two kinds of matrices, by the shorter side: see plan_of.
+enum Kind { kNarrow, kWide, kKinds };
+Kind kind_of(uint32_t rows, uint32_t cols) { return std::min(rows, cols) <= 128 ? kNarrow : kWide; }
+
+// Cuts the matrices of one kind into groups of equal ones that follow each
+// other, and lays their buffers out in the workspace from `used` on. Calls
+// f(groups) for every kGroups of them; returns the workspace's new end.
 template <class F>
-uint64_t for_groups(const OrthoMatrices& ms, F&& f) {
+uint64_t for_groups(const OrthoMatrices& ms, Kind kind, uint64_t used, F&& f) {
   Groups gs = {};
-  uint64_t used = 0;
   for (uint32_t k = 0; k < ms.count; ++k) {
     const uint32_t rows = ms.rows[k], cols = ms.cols[k];
-    if (rows == 0 || cols == 0) continue;
+    if (rows == 0 || cols == 0 || kind_of(rows, cols) != kind) continue;
     Group* last = gs.count ? &gs.g[gs.count - 1] : nullptr;
     if (last && last->rows == rows && last->cols == cols &&
         last->at + (uint64_t)last->count * rows * cols == ms.offsets[k]) {
@@ -488,9 +502,77 @@ hipError_t launch_product(Groups& gs, const Product& p, unsigned char* ws, T* ou
   return hipGetLastError();
 }
 
+// `steps` steps taken as one: with A = X X^T, Q = a I + M, M = b A + c A A,
+// the next step's A is Q A Q = Q (Q A) (they commute, so both products are
+// symmetric) and X moves once, by the product P of the Q. Beyond one step that
+// trades two of X's products (3 m m n) for three halves more of m x m ones.
+// gram, inner, move: parts (1 or 2) of the operands of X X^T, of the m x m
+// products and of P X.
+struct Block {
+  uint32_t steps, gram, inner, move;
+};
+struct Plan {
+  Block b[kMaxSteps];
+  uint32_t count = 0;
+  void add(uint32_t times, Block x) {
+    for (; times > 0; --times) b[count++] = x;
+  }
+};
+
+// What the result's type asks for. fp32: two parts everywhere. 16 bits: the
+// error of a product of single fp16 values (2^-12 of it) in an early step is
+// worn off, because the later steps move every singular value towards the same
+// one: over matrices of 128 to 1024 the last two steps alone account for nearly
+// all of it. So fp16 results take two parts in the last two steps (three where
+// they are taken as one) and bf16 results in the last one but for its A: the
+// result is off by 1e-5 .. 2e-4 and 2e-4 .. 9e-4 of its norm, against 2.1e-4
+// and 1.7e-3 by the rounding to the type itself; narrower matrices (up to 128),
+// where it would be more and costs little, take two parts always.
+// Two steps taken as one, or three at the end, keep fp32's accuracy (5e-7 ..
+// 1.2e-6 of the norm; step by step 4e-7 .. 5e-7; fp32 products 1e-6 .. 2e-6);
+// more do not, as A's small entries would be lost beside its large ones.
+// `paired`: steps taken together.
+Plan plan_of(uint32_t steps, uint32_t type, Kind kind, bool paired) {
+  const Block one{1, 1, 1, 1}, two{2, 1, 1, 1}, exact{1, 2, 2, 2};
+  Plan p;
+  if (kind == kNarrow || type == SPARCML_F32) {
+    const uint32_t last = !paired ? 0 : steps % 2 ? std::min(steps, 3u) : 0;
+    if (!paired) p.add(steps, exact);
+    else p.add((steps - last) / 2, Block{2, 2, 2, 2});
+    if (last) p.add(1, Block{last, 2, 2, 2});
+    return p;
+  }
+  const bool bf16 = type == SPARCML_BF16;
+  const uint32_t tail = std::min(steps, bf16 ? 1u : paired ? 3u : 2u), head = steps - tail;
+  p.add(paired ? head % 2 : head, one);
+  if (paired) p.add(head / 2, two);
+  if (bf16) p.add(tail, Block{1, 1, 2, 2});
+  else if (paired) p.add(1, Block{tail, 2, 2, 2});
+  else p.add(tail, exact);
+  return p;
+}
+
+// Operations of a plan, and what its launches cost in operations: about 5 us
+// each at 5e14 a second.
+double plan_cost(const Plan& p, const Groups& gs) {
+  const auto times = [](uint32_t parts) { return parts == 2 ? 3.0 : 1.0; };
+  double all = 0.0;
+  for (uint32_t k = 0; k < p.count; ++k) {
+    const Block& b = p.b[k];
+    for (uint32_t j = 0; j < gs.count; ++j) {
+      const double m = gs.g[j].m(), n = gs.g[j].n();
+      all += gs.g[j].count * m * m * (n * (times(b.gram) + 2 * times(b.move)) + m * times(b.inner) * (4 * b.steps - 3));
+    }
+    all += 2.5e9 * (2 + 4 * b.steps - 3);
+  }
+  return all;
+}
+
 template <int OUT, class S, class T>
-hipError_t run(Groups& gs, const OrthoSteps& s, const S* update, T* out, Move mv, unsigned char* ws,
-               hipStream_t stream) {
+hipError_t run(Groups& gs, Kind kind, const OrthoSteps& s, uint32_t type, const S* update, T* out, Move mv,
+               unsigned char* ws, hipStream_t stream) {
+  // the longest sums first, so that they do not start when the others end
+  std::sort(gs.g, gs.g + gs.count, [](const Group& x, const Group& y) { return x.n() > y.n(); });
   uint32_t blocks = tiled(gs, parts_of_host);
   hipLaunchKernelGGL(k_squares<S>, dim3(blocks), dim3(kThreads), 0, stream, gs, update, ws);
   hipError_t e = hipGetLastError();
@@ -503,20 +585,45 @@ hipError_t run(Groups& gs, const OrthoSteps& s, const S* update, T* out, Move mv
   blocks = tiled(gs, [](const Group& g) { return g.m() / 64 * (g.n() / 64); });
   hipLaunchKernelGGL(k_split<S>, dim3(blocks), dim3(kThreads), 0, stream, gs, update, s.eps, ws);
   e = hipGetLastError();
-  for (uint32_t k = 0; k < s.steps && e == hipSuccess; ++k) {
-    const uint32_t x = k % 2 ? kX1 : kX0, y = k % 2 ? kX0 : kX1;  // the step's X and the next
-    e = launch_product<2, kPlanes, T>(gs, Product{x, x, x, kA, kA, 1, 1.0f / kScaleX, 0.0f}, ws, nullptr, mv, stream);
-    if (e != hipSuccess) break;
-    e = launch_product<2, kPlanes, T>(gs,
-                                   Product{kA, kA, kA, kM, kM, 1, s.c * kScaleM / (kScaleX * kScaleX),
-                                           s.b * kScaleM / kScaleX},
-                                   ws, nullptr, mv, stream);
-    if (e != hipSuccess) break;
-    const bool last = k + 1 == s.steps;
+
+  const auto planes = [&](uint32_t parts, const Product& p) {
+    if (e != hipSuccess) return;
+    e = parts == 2 ? launch_product<2, kPlanes, float>(gs, p, ws, nullptr, mv, stream)
+                   : launch_product<1, kPlanes, float>(gs, p, ws, nullptr, mv, stream);
+  };
+  const auto result = [&](uint32_t parts, const Product& p) {
+    if (e != hipSuccess) return;
+    e = parts == 2 ? launch_product<2, OUT, T>(gs, p, ws, out, mv, stream)
+                   : launch_product<1, OUT, T>(gs, p, ws, out, mv, stream);
+  };
+  const Plan alone = plan_of(s.steps, type, kind, false), paired = plan_of(s.steps, type, kind, true);
+  const Plan& plan = plan_cost(paired, gs) < plan_cost(alone, gs) ? paired : alone;
+  const float to_m = kScaleM / kScaleX;
+  for (uint32_t k = 0; k < plan.count; ++k) {
+    const Block& blk = plan.b[k];
+    const uint32_t x = k % 2 ? kX1 : kX0, y = k % 2 ? kX0 : kX1;  // this block's X and the next
+    planes(blk.gram, Product{x, x, x, x, kA, kA, 1, 1.0f / kScaleX, 0.0f, 0.0f});
+    uint32_t mm = kP, pp = kP;  // the step's M; P - p0 I
+    float p0 = s.a;
+    for (uint32_t j = 0; j < blk.steps; ++j) {
+      if (j > 0) {  // the next step's A
+        planes(blk.inner, Product{mm, kA, kA, kA, kT, kT, 1, 1.0f / kScaleM, s.a, 0.0f});
+        planes(blk.inner, Product{mm, kT, kT, kT, kA, kA, 1, 1.0f / kScaleM, s.a, 0.0f});
+        mm = kM;
+      }
+      planes(blk.inner, Product{kA, kA, kA, kA, mm, mm, 1, s.c * to_m / kScaleX, s.b * to_m, 0.0f});
+      if (j > 0) {  // (a I + M) (p0 I + P)
+        const uint32_t next = pp == kP ? kP2 : kP;
+        planes(blk.inner, Product{mm, pp, pp, mm, next, next, 1, 1.0f / kScaleM, s.a, p0});
+        pp = next;
+        p0 *= s.a;
+      }
+    }
+    const bool last = k + 1 == plan.count;
     const float unit = last ? 1.0f / kScaleX : 1.0f;
-    const Product px{kM, x + 1, x + 1, y, y + 1, 0, unit / kScaleM, unit * s.a};
-    e = last ? launch_product<2, OUT, T>(gs, px, ws, out, mv, stream)
-             : launch_product<2, kPlanes, T>(gs, px, ws, nullptr, mv, stream);
+    const Product px{pp, x + 1, x + 1, x, y, y + 1, 0, unit / kScaleM, unit * p0, 0.0f};
+    if (last) result(blk.move, px);
+    else planes(blk.move, px);
   }
   return e;
 }
@@ -530,7 +637,9 @@ uint64_t ortho_tiles(uint64_t rows, uint64_t cols) {
 }
 
 size_t ortho_workspace_bytes(const OrthoMatrices& ms) {
-  return (size_t)for_groups(ms, [](Groups&) {}) + 256;
+  uint64_t used = 0;
+  for (int kind = 0; kind < kKinds; ++kind) used = for_groups(ms, (Kind)kind, used, [](Groups&) {});
+  return (size_t)used + 256;
 }
 
 hipError_t ortho_launch(const OrthoMatrices& ms, const OrthoSteps& steps, uint32_t update_type, const void* update,
@@ -538,18 +647,21 @@ hipError_t ortho_launch(const OrthoMatrices& ms, const OrthoSteps& steps, uint32
                         hipStream_t stream) {
   hipError_t e = hipSuccess;
   const Move mv{keep, move};
-  for_groups(ms, [&](Groups& gs) {
-    if (e != hipSuccess) return;
-    e = for_type(update_type, [&](auto s) {
-      return for_type(out_type, [&](auto t) {
-        using S = decltype(s);
-        using T = decltype(t);
-        unsigned char* w = static_cast<unsigned char*>(ws);
-        return is_weight ? run<kWeight, S, T>(gs, steps, (const S*)update, (T*)out, mv, w, stream)
-                         : run<kResult, S, T>(gs, steps, (const S*)update, (T*)out, mv, w, stream);
+  uint64_t used = 0;
+  for (int kind = 0; kind < kKinds; ++kind)
+    used = for_groups(ms, (Kind)kind, used, [&](Groups& gs) {
+      if (e != hipSuccess) return;
+      e = for_type(update_type, [&](auto s) {
+        return for_type(out_type, [&](auto t) {
+          using S = decltype(s);
+          using T = decltype(t);
+          unsigned char* w = static_cast<unsigned char*>(ws);
+          return is_weight
+                     ? run<kWeight, S, T>(gs, (Kind)kind, steps, out_type, (const S*)update, (T*)out, mv, w, stream)
+                     : run<kResult, S, T>(gs, (Kind)kind, steps, out_type, (const S*)update, (T*)out, mv, w, stream);
+        });
       });
     });
-  });
   return e;
 }
 
