@@ -218,6 +218,7 @@ template <int WI_, int WJ_, int TI_, int TJ_, int PARTS_>
 struct Shape {
   static constexpr int WI = WI_, WJ = WJ_, TI = TI_, TJ = TJ_, PARTS = PARTS_;
   static constexpr int W = WI * WJ, NT = W * kWave, I = WI * TI * 32, J = WJ * TJ * 32;
+  static_assert(W % 2 == 0, "a lane's chunk is the same in every pass");
   static constexpr int DEPTH = 64 / PARTS;  // summed index of a pass: rows of 128 bytes in LDS
 };
 
@@ -225,8 +226,8 @@ struct Shape {
 // bytes (64 of hi, or 32 of hi and 32 of lo): while the waves multiply from
 // one, the next pass's rows go from memory straight into the other, so a pass
 // waits once. A row's eight 16-byte chunks are stored in an order that differs
-// by row (chunk c at c ^ (row % 8)): eight lanes that read the same chunk of
-// eight rows then read eight different bank groups.
+// by pairs of rows (chunk c at c ^ (row / 2 % 8)): sixteen lanes that read the
+// same chunk of sixteen rows then read all 64 banks once.
 template <class S, int OUT, class T>
 __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups gs, Product p, unsigned char* ws,
                                                                         T* out, Move mv) {
@@ -247,7 +248,7 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
   const uint32_t wi = wid / S::WJ * (S::TI * 32), wj = wid % S::WJ * (S::TJ * 32);
 
   // this lane's part of 8 rows of a pass: row lane / 8, stored chunk lane % 8
-  const uint32_t chunk = lane % 8 ^ lane / 8;
+  const uint32_t chunk = lane % 8 ^ (wid % 2 * 4 + lane / 16);
   const uint32_t from = S::PARTS == 2 ? chunk / 4 * K + chunk % 4 * 8 : chunk * 8;
   constexpr int LA = S::I / 8 / S::W, LB = S::J / 8 / S::W;
   const f16 *pa = a.hi(i0), *pb = b.hi(j0);
@@ -273,7 +274,7 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
       f16x8 fa[S::PARTS][S::TI], fb[S::PARTS][S::TJ];
 #pragma unroll
       for (int h = 0; h < S::PARTS; ++h) {
-        const uint32_t c = (ks * 2 + h * 4 + lane / 32) ^ lane % 8;  // h: only with DEPTH 32, chunks 4 .. 7
+        const uint32_t c = (ks * 2 + h * 4 + lane / 32) ^ lane / 2 % 8;  // h: only with DEPTH 32, chunks 4 .. 7
 #pragma unroll
         for (int q = 0; q < S::TI; ++q) fa[h][q] = lds[(wi + q * 32 + lane % 32) * 8 + c];
 #pragma unroll
