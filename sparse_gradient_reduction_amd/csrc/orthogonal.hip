@@ -21,6 +21,7 @@
 // with the usual coefficients and may reach 15 before hi overflows.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "kernels.hpp"
 #include "numeric.hpp"
@@ -222,6 +223,19 @@ struct Shape {
   static constexpr int DEPTH = 64 / PARTS;  // summed index of a pass: rows of 128 bytes in LDS
 };
 
+// Tells the scheduler to spread NV memory loads and ND LDS reads over NM
+// multiplications.
+template <int I, int NM, int NV, int ND>
+struct Spread {
+  static __device__ __forceinline__ void over() {
+    constexpr int v = (I + 1) * NV / NM - I * NV / NM, d = (I + 1) * ND / NM - I * ND / NM;
+    if constexpr (d > 0) __builtin_amdgcn_sched_group_barrier(0x100, d, 0);
+    if constexpr (v > 0) __builtin_amdgcn_sched_group_barrier(0x20, v, 0);
+    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+    if constexpr (I + 1 < NM) Spread<I + 1, NM, NV, ND>::over();
+  }
+};
+
 // A workgroup multiplies I x J tiles. Two LDS buffers of (I + J) rows of 128
 // bytes (64 of hi, or 32 of hi and 32 of lo): while the waves multiply from
 // one, the next pass's rows go from memory straight into the other, so a pass
@@ -258,53 +272,84 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
     const uint32_t r = (t < LA ? t : t - LA) * S::W * 8 + wid * 8 + lane / 8;
     src[t] = min(r, (t < LA ? m - i0 : J - j0) - 1) * 2 * K + from;
   }
-  const auto load = [&](f16x8* lds) {
+  constexpr int LN = LA + LB;
+  const auto load = [&](f16x8* lds, auto first, auto last) {  // loads [first, last) of a pass
 #pragma unroll
-    for (int t = 0; t < LA + LB; ++t) {
-      load_to_lds((t < LA ? pa : pb) + src[t], lds + (t * S::W + wid) * 64);
+    for (int t = first(); t < last(); ++t) load_to_lds((t < LA ? pa : pb) + src[t], lds + (t * S::W + wid) * 64);
+    if constexpr (last() == LN) {
+      pa += S::DEPTH;
+      pb += S::DEPTH;
     }
-    pa += S::DEPTH;
-    pb += S::DEPTH;
   };
 
   f32x16 acc[S::TI][S::TJ] = {};
-  const auto multiply = [&](const f16x8* lds) {
+  struct Parts {
+    f16x8 a[S::PARTS][S::TI], b[S::PARTS][S::TJ];
+  } f[2];
+  constexpr int KS = S::DEPTH / 16;  // even, so that a pass starts with f[0]
+  const auto read = [&](const f16x8* lds, int ks, Parts& to) {
 #pragma unroll
-    for (int ks = 0; ks < S::DEPTH / 16; ++ks) {
-      f16x8 fa[S::PARTS][S::TI], fb[S::PARTS][S::TJ];
+    for (int h = 0; h < S::PARTS; ++h) {
+      const uint32_t c = (ks * 2 + h * 4 + lane / 32) ^ lane / 2 % 8;  // h: only with DEPTH 32, chunks 4 .. 7
 #pragma unroll
-      for (int h = 0; h < S::PARTS; ++h) {
-        const uint32_t c = (ks * 2 + h * 4 + lane / 32) ^ lane / 2 % 8;  // h: only with DEPTH 32, chunks 4 .. 7
+      for (int q = 0; q < S::TI; ++q) to.a[h][q] = lds[(wi + q * 32 + lane % 32) * 8 + c];
 #pragma unroll
-        for (int q = 0; q < S::TI; ++q) fa[h][q] = lds[(wi + q * 32 + lane % 32) * 8 + c];
-#pragma unroll
-        for (int q = 0; q < S::TJ; ++q) fb[h][q] = lds[(S::I + wj + q * 32 + lane % 32) * 8 + c];
-      }
-#pragma unroll
-      for (int x = 0; x < S::TI; ++x)
-#pragma unroll
-        for (int y = 0; y < S::TJ; ++y) {
-          acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[0][x], fb[0][y], acc[x][y], 0, 0, 0);
-          if constexpr (S::PARTS == 2) {
-            acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[0][x], fb[1][y], acc[x][y], 0, 0, 0);
-            acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[1][x], fb[0][y], acc[x][y], 0, 0, 0);
-          }
-        }
-      __builtin_amdgcn_sched_barrier(0);  // one part's operands at a time: the accumulators leave no room for more
+      for (int q = 0; q < S::TJ; ++q) to.b[h][q] = lds[(S::I + wj + q * 32 + lane % 32) * 8 + c];
     }
   };
+  const auto multiply = [&](const Parts& by) {
+#pragma unroll
+    for (int x = 0; x < S::TI; ++x)
+#pragma unroll
+      for (int y = 0; y < S::TJ; ++y) {
+        acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(by.a[0][x], by.b[0][y], acc[x][y], 0, 0, 0);
+        if constexpr (S::PARTS == 2) {
+          acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(by.a[0][x], by.b[1][y], acc[x][y], 0, 0, 0);
+          acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(by.a[1][x], by.b[0][y], acc[x][y], 0, 0, 0);
+        }
+      }
+  };
 
+  // The operands of a part of a pass are read while the part before it is
+  // multiplied. So at a pass's barrier all of its operands are in registers:
+  // its buffer is free for the pass after the next one, and the last part is
+  // multiplied behind the barrier, while the next pass's first operands arrive.
+  // The loads from memory are spread between the multiplications that follow:
+  // issued at once, 64 of them hold the waves up for a thousand cycles. Passes
+  // past the last load what follows in the workspace, and nothing reads it.
+  constexpr int NM = S::TI * S::TJ * (S::PARTS == 2 ? 3 : 1), ND = S::PARTS * (S::TI + S::TJ);
+  constexpr int LH = S::PARTS == 2 ? LN : LN / 2;  // loads behind the barrier; the others with the next part
+  constexpr std::integral_constant<int, 0> l0;
+  constexpr std::integral_constant<int, LH> l1;
+  constexpr std::integral_constant<int, LN> l2;
   const uint32_t passes = K / S::DEPTH;
-  load(lds0);
-  for (uint32_t k = 0; k < passes; k += 2) {
-    __syncthreads();  // buffer 0 is filled, buffer 1 no longer read
-    if (k + 1 < passes) load(lds1);
-    multiply(lds0);
-    if (k + 1 == passes) break;
+  const auto pass = [&](f16x8* now, f16x8* next) {
+#pragma unroll
+    for (int ks = 0; ks + 1 < KS; ++ks) {
+      read(now, ks + 1, f[(ks + 1) % 2]);
+      if (ks == 0 && LH < LN) load(next, l1, l2);
+      multiply(f[ks % 2]);
+      if (ks == 0) Spread<0, NM, LN - LH, ND>::over();
+      else Spread<0, NM, 0, ND>::over();
+      __builtin_amdgcn_sched_barrier(0);
+    }
     __syncthreads();
-    if (k + 2 < passes) load(lds0);
-    multiply(lds1);
+    load(now, l0, l1);
+    read(next, 0, f[0]);
+    multiply(f[1]);
+    Spread<0, NM, LH, ND>::over();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  load(lds0, l0, l2);
+  __syncthreads();
+  load(lds1, l0, l1);
+  read(lds0, 0, f[0]);
+  uint32_t k = 0;
+  for (; k + 2 <= passes; k += 2) {
+    pass(lds0, lds1);
+    pass(lds1, lds0);
   }
+  if (k < passes) pass(lds0, lds1);
 
   // A wave turns its blocks of 32 x 32 through LDS: lane l finishes row l / 2,
   // half l % 2, of the block's 32 rows of 32, and so moves 32 bytes at a time.
@@ -640,7 +685,7 @@ uint64_t ortho_tiles(uint64_t rows, uint64_t cols) {
 size_t ortho_workspace_bytes(const OrthoMatrices& ms) {
   uint64_t used = 0;
   for (int kind = 0; kind < kKinds; ++kind) used = for_groups(ms, (Kind)kind, used, [](Groups&) {});
-  return (size_t)used + 256;
+  return (size_t)used + 1024;  // passes past the last load up to 256 bytes past a buffer
 }
 
 hipError_t ortho_launch(const OrthoMatrices& ms, const OrthoSteps& steps, uint32_t update_type, const void* update,
