@@ -40,6 +40,7 @@ constexpr float kScaleM = 256.0f;    // of M
 typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 typedef f16 f16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 __host__ __device__ __forceinline__ uint32_t up(uint32_t v, uint32_t to) { return (v + to - 1) / to * to; }
 
@@ -165,6 +166,7 @@ struct Product {
   uint32_t c_ji, c2;    // C, stored [j][i]; C2, symmetric
   uint32_t d_ij, d_ji;  // D in both orders (planes only)
   uint32_t sym;         // D symmetric: a == b's rows, tiles j <= i
+  uint32_t lo_ij;       // the lo parts are wanted in the order [i][j] too
   float alpha, beta, gamma;
 };
 enum Out { kPlanes, kResult, kWeight };
@@ -200,7 +202,7 @@ __device__ __forceinline__ void tile_at(uint32_t slot, uint32_t j, bool sym, uin
 }
 
 // 16 bytes a lane from memory straight into LDS, at `to` + 16 * lane.
-__device__ __forceinline__ void load_to_lds(const f16* from, f16x8* to) {
+__device__ __forceinline__ void load_to_lds(const char* from, f16x8* to) {
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
                                    (__attribute__((address_space(3))) void*)to, 16, 0, 0);
 }
@@ -265,20 +267,21 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
   const uint32_t chunk = lane % 8 ^ (wid % 2 * 4 + lane / 16);
   const uint32_t from = S::PARTS == 2 ? chunk / 4 * K + chunk % 4 * 8 : chunk * 8;
   constexpr int LA = S::I / 8 / S::W, LB = S::J / 8 / S::W;
-  const f16 *pa = a.hi(i0), *pb = b.hi(j0);
-  uint32_t src[LA + LB];  // elements from there; at most 256 rows of 2 * 2^21
+  const char *pa = (const char*)a.hi(i0), *pb = (const char*)b.hi(j0);
+  uint32_t src[LA + LB];  // bytes from there; at most 256 rows of 2 * 2^21 fp16
 #pragma unroll
   for (int t = 0; t < LA + LB; ++t) {
     const uint32_t r = (t < LA ? t : t - LA) * S::W * 8 + wid * 8 + lane / 8;
-    src[t] = min(r, (t < LA ? m - i0 : J - j0) - 1) * 2 * K + from;
+    src[t] = (min(r, (t < LA ? m - i0 : J - j0) - 1) * 2 * K + from) * sizeof(f16);
   }
   constexpr int LN = LA + LB;
   const auto load = [&](f16x8* lds, auto first, auto last) {  // loads [first, last) of a pass
 #pragma unroll
     for (int t = first(); t < last(); ++t) load_to_lds((t < LA ? pa : pb) + src[t], lds + (t * S::W + wid) * 64);
     if constexpr (last() == LN) {
-      pa += S::DEPTH;
-      pb += S::DEPTH;
+      pa += S::DEPTH * sizeof(f16);
+      pb += S::DEPTH * sizeof(f16);
+      asm("" : "+s"(pa), "+s"(pb));  // stays a scalar base and 32-bit offsets
     }
   };
 
@@ -351,105 +354,149 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
   }
   if (k < passes) pass(lds0, lds1);
 
-  // A wave turns its blocks of 32 x 32 through LDS: lane l finishes row l / 2,
-  // half l % 2, of the block's 32 rows of 32, and so moves 32 bytes at a time.
-  __syncthreads();
-  uint32_t* turn = reinterpret_cast<uint32_t*>(lds0) + wid * 32 * 33;
-  const Plane c = plane(base, m, n, p.c_ji), c2 = plane(base, m, n, p.c2), dij = plane(base, m, n, p.d_ij), dji = plane(base, m, n, p.d_ji);
-  const float move = mv.move * sqrtf(fmaxf(1.0f, (float)g.rows / (float)g.cols));
-  T* o = out + g.at + it.k * (uint64_t)g.rows * g.cols;
-  const uint32_t row = lane / 2, half = lane % 2 * 16;
+  // C is added before anything is stored: a load behind stores would wait for
+  // them, block after block.
+  const auto outside = [&](int x, int y) {  // blocks of 32 lie inside or outside
+    return i0 + wi + x * 32 >= m || j0 + wj + y * 32 >= J;
+  };
+  const auto add = [&](const Plane& c, float by) {
+#pragma unroll
+    for (int y = 0; y < S::TJ; ++y) {
+      f16x4 hi[S::TI][4] = {}, lo[S::TI][4] = {};
+      const uint32_t j = j0 + wj + y * 32 + lane % 32, i = i0 + wi + lane / 32 * 4;
+#pragma unroll
+      for (int x = 0; x < S::TI; ++x)
+        if (!outside(x, y)) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            hi[x][q] = *reinterpret_cast<const f16x4*>(c.hi(j) + i + x * 32 + q * 8);
+            lo[x][q] = *reinterpret_cast<const f16x4*>(c.lo(j) + i + x * 32 + q * 8);
+          }
+        }
+#pragma unroll
+      for (int x = 0; x < S::TI; ++x)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          acc[x][y][e] = fmaf(by, (float)hi[x][e / 4][e % 4] + (float)lo[x][e / 4][e % 4], acc[x][y][e]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
 #pragma unroll
   for (int x = 0; x < S::TI; ++x)
 #pragma unroll
-    for (int y = 0; y < S::TJ; ++y) {
-      const uint32_t ix = i0 + wi + x * 32, jx = j0 + wj + y * 32;
-      if (ix >= m || jx >= J) continue;  // blocks of 32 lie inside or outside
+    for (int y = 0; y < S::TJ; ++y)
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        turn[lane % 32 * 33 + e / 4 * 8 + lane / 32 * 4 + e % 4] = __float_as_uint(acc[x][y][e]);
-      wave_fence();
-      const uint32_t j = jx + row, i = ix + half;
-      float v[16];
-      f16x8 ch[2] = {}, cl[2] = {};
-      if (p.beta != 0.0f) {
+      for (int e = 0; e < 16; ++e) acc[x][y][e] *= p.alpha;
+  if (p.beta != 0.0f) add(plane(base, m, n, p.c_ji), p.beta);
+  if (p.gamma != 0.0f) add(plane(base, m, n, p.c2), p.gamma);
+
+  // A wave turns its blocks of 32 x 32 through LDS: lane l stores row l / 2,
+  // half l % 2, of the block's 32 rows of 32, 32 bytes at a time.
+  __syncthreads();
+  constexpr int PITCH = 36;
+  uint32_t* turn = reinterpret_cast<uint32_t*>(lds0) + wid * 32 * PITCH;
+  const uint32_t row = lane / 2, half = lane % 2 * 16;
+  u32x4* put = reinterpret_cast<u32x4*>(turn + lane % 32 * PITCH + lane / 32 * 4);
+  const u32x4* along = reinterpret_cast<const u32x4*>(turn + row * PITCH + half);
+  const uint32_t* across = turn + half * PITCH + row;
+  if constexpr (OUT == kPlanes) {
+    const Plane dij = plane(base, m, n, p.d_ij), dji = plane(base, m, n, p.d_ji);
+    const auto store = [&](const uint32_t (&w)[16], f16* hi, f16* lo) {
+      f16x8 h[2], l[2];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          ch[q] = reinterpret_cast<const f16x8*>(c.hi(j) + i)[q];
-          cl[q] = reinterpret_cast<const f16x8*>(c.lo(j) + i)[q];
-        }
+      for (int e = 0; e < 16; ++e) {
+        h[e / 8][e % 8] = __builtin_bit_cast(f16, (uint16_t)w[e]);
+        l[e / 8][e % 8] = __builtin_bit_cast(f16, (uint16_t)(w[e] >> 16));
       }
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        v[e] = fmaf(p.alpha, __uint_as_float(turn[row * 33 + half + e]),
-                    p.beta * ((float)ch[e / 8][e % 8] + (float)cl[e / 8][e % 8]));
-      if (p.gamma != 0.0f) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          ch[q] = reinterpret_cast<const f16x8*>(c2.hi(j) + i)[q];
-          cl[q] = reinterpret_cast<const f16x8*>(c2.lo(j) + i)[q];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[q * 8 + e] = fmaf(p.gamma, (float)ch[q][e] + (float)cl[q][e], v[q * 8 + e]);
-        }
+      for (int q = 0; q < 2; ++q) {
+        reinterpret_cast<f16x8*>(hi)[q] = h[q];
+        if (lo) reinterpret_cast<f16x8*>(lo)[q] = l[q];
       }
-      if constexpr (OUT == kPlanes) {
-        f16x8 dh[2], dl[2];
+    };
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const f16 h = (f16)v[e], l = (f16)(v[e] - (float)h);
-          dh[e / 8][e % 8] = h;
-          dl[e / 8][e % 8] = l;
-          turn[row * 33 + half + e] = (uint32_t)__builtin_bit_cast(uint16_t, h) |
-                                      (uint32_t)__builtin_bit_cast(uint16_t, l) << 16;
-        }
+    for (int x = 0; x < S::TI; ++x)
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          reinterpret_cast<f16x8*>(dji.hi(j) + i)[q] = dh[q];
-          reinterpret_cast<f16x8*>(dji.lo(j) + i)[q] = dl[q];
+      for (int y = 0; y < S::TJ; ++y) {
+        asm volatile("" : "+v"(acc[x][y]));  // not converted before its turn
+        if (outside(x, y)) continue;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          u32x4 w;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float v = acc[x][y][q * 4 + e];
+            const f16 h = (f16)v, l = (f16)(v - (float)h);
+            w[e] = (uint32_t)__builtin_bit_cast(uint16_t, h) | (uint32_t)__builtin_bit_cast(uint16_t, l) << 16;
+          }
+          put[q * 2] = w;
         }
+        wave_fence();
+        const uint32_t ix = i0 + wi + x * 32, jx = j0 + wj + y * 32;
+        uint32_t w[16];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[q * 4 + e] = along[q][e];
+        store(w, dji.hi(jx + row) + ix + half, dji.lo(jx + row) + ix + half);
         if (!(p.sym && ti == tj)) {
-          wave_fence();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const uint32_t w = turn[(half + e) * 33 + row];
-            dh[e / 8][e % 8] = __builtin_bit_cast(f16, (uint16_t)w);
-            dl[e / 8][e % 8] = __builtin_bit_cast(f16, (uint16_t)(w >> 16));
-          }
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            reinterpret_cast<f16x8*>(dij.hi(ix + row) + jx + half)[q] = dh[q];
-            reinterpret_cast<f16x8*>(dij.lo(ix + row) + jx + half)[q] = dl[q];
-          }
+          for (int e = 0; e < 16; ++e) w[e] = across[e * PITCH];
+          store(w, dij.hi(ix + row) + jx + half, p.lo_ij ? dij.lo(ix + row) + jx + half : nullptr);
         }
-      } else {
-        uint32_t r = j, col = i;  // tall: the result's rows are j
-        if (!g.tall()) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) turn[row * 33 + half + e] = __float_as_uint(v[e]);
-          wave_fence();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(turn[(half + e) * 33 + row]);
-          r = ix + row;
-          col = jx + half;
-        }
-        if (r < g.rows) {
-          constexpr int N = Pack<T>::N;
-#pragma unroll
-          for (int q = 0; q < 16 / N; ++q) {
-            const int64_t room = (int64_t)g.cols - col - q * N;
-            if (room <= 0) break;
-            T* at = o + (uint64_t)r * g.cols + col + q * N;
-            typename Pack<T>::V w = {};
-            if (OUT == kWeight) w = load_pack(at, room);
-#pragma unroll
-            for (int e = 0; e < N; ++e)
-              w[e] = from_f32<T>(OUT == kWeight ? fmaf(mv.keep, to_f32((T)w[e]), -move * v[q * N + e]) : v[q * N + e]);
-            store_pack(w, at, room);
-          }
-        }
+        wave_fence();  // before the next block's values
+        __builtin_amdgcn_sched_barrier(0);
       }
-      wave_fence();  // before the next block's values
+  } else {
+    constexpr int N = Pack<T>::N;
+    const float move = mv.move * sqrtf(fmaxf(1.0f, (float)g.rows / (float)g.cols));
+    T* o = out + g.at + it.k * (uint64_t)g.rows * g.cols;
+#pragma unroll
+    for (int x = 0; x < S::TI; ++x) {
+      typename Pack<T>::V w[S::TJ][16 / N];
+      T* at[S::TJ];
+      int64_t room[S::TJ];
+#pragma unroll
+      for (int y = 0; y < S::TJ; ++y) {  // the result's rows are j where it is tall, else i
+        const uint32_t ix = i0 + wi + x * 32, jx = j0 + wj + y * 32;
+        const uint32_t r = (g.tall() ? jx : ix) + row, col = (g.tall() ? ix : jx) + half;
+        at[y] = o + (uint64_t)r * g.cols + col;
+        room[y] = r < g.rows && !outside(x, y) ? (int64_t)g.cols - col : 0;
+#pragma unroll
+        for (int q = 0; q < 16 / N; ++q)
+          if (OUT == kWeight) w[y][q] = load_pack(at[y] + q * N, room[y] - q * N);
+      }
+#pragma unroll
+      for (int y = 0; y < S::TJ; ++y) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          u32x4 v;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = __float_as_uint(acc[x][y][q * 4 + e]);
+          put[q * 2] = v;
+        }
+        wave_fence();
+        float v[16];
+        if (g.tall()) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(along[e / 4][e % 4]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(across[e * PITCH]);
+        }
+#pragma unroll
+        for (int q = 0; q < 16 / N; ++q) {
+#pragma unroll
+          for (int e = 0; e < N; ++e)
+            w[y][q][e] = from_f32<T>(OUT == kWeight ? fmaf(mv.keep, to_f32((T)w[y][q][e]), -move * v[q * N + e])
+                                                    : v[q * N + e]);
+          store_pack(w[y][q], at[y] + q * N, room[y] - q * N);
+        }
+        wave_fence();
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
+  }
 }
 
 // No steps: the normalised update itself.
@@ -648,26 +695,27 @@ hipError_t run(Groups& gs, Kind kind, const OrthoSteps& s, uint32_t type, const 
   for (uint32_t k = 0; k < plan.count; ++k) {
     const Block& blk = plan.b[k];
     const uint32_t x = k % 2 ? kX1 : kX0, y = k % 2 ? kX0 : kX1;  // this block's X and the next
-    planes(blk.gram, Product{x, x, x, x, kA, kA, 1, 1.0f / kScaleX, 0.0f, 0.0f});
+    planes(blk.gram, Product{x, x, x, x, kA, kA, 1, 1, 1.0f / kScaleX, 0.0f, 0.0f});
     uint32_t mm = kP, pp = kP;  // the step's M; P - p0 I
     float p0 = s.a;
     for (uint32_t j = 0; j < blk.steps; ++j) {
       if (j > 0) {  // the next step's A
-        planes(blk.inner, Product{mm, kA, kA, kA, kT, kT, 1, 1.0f / kScaleM, s.a, 0.0f});
-        planes(blk.inner, Product{mm, kT, kT, kT, kA, kA, 1, 1.0f / kScaleM, s.a, 0.0f});
+        planes(blk.inner, Product{mm, kA, kA, kA, kT, kT, 1, 1, 1.0f / kScaleM, s.a, 0.0f});
+        planes(blk.inner, Product{mm, kT, kT, kT, kA, kA, 1, 1, 1.0f / kScaleM, s.a, 0.0f});
         mm = kM;
       }
-      planes(blk.inner, Product{kA, kA, kA, kA, mm, mm, 1, s.c * to_m / kScaleX, s.b * to_m, 0.0f});
+      planes(blk.inner, Product{kA, kA, kA, kA, mm, mm, 1, 1, s.c * to_m / kScaleX, s.b * to_m, 0.0f});
       if (j > 0) {  // (a I + M) (p0 I + P)
         const uint32_t next = pp == kP ? kP2 : kP;
-        planes(blk.inner, Product{mm, pp, pp, mm, next, next, 1, 1.0f / kScaleM, s.a, p0});
+        planes(blk.inner, Product{mm, pp, pp, mm, next, next, 1, 1, 1.0f / kScaleM, s.a, p0});
         pp = next;
         p0 *= s.a;
       }
     }
     const bool last = k + 1 == plan.count;
     const float unit = last ? 1.0f / kScaleX : 1.0f;
-    const Product px{pp, x + 1, x + 1, x, y, y + 1, 0, unit / kScaleM, unit * p0, 0.0f};
+    const bool lo = !last && plan.b[k + 1].gram == 2;  // X itself only goes into the next A
+    const Product px{pp, x + 1, x + 1, x, y, y + 1, 0, lo, unit / kScaleM, unit * p0, 0.0f};
     if (last) result(blk.move, px);
     else planes(blk.move, px);
   }
