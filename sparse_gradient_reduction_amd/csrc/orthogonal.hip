@@ -62,14 +62,21 @@ struct Groups {
 
 // A matrix's buffers: partial sums, then X, X^T, the next X and X^T, and the
 // square ones: A, the step's M, Q A, and the product of the steps' Q (two).
-// A row of `ld` values is stored as their hi parts, then their lo parts.
+// A row of `ld` values holds 2 * ld fp16. What single products read is stored
+// as the hi parts, then the lo parts; what products of both parts read is mixed,
+// 32 hi, 32 lo and so on: either way 128 bytes of a row are a pass's operands
+// (64 bytes at a time, memory gives a workgroup 59 GB/s instead of 100).
 enum Buffer : uint32_t { kX0, kXT0, kX1, kXT1, kA, kM, kT, kP, kP2, kBuffers };
 
 struct Plane {
   f16* p;
   uint32_t ld;
-  __device__ __forceinline__ f16* hi(uint64_t row) const { return p + row * 2 * ld; }
-  __device__ __forceinline__ f16* lo(uint64_t row) const { return p + row * 2 * ld + ld; }
+  __device__ __forceinline__ f16* row(uint64_t r) const { return p + r * 2 * ld; }
+  // element e's hi part, and from there to its lo part
+  __device__ __forceinline__ f16* hi(uint64_t r, uint32_t e, bool mixed) const {
+    return row(r) + e + (mixed ? e / 32 * 32 : 0);
+  }
+  __device__ __forceinline__ uint32_t to_lo(bool mixed) const { return mixed ? 32 : ld; }
 };
 __host__ __device__ __forceinline__ uint64_t buffers_bytes(uint32_t m, uint32_t n) {
   return kParts * sizeof(double) + 4ull * (4ull * m * n + (uint64_t)(kBuffers - kA) * m * m);
@@ -123,7 +130,8 @@ __global__ __launch_bounds__(kThreads) void k_squares(Groups gs, const T* update
 
 // X0 and its transpose, one 64 x 64 tile of the padded matrix.
 template <class T>
-__global__ __launch_bounds__(kThreads) void k_split(Groups gs, const T* update, float eps, unsigned char* ws) {
+__global__ __launch_bounds__(kThreads) void k_split(Groups gs, const T* update, float eps, bool mix_x, bool mix_xt,
+                                                    unsigned char* ws) {
   __shared__ float t[64][65];
   __shared__ double scratch[kThreads / kWave];
   const Item it = item_of(gs, blockIdx.x);
@@ -142,20 +150,23 @@ __global__ __launch_bounds__(kThreads) void k_split(Groups gs, const T* update, 
   // as stored: the wide X if rows <= cols, else X^T
   const Plane same = plane(base, g.m(), g.n(), g.tall() ? kXT0 : kX0);
   const Plane turned = plane(base, g.m(), g.n(), g.tall() ? kX0 : kXT0);
+  const bool mix_same = g.tall() ? mix_xt : mix_x, mix_turned = g.tall() ? mix_x : mix_xt;
   for (uint32_t y = ty; y < 64; y += 4) {
     const uint32_t r = r0 + y, c = c0 + tx;
     const float v = r < g.rows && c < g.cols ? (float)((double)to_f32(x[(uint64_t)r * g.cols + c]) * by) : 0.0f;
     t[y][tx] = v;
     const f16 hi = (f16)v;
-    same.hi(r)[c] = hi;
-    same.lo(r)[c] = (f16)(v - (float)hi);
+    f16* to = same.hi(r, c, mix_same);
+    to[0] = hi;
+    to[same.to_lo(mix_same)] = (f16)(v - (float)hi);
   }
   __syncthreads();
   for (uint32_t y = ty; y < 64; y += 4) {
     const float v = t[tx][y];
     const f16 hi = (f16)v;
-    turned.hi(c0 + y)[r0 + tx] = hi;
-    turned.lo(c0 + y)[r0 + tx] = (f16)(v - (float)hi);
+    f16* to = turned.hi(c0 + y, r0 + tx, mix_turned);
+    to[0] = hi;
+    to[turned.to_lo(mix_turned)] = (f16)(v - (float)hi);
   }
 }
 
@@ -167,6 +178,7 @@ struct Product {
   uint32_t d_ij, d_ji;  // D in both orders (planes only)
   uint32_t sym;         // D symmetric: a == b's rows, tiles j <= i
   uint32_t lo_ij;       // the lo parts are wanted in the order [i][j] too
+  uint32_t mix_c, mix_ij, mix_ji;  // C and C2, D in either order: mixed
   float alpha, beta, gamma;
 };
 enum Out { kPlanes, kResult, kWeight };
@@ -214,15 +226,26 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// Waits until at most N of this wave's memory operations are under way and its
+// LDS reads have arrived, then for the workgroup's other waves to be there too.
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | 7 << 4 | N / 16 << 14);  // vmcnt N, lgkmcnt 0
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // The shape of a workgroup's tile: WI x WJ waves, each TI x TJ blocks of
-// 32 x 32, and the parts of its operands: PARTS = 2 multiplies hi and lo
-// (three products), 1 hi alone.
-template <int WI_, int WJ_, int TI_, int TJ_, int PARTS_>
+// 32 x 32, the parts of its operands (2 multiplies hi and lo, three products,
+// 1 hi alone) and the LDS buffers.
+template <int WI_, int WJ_, int TI_, int TJ_, int PARTS_, int BUFFERS_>
 struct Shape {
-  static constexpr int WI = WI_, WJ = WJ_, TI = TI_, TJ = TJ_, PARTS = PARTS_;
+  static constexpr int WI = WI_, WJ = WJ_, TI = TI_, TJ = TJ_, PARTS = PARTS_, BUFFERS = BUFFERS_;
   static constexpr int W = WI * WJ, NT = W * kWave, I = WI * TI * 32, J = WJ * TJ * 32;
-  static_assert(W % 2 == 0, "a lane's chunk is the same in every pass");
-  static constexpr int DEPTH = 64 / PARTS;  // summed index of a pass: rows of 128 bytes in LDS
+  static constexpr int DEPTH = 64 / PARTS;  // summed index of a pass: rows of 128 bytes
+  static constexpr int SIZE = (I + J) * 8;
+  static_assert(W % 2 == 0, "a lane's chunk is the same in every load");
 };
 
 // Tells the scheduler to spread NV memory loads and ND LDS reads over NM
@@ -238,16 +261,15 @@ struct Spread {
   }
 };
 
-// A workgroup multiplies I x J tiles. Two LDS buffers of (I + J) rows of 128
-// bytes (64 of hi, or 32 of hi and 32 of lo): while the waves multiply from
-// one, the next pass's rows go from memory straight into the other, so a pass
-// waits once. A row's eight 16-byte chunks are stored in an order that differs
-// by pairs of rows (chunk c at c ^ (row / 2 % 8)): sixteen lanes that read the
-// same chunk of sixteen rows then read all 64 banks once.
+// A workgroup multiplies I x J tiles. LDS buffers of (I + J) rows of 128 bytes:
+// while the waves multiply from one, the rows of the next passes go from memory
+// straight into the others. A row's eight 16-byte chunks are stored in an order
+// that differs by pairs of rows (chunk c at c ^ (row / 2 % 8)): sixteen lanes
+// that read the same chunk of sixteen rows then read all 64 banks once.
 template <class S, int OUT, class T>
 __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups gs, Product p, unsigned char* ws,
                                                                         T* out, Move mv) {
-  __shared__ f16x8 lds0[(S::I + S::J) * 8], lds1[(S::I + S::J) * 8];
+  __shared__ f16x8 lds0[S::SIZE], lds1[S::SIZE], lds2[S::BUFFERS > 2 ? S::SIZE : 1], lds3[S::BUFFERS > 2 ? S::SIZE : 1];
   const Item it = item_of(gs, blockIdx.x);
   const Group& g = gs.g[it.g];
   if (it.k >= g.count) return;
@@ -263,24 +285,23 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
   const uint32_t lane = lane_id(), wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const uint32_t wi = wid / S::WJ * (S::TI * 32), wj = wid % S::WJ * (S::TJ * 32);
 
-  // this lane's part of 8 rows of a pass: row lane / 8, stored chunk lane % 8
-  const uint32_t chunk = lane % 8 ^ (wid % 2 * 4 + lane / 16);
-  const uint32_t from = S::PARTS == 2 ? chunk / 4 * K + chunk % 4 * 8 : chunk * 8;
-  constexpr int LA = S::I / 8 / S::W, LB = S::J / 8 / S::W;
-  const char *pa = (const char*)a.hi(i0), *pb = (const char*)b.hi(j0);
-  uint32_t src[LA + LB];  // bytes from there; at most 256 rows of 2 * 2^21 fp16
+  // this lane's part of the 8 rows that its wave loads at once: row lane / 8, stored chunk lane % 8
+  const uint32_t from = (lane % 8 ^ (wid % 2 * 4 + lane / 16)) * 8;
+  constexpr int LA = S::I / 8 / S::W, LN = LA + S::J / 8 / S::W;
+  const char *pa = (const char*)a.row(i0), *pb = (const char*)b.row(j0);
+  uint32_t src[LN];  // bytes from there; at most 256 rows of 2 * 2^21 fp16
 #pragma unroll
-  for (int t = 0; t < LA + LB; ++t) {
-    const uint32_t r = (t < LA ? t : t - LA) * S::W * 8 + wid * 8 + lane / 8;
+  for (int t = 0; t < LN; ++t) {
+    const uint32_t r = ((t < LA ? t : t - LA) * S::W + wid) * 8 + lane / 8;
     src[t] = (min(r, (t < LA ? m - i0 : J - j0) - 1) * 2 * K + from) * sizeof(f16);
   }
-  constexpr int LN = LA + LB;
   const auto load = [&](f16x8* lds, auto first, auto last) {  // loads [first, last) of a pass
 #pragma unroll
-    for (int t = first(); t < last(); ++t) load_to_lds((t < LA ? pa : pb) + src[t], lds + (t * S::W + wid) * 64);
+    for (int t = first(); t < last(); ++t)
+      load_to_lds((t < LA ? pa : pb) + src[t], lds + (t * S::W + wid) * kWave);
     if constexpr (last() == LN) {
-      pa += S::DEPTH * sizeof(f16);
-      pb += S::DEPTH * sizeof(f16);
+      pa += 128;
+      pb += 128;
       asm("" : "+s"(pa), "+s"(pb));  // stays a scalar base and 32-bit offsets
     }
   };
@@ -289,11 +310,11 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
   struct Parts {
     f16x8 a[S::PARTS][S::TI], b[S::PARTS][S::TJ];
   } f[2];
-  constexpr int KS = S::DEPTH / 16;  // even, so that a pass starts with f[0]
+  constexpr int KS = S::DEPTH / 16;  // parts of a pass; even, so that a pass starts with f[0]
   const auto read = [&](const f16x8* lds, int ks, Parts& to) {
 #pragma unroll
     for (int h = 0; h < S::PARTS; ++h) {
-      const uint32_t c = (ks * 2 + h * 4 + lane / 32) ^ lane / 2 % 8;  // h: only with DEPTH 32, chunks 4 .. 7
+      const uint32_t c = (ks * 2 + h * 4 + lane / 32) ^ lane / 2 % 8;
 #pragma unroll
       for (int q = 0; q < S::TI; ++q) to.a[h][q] = lds[(wi + q * 32 + lane % 32) * 8 + c];
 #pragma unroll
@@ -315,28 +336,29 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
 
   // The operands of a part of a pass are read while the part before it is
   // multiplied. So at a pass's barrier all of its operands are in registers:
-  // its buffer is free for the pass after the next one, and the last part is
+  // its buffer is free for the pass BUFFERS later, and the last part is
   // multiplied behind the barrier, while the next pass's first operands arrive.
-  // The loads from memory are spread between the multiplications that follow:
-  // issued at once, 64 of them hold the waves up for a thousand cycles. Passes
-  // past the last load what follows in the workspace, and nothing reads it.
+  // The barrier waits for the next pass's loads only. The loads are spread
+  // between the multiplications: issued at once, a pass's 64 hold the waves up
+  // for a thousand cycles. Passes past the last load what follows in the
+  // workspace, and nothing reads it.
   constexpr int NM = S::TI * S::TJ * (S::PARTS == 2 ? 3 : 1), ND = S::PARTS * (S::TI + S::TJ);
   constexpr int LH = S::PARTS == 2 ? LN : LN / 2;  // loads behind the barrier; the others with the next part
   constexpr std::integral_constant<int, 0> l0;
   constexpr std::integral_constant<int, LH> l1;
   constexpr std::integral_constant<int, LN> l2;
   const uint32_t passes = K / S::DEPTH;
-  const auto pass = [&](f16x8* now, f16x8* next) {
+  const auto pass = [&](f16x8* before, f16x8* now, const f16x8* next) {
 #pragma unroll
     for (int ks = 0; ks + 1 < KS; ++ks) {
       read(now, ks + 1, f[(ks + 1) % 2]);
-      if (ks == 0 && LH < LN) load(next, l1, l2);
+      if (ks == 0 && LH < LN) load(before, l1, l2);
       multiply(f[ks % 2]);
       if (ks == 0) Spread<0, NM, LN - LH, ND>::over();
       else Spread<0, NM, 0, ND>::over();
       __builtin_amdgcn_sched_barrier(0);
     }
-    __syncthreads();
+    wait_and_meet<(S::BUFFERS - 2) * LN>();
     load(now, l0, l1);
     read(next, 0, f[0]);
     multiply(f[1]);
@@ -344,15 +366,33 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
     __builtin_amdgcn_sched_barrier(0);
   };
   load(lds0, l0, l2);
-  __syncthreads();
-  load(lds1, l0, l1);
-  read(lds0, 0, f[0]);
-  uint32_t k = 0;
-  for (; k + 2 <= passes; k += 2) {
-    pass(lds0, lds1);
-    pass(lds1, lds0);
+  if constexpr (S::BUFFERS == 2) {
+    load(lds1, l0, l1);
+    wait_and_meet<LH>();
+    read(lds0, 0, f[0]);
+    uint32_t k = 0;
+    for (; k + 2 <= passes; k += 2) {
+      pass(lds1, lds0, lds1);
+      pass(lds0, lds1, lds0);
+    }
+    if (k < passes) pass(lds1, lds0, lds1);
+  } else {
+    load(lds1, l0, l2);
+    load(lds2, l0, l2);
+    load(lds3, l0, l1);
+    wait_and_meet<2 * LN + LH>();
+    read(lds0, 0, f[0]);
+    uint32_t k = 0;
+    for (; k + 4 <= passes; k += 4) {
+      pass(lds3, lds0, lds1);
+      pass(lds0, lds1, lds2);
+      pass(lds1, lds2, lds3);
+      pass(lds2, lds3, lds0);
+    }
+    if (k < passes) pass(lds3, lds0, lds1);
+    if (k + 1 < passes) pass(lds0, lds1, lds2);
+    if (k + 2 < passes) pass(lds1, lds2, lds3);
   }
-  if (k < passes) pass(lds0, lds1);
 
   // C is added before anything is stored: a load behind stores would wait for
   // them, block after block.
@@ -360,6 +400,7 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
     return i0 + wi + x * 32 >= m || j0 + wj + y * 32 >= J;
   };
   const auto add = [&](const Plane& c, float by) {
+    const uint32_t to_lo = c.to_lo(p.mix_c);
 #pragma unroll
     for (int y = 0; y < S::TJ; ++y) {
       f16x4 hi[S::TI][4] = {}, lo[S::TI][4] = {};
@@ -369,8 +410,9 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
         if (!outside(x, y)) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            hi[x][q] = *reinterpret_cast<const f16x4*>(c.hi(j) + i + x * 32 + q * 8);
-            lo[x][q] = *reinterpret_cast<const f16x4*>(c.lo(j) + i + x * 32 + q * 8);
+            const f16* at = c.hi(j, i + x * 32 + q * 8, p.mix_c);
+            hi[x][q] = *reinterpret_cast<const f16x4*>(at);
+            lo[x][q] = *reinterpret_cast<const f16x4*>(at + to_lo);
           }
         }
 #pragma unroll
@@ -401,7 +443,7 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
   const uint32_t* across = turn + half * PITCH + row;
   if constexpr (OUT == kPlanes) {
     const Plane dij = plane(base, m, n, p.d_ij), dji = plane(base, m, n, p.d_ji);
-    const auto store = [&](const uint32_t (&w)[16], f16* hi, f16* lo) {
+    const auto store = [&](const uint32_t (&w)[16], f16* hi, uint32_t to_lo) {  // 0: hi alone
       f16x8 h[2], l[2];
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
@@ -411,7 +453,7 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         reinterpret_cast<f16x8*>(hi)[q] = h[q];
-        if (lo) reinterpret_cast<f16x8*>(lo)[q] = l[q];
+        if (to_lo) reinterpret_cast<f16x8*>(hi + to_lo)[q] = l[q];
       }
     };
 #pragma unroll
@@ -438,11 +480,11 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
         for (int q = 0; q < 4; ++q)
 #pragma unroll
           for (int e = 0; e < 4; ++e) w[q * 4 + e] = along[q][e];
-        store(w, dji.hi(jx + row) + ix + half, dji.lo(jx + row) + ix + half);
+        store(w, dji.hi(jx + row, ix + half, p.mix_ji), dji.to_lo(p.mix_ji));
         if (!(p.sym && ti == tj)) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) w[e] = across[e * PITCH];
-          store(w, dij.hi(ix + row) + jx + half, p.lo_ij ? dij.lo(ix + row) + jx + half : nullptr);
+          store(w, dij.hi(ix + row, jx + half, p.mix_ij), p.lo_ij ? dij.to_lo(p.mix_ij) : 0);
         }
         wave_fence();  // before the next block's values
         __builtin_amdgcn_sched_barrier(0);
@@ -584,8 +626,8 @@ uint64_t product_tiles(const Groups& gs, const Product& p) {
 
 template <int PARTS, int OUT, class T>
 hipError_t launch_product(Groups& gs, const Product& p, unsigned char* ws, T* out, Move mv, hipStream_t stream) {
-  using Large = Shape<2, 4, 4, 2, PARTS>;  // 256 x 256, 8 waves
-  using Small = Shape<2, 2, 2, 2, PARTS>;  // 128 x 128, 4 waves
+  using Large = Shape<2, 4, 4, 2, PARTS, 2>;  // 256 x 256, 8 waves
+  using Small = Shape<2, 2, 2, 2, PARTS, 4>;  // 128 x 128, 4 waves
   if (product_tiles<Large>(gs, p) >= 256)
     hipLaunchKernelGGL((k_product<Large, OUT, T>), dim3(product_blocks<Large>(gs, p)), dim3(Large::NT), 0, stream, gs,
                        p, ws, out, mv);
@@ -600,7 +642,7 @@ hipError_t launch_product(Groups& gs, const Product& p, unsigned char* ws, T* ou
 // symmetric) and X moves once, by the product P of the Q. Beyond one step that
 // trades two of X's products (3 m m n) for three halves more of m x m ones.
 // gram, inner, move: parts (1 or 2) of the operands of X X^T, of the m x m
-// products and of P X.
+// products and of P X; inner == move, as P is read by both.
 struct Block {
   uint32_t steps, gram, inner, move;
 };
@@ -675,8 +717,11 @@ hipError_t run(Groups& gs, Kind kind, const OrthoSteps& s, uint32_t type, const 
                        mv);
     return hipGetLastError();
   }
+  const Plan alone = plan_of(s.steps, type, kind, false), paired = plan_of(s.steps, type, kind, true);
+  const Plan& plan = plan_cost(paired, gs) < plan_cost(alone, gs) ? paired : alone;
   blocks = tiled(gs, [](const Group& g) { return g.m() / 64 * (g.n() / 64); });
-  hipLaunchKernelGGL(k_split<S>, dim3(blocks), dim3(kThreads), 0, stream, gs, update, s.eps, ws);
+  hipLaunchKernelGGL(k_split<S>, dim3(blocks), dim3(kThreads), 0, stream, gs, update, s.eps, plan.b[0].gram == 2,
+                     plan.b[0].move == 2, ws);
   e = hipGetLastError();
 
   const auto planes = [&](uint32_t parts, const Product& p) {
@@ -689,33 +734,38 @@ hipError_t run(Groups& gs, Kind kind, const OrthoSteps& s, uint32_t type, const 
     e = parts == 2 ? launch_product<2, OUT, T>(gs, p, ws, out, mv, stream)
                    : launch_product<1, OUT, T>(gs, p, ws, out, mv, stream);
   };
-  const Plan alone = plan_of(s.steps, type, kind, false), paired = plan_of(s.steps, type, kind, true);
-  const Plan& plan = plan_cost(paired, gs) < plan_cost(alone, gs) ? paired : alone;
   const float to_m = kScaleM / kScaleX;
   for (uint32_t k = 0; k < plan.count; ++k) {
     const Block& blk = plan.b[k];
     const uint32_t x = k % 2 ? kX1 : kX0, y = k % 2 ? kX0 : kX1;  // this block's X and the next
-    planes(blk.gram, Product{x, x, x, x, kA, kA, 1, 1, 1.0f / kScaleX, 0.0f, 0.0f});
+    const uint32_t mix = blk.inner == 2;
+    // symmetric: D = alpha * A B + beta * B + gamma * C2, read by products of `inner` parts
+    const auto square = [&](uint32_t parts, uint32_t a, uint32_t b, uint32_t c2, uint32_t d, float alpha, float beta,
+                            float gamma) {
+      planes(parts, Product{a, b, b, c2, d, d, 1, 1, mix, mix, mix, alpha, beta, gamma});
+    };
+    square(blk.gram, x, x, x, kA, 1.0f / kScaleX, 0.0f, 0.0f);
     uint32_t mm = kP, pp = kP;  // the step's M; P - p0 I
     float p0 = s.a;
     for (uint32_t j = 0; j < blk.steps; ++j) {
       if (j > 0) {  // the next step's A
-        planes(blk.inner, Product{mm, kA, kA, kA, kT, kT, 1, 1, 1.0f / kScaleM, s.a, 0.0f});
-        planes(blk.inner, Product{mm, kT, kT, kT, kA, kA, 1, 1, 1.0f / kScaleM, s.a, 0.0f});
+        square(blk.inner, mm, kA, kA, kT, 1.0f / kScaleM, s.a, 0.0f);
+        square(blk.inner, mm, kT, kT, kA, 1.0f / kScaleM, s.a, 0.0f);
         mm = kM;
       }
-      planes(blk.inner, Product{kA, kA, kA, kA, mm, mm, 1, 1, s.c * to_m / kScaleX, s.b * to_m, 0.0f});
+      square(blk.inner, kA, kA, kA, mm, s.c * to_m / kScaleX, s.b * to_m, 0.0f);
       if (j > 0) {  // (a I + M) (p0 I + P)
         const uint32_t next = pp == kP ? kP2 : kP;
-        planes(blk.inner, Product{mm, pp, pp, mm, next, next, 1, 1, 1.0f / kScaleM, s.a, p0});
+        square(blk.inner, mm, pp, mm, next, 1.0f / kScaleM, s.a, p0);
         pp = next;
         p0 *= s.a;
       }
     }
     const bool last = k + 1 == plan.count;
     const float unit = last ? 1.0f / kScaleX : 1.0f;
-    const bool lo = !last && plan.b[k + 1].gram == 2;  // X itself only goes into the next A
-    const Product px{pp, x + 1, x + 1, x, y, y + 1, 0, lo, unit / kScaleM, unit * p0, 0.0f};
+    const uint32_t gram = last ? 1 : plan.b[k + 1].gram, move = last ? 1 : plan.b[k + 1].move;  // what reads X, X^T
+    const Product px{pp, x + 1, x + 1, x, y, y + 1, 0, gram == 2, blk.move == 2, gram == 2, move == 2,
+                     unit / kScaleM, unit * p0, 0.0f};
     if (last) result(blk.move, px);
     else planes(blk.move, px);
   }
