@@ -33,7 +33,7 @@ constexpr int kThreads = 256;
 constexpr uint32_t kPad = 64;        // sides are padded with zeros to this
 constexpr uint32_t kGroups = 24;     // groups of equal matrices in one set of launches
 constexpr uint32_t kMaxSteps = 64;
-constexpr uint32_t kParts = 256;     // partial sums of squares of one matrix, at most
+constexpr uint32_t kParts = 1024;    // partial sums of squares of one matrix, at most
 constexpr float kScaleX = 4096.0f;   // of X, X^T, A
 constexpr float kScaleM = 256.0f;    // of M
 
@@ -110,28 +110,57 @@ __device__ __forceinline__ uint32_t parts_of(uint64_t size) {
 }
 
 // Sums of squares, fp64, in parts of a fixed order.
+__device__ __forceinline__ double sum_of_parts(const double* part, uint32_t parts, double* scratch) {
+  double s = 0.0;
+  for (uint32_t i = threadIdx.x; i < parts; i += kThreads) s += part[i];
+  return block_sum_f64<kThreads>(s, scratch);
+}
+
 template <class T>
 __global__ __launch_bounds__(kThreads) void k_squares(Groups gs, const T* update, unsigned char* ws) {
   __shared__ double scratch[kThreads / kWave];
   const Item it = item_of(gs, blockIdx.x);
   const Group& g = gs.g[it.g];
   if (it.k >= g.count) return;
-  const uint64_t size = (uint64_t)g.rows * g.cols, each = (size + g.tiles - 1) / g.tiles;
+  const uint64_t size = (uint64_t)g.rows * g.cols, each = (size + 8ull * g.tiles - 1) / (8ull * g.tiles) * 8;
   const T* x = update + g.at + it.k * size;
   const uint64_t begin = it.tile * each, end = min(begin + each, size);
+  constexpr int V = Pack<T>::N;
   double s = 0.0;
-  for (uint64_t i = begin + threadIdx.x; i < end; i += kThreads) {
-    const double v = to_f32(x[i]);
-    s += v * v;
+#pragma unroll 4
+  for (uint64_t i = begin + threadIdx.x * V; i < end; i += kThreads * V) {
+    const typename Pack<T>::V v = load_pack(x + i, (int64_t)(end - i));
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const double w = to_f32((T)v[e]);
+      s = fma(w, w, s);
+    }
   }
   s = block_sum_f64<kThreads>(s, scratch);
   if (threadIdx.x == 0) reinterpret_cast<double*>(ws + g.ws + it.k * g.ws_of)[it.tile] = s;
 }
 
-// X0 and its transpose, one 64 x 64 tile of the padded matrix.
+// 16 values to a row's elements e .. e + 15 as hi and lo parts (to_lo 0: hi alone).
+__device__ __forceinline__ void store_parts(const float (&v)[16], f16* hi, uint32_t to_lo) {
+  f16x8 h[2], l[2];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    h[e / 8][e % 8] = (f16)v[e];
+    l[e / 8][e % 8] = (f16)(v[e] - (float)h[e / 8][e % 8]);
+  }
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    reinterpret_cast<f16x8*>(hi)[q] = h[q];
+    if (to_lo) reinterpret_cast<f16x8*>(hi + to_lo)[q] = l[q];
+  }
+}
+
+// X0 and its transpose, one 64 x 64 tile of the padded matrix; a thread takes
+// 16 elements of a row, then 16 of a row of the transpose. mix_x, mix_xt: how
+// they are stored; lo_x: whether X's lo parts are wanted (X^T's always are).
 template <class T>
 __global__ __launch_bounds__(kThreads) void k_split(Groups gs, const T* update, float eps, bool mix_x, bool mix_xt,
-                                                    unsigned char* ws) {
+                                                    bool lo_x, unsigned char* ws) {
   __shared__ float t[64][65];
   __shared__ double scratch[kThreads / kWave];
   const Item it = item_of(gs, blockIdx.x);
@@ -139,35 +168,35 @@ __global__ __launch_bounds__(kThreads) void k_split(Groups gs, const T* update, 
   if (it.k >= g.count) return;
   unsigned char* base = ws + g.ws + it.k * g.ws_of;
   const uint64_t size = (uint64_t)g.rows * g.cols;
-  const uint32_t parts = parts_of(size);
-  const double* part = reinterpret_cast<const double*>(base);
-  const double sum = block_sum_f64<kThreads>(threadIdx.x < parts ? part[threadIdx.x] : 0.0, scratch);
-  const double by = (double)kScaleX / (sqrt(sum) + (double)eps);
-  const uint32_t pc = up(g.cols, kPad);
-  const uint32_t r0 = it.tile / (pc / 64) * 64, c0 = it.tile % (pc / 64) * 64;
+  const uint32_t across = up(g.cols, kPad) / 64;
+  const uint32_t r0 = it.tile / across * 64, c0 = it.tile % across * 64;
   const T* x = update + g.at + it.k * size;
-  const uint32_t tx = threadIdx.x % 64, ty = threadIdx.x / 64;
+  const uint32_t row = threadIdx.x / 4, seg = threadIdx.x % 4 * 16;
+  const uint32_t r = r0 + row, c = c0 + seg;
+  constexpr int V = Pack<T>::N;
+  typename Pack<T>::V w[16 / V];
+#pragma unroll
+  for (int q = 0; q < 16 / V; ++q) {
+    const int64_t room = r < g.rows ? (int64_t)g.cols - c - q * V : 0;
+    w[q] = load_pack(x + (uint64_t)r * g.cols + c + q * V, room);
+  }
+  const double sum = sum_of_parts(reinterpret_cast<const double*>(base), parts_of(size), scratch);
+  const double by = (double)kScaleX / (sqrt(sum) + (double)eps);
+  float v[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    v[e] = r < g.rows && c + e < g.cols ? (float)((double)to_f32((T)w[e / V][e % V]) * by) : 0.0f;
+    t[row][seg + e] = v[e];
+  }
   // as stored: the wide X if rows <= cols, else X^T
-  const Plane same = plane(base, g.m(), g.n(), g.tall() ? kXT0 : kX0);
-  const Plane turned = plane(base, g.m(), g.n(), g.tall() ? kX0 : kXT0);
-  const bool mix_same = g.tall() ? mix_xt : mix_x, mix_turned = g.tall() ? mix_x : mix_xt;
-  for (uint32_t y = ty; y < 64; y += 4) {
-    const uint32_t r = r0 + y, c = c0 + tx;
-    const float v = r < g.rows && c < g.cols ? (float)((double)to_f32(x[(uint64_t)r * g.cols + c]) * by) : 0.0f;
-    t[y][tx] = v;
-    const f16 hi = (f16)v;
-    f16* to = same.hi(r, c, mix_same);
-    to[0] = hi;
-    to[same.to_lo(mix_same)] = (f16)(v - (float)hi);
-  }
+  const bool tall = g.tall();
+  const Plane same = plane(base, g.m(), g.n(), tall ? kXT0 : kX0), turned = plane(base, g.m(), g.n(), tall ? kX0 : kXT0);
+  const bool mix_same = tall ? mix_xt : mix_x, mix_turned = tall ? mix_x : mix_xt;
+  store_parts(v, same.hi(r, c, mix_same), tall || lo_x ? same.to_lo(mix_same) : 0);
   __syncthreads();
-  for (uint32_t y = ty; y < 64; y += 4) {
-    const float v = t[tx][y];
-    const f16 hi = (f16)v;
-    f16* to = turned.hi(c0 + y, r0 + tx, mix_turned);
-    to[0] = hi;
-    to[turned.to_lo(mix_turned)] = (f16)(v - (float)hi);
-  }
+#pragma unroll
+  for (int e = 0; e < 16; ++e) v[e] = t[seg + e][row];
+  store_parts(v, turned.hi(c0 + row, r0 + seg, mix_turned), !tall || lo_x ? turned.to_lo(mix_turned) : 0);
 }
 
 // One product of every matrix: D = alpha * A B^T + beta * C + gamma * C2 in stored units.
@@ -306,6 +335,39 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
     }
   };
 
+  // C and C2, 32 columns at a time. A tile of few registers loads them ahead of
+  // the products. They are added before anything is stored: a load behind
+  // stores would wait for them, block after block.
+  constexpr bool AHEAD = S::TI * S::TJ <= 4;
+  const auto outside = [&](int x, int y) {  // blocks of 32 lie inside or outside
+    return i0 + wi + x * 32 >= m || j0 + wj + y * 32 >= J;
+  };
+  struct Columns {
+    f16x4 hi[S::TI][4], lo[S::TI][4];
+  };
+  const auto load_c = [&](const Plane& c, int y, Columns& to) {
+    to = Columns{};
+    const uint32_t j = j0 + wj + y * 32 + lane % 32, i = i0 + wi + lane / 32 * 4, to_lo = c.to_lo(p.mix_c);
+#pragma unroll
+    for (int x = 0; x < S::TI; ++x)
+      if (!outside(x, y)) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f16* at = c.hi(j, i + x * 32 + q * 8, p.mix_c);
+          to.hi[x][q] = *reinterpret_cast<const f16x4*>(at);
+          to.lo[x][q] = *reinterpret_cast<const f16x4*>(at + to_lo);
+        }
+      }
+  };
+  Columns ahead[2][AHEAD ? S::TJ : 1];
+  if constexpr (AHEAD) {
+#pragma unroll
+    for (int y = 0; y < S::TJ; ++y) {
+      if (p.beta != 0.0f) load_c(plane(base, m, n, p.c_ji), y, ahead[0][y]);
+      if (p.gamma != 0.0f) load_c(plane(base, m, n, p.c2), y, ahead[1][y]);
+    }
+  }
+
   f32x16 acc[S::TI][S::TJ] = {};
   struct Parts {
     f16x8 a[S::PARTS][S::TI], b[S::PARTS][S::TJ];
@@ -394,43 +456,28 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
     if (k + 2 < passes) pass(lds1, lds2, lds3);
   }
 
-  // C is added before anything is stored: a load behind stores would wait for
-  // them, block after block.
-  const auto outside = [&](int x, int y) {  // blocks of 32 lie inside or outside
-    return i0 + wi + x * 32 >= m || j0 + wj + y * 32 >= J;
-  };
-  const auto add = [&](const Plane& c, float by) {
-    const uint32_t to_lo = c.to_lo(p.mix_c);
-#pragma unroll
-    for (int y = 0; y < S::TJ; ++y) {
-      f16x4 hi[S::TI][4] = {}, lo[S::TI][4] = {};
-      const uint32_t j = j0 + wj + y * 32 + lane % 32, i = i0 + wi + lane / 32 * 4;
-#pragma unroll
-      for (int x = 0; x < S::TI; ++x)
-        if (!outside(x, y)) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const f16* at = c.hi(j, i + x * 32 + q * 8, p.mix_c);
-            hi[x][q] = *reinterpret_cast<const f16x4*>(at);
-            lo[x][q] = *reinterpret_cast<const f16x4*>(at + to_lo);
-          }
-        }
-#pragma unroll
-      for (int x = 0; x < S::TI; ++x)
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          acc[x][y][e] = fmaf(by, (float)hi[x][e / 4][e % 4] + (float)lo[x][e / 4][e % 4], acc[x][y][e]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
 #pragma unroll
   for (int x = 0; x < S::TI; ++x)
 #pragma unroll
     for (int y = 0; y < S::TJ; ++y)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[x][y][e] *= p.alpha;
-  if (p.beta != 0.0f) add(plane(base, m, n, p.c_ji), p.beta);
-  if (p.gamma != 0.0f) add(plane(base, m, n, p.c2), p.gamma);
+  const auto add = [&](uint32_t buffer, int which, float by) {
+#pragma unroll
+    for (int y = 0; y < S::TJ; ++y) {
+      Columns c;
+      if constexpr (AHEAD) c = ahead[which][y];
+      else load_c(plane(base, m, n, buffer), y, c);
+#pragma unroll
+      for (int x = 0; x < S::TI; ++x)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          acc[x][y][e] = fmaf(by, (float)c.hi[x][e / 4][e % 4] + (float)c.lo[x][e / 4][e % 4], acc[x][y][e]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  if (p.beta != 0.0f) add(p.c_ji, 0, p.beta);
+  if (p.gamma != 0.0f) add(p.c2, 1, p.gamma);
 
   // A wave turns its blocks of 32 x 32 through LDS: lane l stores row l / 2,
   // half l % 2, of the block's 32 rows of 32, 32 bytes at a time.
@@ -551,7 +598,7 @@ __global__ __launch_bounds__(kThreads) void k_normalised(Groups gs, const S* upd
   if (it.k >= g.count) return;
   const uint64_t size = (uint64_t)g.rows * g.cols, each = (size + g.tiles - 1) / g.tiles;
   const double* part = reinterpret_cast<const double*>(ws + g.ws + it.k * g.ws_of);
-  const double sum = block_sum_f64<kThreads>(threadIdx.x < g.tiles ? part[threadIdx.x] : 0.0, scratch);
+  const double sum = sum_of_parts(part, g.tiles, scratch);
   const double by = 1.0 / (sqrt(sum) + (double)eps);
   const float move = mv.move * sqrtf(fmaxf(1.0f, (float)g.rows / (float)g.cols));
   const uint64_t begin = it.tile * each, end = min(begin + each, size), at = g.at + it.k * size;
@@ -721,7 +768,7 @@ hipError_t run(Groups& gs, Kind kind, const OrthoSteps& s, uint32_t type, const 
   const Plan& plan = plan_cost(paired, gs) < plan_cost(alone, gs) ? paired : alone;
   blocks = tiled(gs, [](const Group& g) { return g.m() / 64 * (g.n() / 64); });
   hipLaunchKernelGGL(k_split<S>, dim3(blocks), dim3(kThreads), 0, stream, gs, update, s.eps, plan.b[0].gram == 2,
-                     plan.b[0].move == 2, ws);
+                     plan.b[0].move == 2, plan.b[0].gram == 2, ws);
   e = hipGetLastError();
 
   const auto planes = [&](uint32_t parts, const Product& p) {
