@@ -217,29 +217,43 @@ struct Move {
   float keep, move;
 };
 
-// Tiles are taken in blocks of 4 x 4 (on and below the diagonal where the
-// result is symmetric), so that the neighbouring ones that share an XCD's L2
-// read few rows of A and B. A slot may lie outside the result.
-constexpr uint32_t kBlock = 4;
-__host__ __device__ __forceinline__ uint32_t tile_slots(uint32_t i, uint32_t j, bool sym) {
-  const uint32_t bi = (i + kBlock - 1) / kBlock, bj = (j + kBlock - 1) / kBlock;
-  return (sym ? bi * (bi + 1) / 2 : bi * bj) * kBlock * kBlock;
+// Tiles of a product, I x J of them, or those on and below the diagonal. They
+// are taken in bands of 4 rows, column by column, so that neighbouring ones,
+// which share an XCD's L2, read few rows of A and B. Every number is a tile: a
+// workgroup without one would take a CU's LDS from another's first turn (72
+// such among 288 made a product of six matrices of width 1024 take 34 us, not
+// 21).
+constexpr uint32_t kBand = 4;
+__host__ __device__ __forceinline__ uint32_t tiles_of(uint32_t I, uint32_t J, bool sym) {
+  return sym ? I * (I + 1) / 2 : I * J;
 }
-__device__ __forceinline__ void tile_at(uint32_t slot, uint32_t j, bool sym, uint32_t& ti, uint32_t& tj) {
-  const uint32_t b = slot / (kBlock * kBlock), in = slot % (kBlock * kBlock);
-  uint32_t bi, bj;
-  if (sym) {  // the b-th (bi, bj), bj <= bi
-    bi = (uint32_t)((sqrtf(8.0f * (float)b + 1.0f) - 1.0f) * 0.5f);
-    while ((uint64_t)bi * (bi + 1) / 2 > b) --bi;
-    while ((uint64_t)(bi + 1) * (bi + 2) / 2 <= b) ++bi;
-    bj = b - (uint32_t)((uint64_t)bi * (bi + 1) / 2);
+// (i, j), j <= i, of the t-th pair in the order (0, 0), (1, 0), (1, 1), (2, 0) ...
+__host__ __device__ __forceinline__ void pair_at(uint32_t t, uint32_t& i, uint32_t& j) {
+  i = (uint32_t)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
+  while ((uint64_t)i * (i + 1) / 2 > t) --i;
+  while ((uint64_t)(i + 1) * (i + 2) / 2 <= t) ++i;
+  j = t - (uint32_t)((uint64_t)i * (i + 1) / 2);
+}
+__host__ __device__ __forceinline__ void tile_at(uint32_t t, uint32_t I, uint32_t J, bool sym, uint32_t& ti,
+                                                 uint32_t& tj) {
+  uint32_t r0, u;
+  if (sym) {
+    pair_at(t, ti, tj);
+    r0 = ti / kBand * kBand;
+    u = t - r0 * (r0 + 1) / 2;
   } else {
-    const uint32_t across = (j + kBlock - 1) / kBlock;
-    bi = b / across;
-    bj = b % across;
+    r0 = t / (kBand * J) * kBand;
+    u = t - r0 * J;
   }
-  ti = bi * kBlock + in % kBlock;
-  tj = bj * kBlock + in / kBlock;
+  const uint32_t h = min(kBand, I - r0);  // rows of the band
+  if (!sym || u < r0 * h) {
+    ti = r0 + u % h;
+    tj = u / h;
+  } else {  // the band's own triangle
+    pair_at(u - r0 * h, ti, tj);
+    ti += r0;
+    tj += r0;
+  }
 }
 
 // 16 bytes a lane from memory straight into LDS, at `to` + 16 * lane.
@@ -305,9 +319,8 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
   const uint32_t m = g.m(), n = g.n();
   const uint32_t J = p.sym ? m : n;
   uint32_t ti, tj;
-  tile_at(it.tile, (J + S::J - 1) / S::J, p.sym, ti, tj);
+  tile_at(it.tile, (m + S::I - 1) / S::I, (J + S::J - 1) / S::J, p.sym, ti, tj);
   const uint32_t i0 = ti * S::I, j0 = tj * S::J;
-  if (i0 >= m || j0 >= J || (p.sym && tj > ti)) return;
   unsigned char* base = ws + g.ws + it.k * g.ws_of;
   const Plane a = plane(base, m, n, p.a), b = plane(base, m, n, p.b);
   const uint32_t K = a.ld;
@@ -656,32 +669,23 @@ uint32_t parts_of_host(const Group& g) {
 }
 
 template <class S>
-uint32_t product_blocks(Groups& gs, const Product& p) {
-  return tiled(gs, [&](const Group& g) {
-    return tile_slots((g.m() + S::I - 1) / S::I, ((p.sym ? g.m() : g.n()) + S::J - 1) / S::J, p.sym);
-  });
-}
-template <class S>
-uint64_t product_tiles(const Groups& gs, const Product& p) {
-  uint64_t all = 0;
-  for (uint32_t k = 0; k < gs.count; ++k) {
-    const uint64_t i = (gs.g[k].m() + S::I - 1) / S::I, j = ((p.sym ? gs.g[k].m() : gs.g[k].n()) + S::J - 1) / S::J;
-    all += gs.g[k].count * (p.sym ? i * (i + 1) / 2 : i * j);
-  }
-  return all;
+uint32_t product_tiles(const Group& g, const Product& p) {
+  return tiles_of((g.m() + S::I - 1) / S::I, ((p.sym ? g.m() : g.n()) + S::J - 1) / S::J, p.sym);
 }
 
 template <int PARTS, int OUT, class T>
 hipError_t launch_product(Groups& gs, const Product& p, unsigned char* ws, T* out, Move mv, hipStream_t stream) {
   using Large = Shape<2, 4, 4, 2, PARTS, 2>;  // 256 x 256, 8 waves
   using Small = Shape<2, 2, 2, 2, PARTS, 4>;  // 128 x 128, 4 waves
-  if (product_tiles<Large>(gs, p) >= 256)
-    hipLaunchKernelGGL((k_product<Large, OUT, T>), dim3(product_blocks<Large>(gs, p)), dim3(Large::NT), 0, stream, gs,
-                       p, ws, out, mv);
-  else
-    hipLaunchKernelGGL((k_product<Small, OUT, T>), dim3(product_blocks<Small>(gs, p)), dim3(Small::NT), 0, stream, gs,
-                       p, ws, out, mv);
-  return hipGetLastError();
+  uint64_t large = 0;
+  for (uint32_t k = 0; k < gs.count; ++k) large += (uint64_t)gs.g[k].count * product_tiles<Large>(gs.g[k], p);
+  const auto launch = [&](auto shape) {
+    using S = decltype(shape);
+    const uint32_t blocks = tiled(gs, [&](const Group& g) { return product_tiles<S>(g, p); });
+    hipLaunchKernelGGL((k_product<S, OUT, T>), dim3(blocks), dim3(S::NT), 0, stream, gs, p, ws, out, mv);
+    return hipGetLastError();
+  };
+  return large >= 256 ? launch(Large{}) : launch(Small{});
 }
 
 // `steps` steps taken as one: with A = X X^T, Q = a I + M, M = b A + c A A,
