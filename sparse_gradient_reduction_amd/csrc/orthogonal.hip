@@ -9,7 +9,9 @@
 //   A = X X^T (symmetric), M = c A A + b A (symmetric), X' = M X + a X,
 // so one kernel multiplies tiles whose operands both run along the summed
 // index. Symmetric results are computed for the tiles on and below the
-// diagonal and stored twice; X is kept in both orders (X and X^T), since the
+// diagonal and stored twice: exactly symmetric, because a rounding that makes
+// A B^T differ from A B grows from step to step (20 times in three steps taken
+// as one, below); X is kept in both orders (X and X^T), since the
 // first product sums along its rows and the third along its columns.
 //
 // Numbers: the matrix cores multiply fp16 and add in fp32. A value v is held
@@ -205,7 +207,7 @@ struct Product {
   uint32_t a, b;        // operands, rows along the summed index
   uint32_t c_ji, c2;    // C, stored [j][i]; C2, symmetric
   uint32_t d_ij, d_ji;  // D in both orders (planes only)
-  uint32_t sym;         // D symmetric: a == b's rows, tiles j <= i
+  uint32_t sym;         // D symmetric: what lies above the diagonal is the mirror of what lies below
   uint32_t lo_ij;       // the lo parts are wanted in the order [i][j] too
   uint32_t mix_c, mix_ij, mix_ji;  // C and C2, D in either order: mixed
   float alpha, beta, gamma;
@@ -535,13 +537,18 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
         }
         wave_fence();
         const uint32_t ix = i0 + wi + x * 32, jx = j0 + wj + y * 32;
+        if (p.sym && ix < jx) continue;  // the mirror of another block
         uint32_t w[16];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
           for (int e = 0; e < 4; ++e) w[q * 4 + e] = along[q][e];
+        if (p.sym && ix == jx) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[e] = half + e >= row ? w[e] : across[e * PITCH];
+        }
         store(w, dji.hi(jx + row, ix + half, p.mix_ji), dji.to_lo(p.mix_ji));
-        if (!(p.sym && ti == tj)) {
+        if (!(p.sym && ix == jx)) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) w[e] = across[e * PITCH];
           store(w, dij.hi(ix + row, jx + half, p.mix_ij), p.lo_ij ? dij.to_lo(p.mix_ij) : 0);
@@ -601,6 +608,235 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
   }
 }
 
+// ---- matrices of a shorter side of at most 64 ---------------------------------
+//
+// One workgroup takes a matrix through all of its steps, so the chain of some
+// twenty dependent products costs no launches. The square matrices stay in LDS
+// (64 x 64, hi and lo). X passes by in chunks of 64 columns: the first pass makes
+// X X^T; every further one moves a chunk by P, keeps it in the workspace, fp32,
+// for the next pass, and adds the moved chunk's products to the next X X^T while
+// it is in LDS. Each of the 8 waves holds two blocks of 16 x 16 of a product.
+// Bound by latency: 20 matrices of 16 x 16 .. 64 x 576 take as long as the
+// largest one.
+constexpr int kSmallThreads = 512;
+constexpr uint32_t kSmallSide = 64, kSmallLong = 2048;
+constexpr int kRow = 72;  // fp16 of a row in LDS: sixteen rows' 16-byte chunks fall into different banks
+
+typedef float f32x4v __attribute__((ext_vector_type(4)));
+
+// `count` blocks of `each` steps, the last one of `last`.
+struct SmallPlan {
+  uint32_t count, each, last;
+  __device__ __forceinline__ uint32_t steps(uint32_t k) const { return k + 1 < count ? each : last; }
+};
+__host__ __device__ __forceinline__ uint64_t small_bytes(uint32_t n) { return (uint64_t)up(n, 64) * 64 * sizeof(float); }
+
+template <int OUT, class S, class T>
+__global__ __launch_bounds__(kSmallThreads) void k_small(Groups gs, SmallPlan alone, SmallPlan paired, float a, float b,
+                                                         float c, float eps, const S* update, unsigned char* ws, T* out,
+                                                         Move mv) {
+  enum { A, M, Q, P0, P1, SQUARES };
+  __shared__ __align__(16) f16 sq[SQUARES][2][64 * kRow];
+  __shared__ __align__(16) f16 xt[2][64 * kRow], xi[2][64 * kRow];  // a chunk: [j][i] as it comes, [i][j] once moved
+  __shared__ double scratch[kSmallThreads / kWave];
+  const Item it = item_of(gs, blockIdx.x);
+  const Group& g = gs.g[it.g];
+  if (it.k >= g.count) return;
+  const bool tall = g.tall();
+  const uint32_t m = tall ? g.cols : g.rows, n = tall ? g.rows : g.cols, chunks = (n + 63) / 64;
+  const uint64_t size = (uint64_t)g.rows * g.cols;
+  const S* x = update + g.at + it.k * size;
+  T* o = out + g.at + it.k * size;
+  float* kept = reinterpret_cast<float*>(ws + g.ws + it.k * g.ws_of);  // X, [j][64]
+  const uint32_t lane = lane_id(), wid = threadIdx.x / kWave;
+  const uint32_t bi = wid / 2 * 16, bj = wid % 2 * 32;  // this wave's blocks: rows bi, columns bj and bj + 16
+
+  constexpr int V = Pack<S>::N;
+  double sum = 0.0;
+#pragma unroll 4
+  for (uint64_t i = threadIdx.x * V; i < size; i += kSmallThreads * V) {
+    const typename Pack<S>::V w = load_pack(x + i, (int64_t)(size - i));
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const double v = to_f32((S)w[e]);
+      sum = fma(v, v, sum);
+    }
+  }
+  const double by = (double)kScaleX / (sqrt(block_sum_f64<kSmallThreads>(sum, scratch)) + (double)eps);
+
+  const auto split = [](float v, f16& hi, f16& lo) {
+    hi = (f16)v;
+    lo = (f16)(v - (float)hi);
+  };
+  typedef f16 Part[64 * kRow];
+  // acc += rows bi of `l` times rows bj of `r`, both along the summed index
+  const auto multiply = [&](const Part (&l)[2], const Part (&r)[2], f32x4v (&acc)[2]) {
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      const uint32_t at = lane % 16 * kRow + ks * 32 + lane / 16 * 8;
+      const f16x8 lh = *reinterpret_cast<const f16x8*>(&l[0][bi * kRow + at]);
+      const f16x8 ll = *reinterpret_cast<const f16x8*>(&l[1][bi * kRow + at]);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const f16x8 rh = *reinterpret_cast<const f16x8*>(&r[0][(bj + q * 16) * kRow + at]);
+        const f16x8 rl = *reinterpret_cast<const f16x8*>(&r[1][(bj + q * 16) * kRow + at]);
+        acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lh, rh, acc[q], 0, 0, 0);
+        acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lh, rl, acc[q], 0, 0, 0);
+        acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ll, rh, acc[q], 0, 0, 0);
+      }
+    }
+  };
+  // acc[q][e] is at row i + e, column j of the product
+  const uint32_t i = bi + lane / 16 * 4;
+  const auto column = [&](int q) { return bj + q * 16 + lane % 16; };
+  // four values along i of a matrix stored [j][i]
+  const auto get = [&](const Part (&from)[2], int q) {
+    const f16x4 h = *reinterpret_cast<const f16x4*>(&from[0][column(q) * kRow + i]);
+    const f16x4 l = *reinterpret_cast<const f16x4*>(&from[1][column(q) * kRow + i]);
+    f32x4v v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = (float)h[e] + (float)l[e];
+    return v;
+  };
+  // A symmetric matrix from its values on and below the diagonal.
+  const auto put_symmetric = [&](Part (&to)[2], int q, f32x4v v) {
+    const uint32_t j = column(q);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (i + e < j) continue;
+      f16 hi, lo;
+      split(v[e], hi, lo);
+      to[0][j * kRow + i + e] = hi;
+      to[1][j * kRow + i + e] = lo;
+      to[0][(i + e) * kRow + j] = hi;
+      to[1][(i + e) * kRow + j] = lo;
+    }
+  };
+  // d = alpha l r + beta r + gamma c2, all symmetric
+  const auto square = [&](int l, int r, int c2, int d, float alpha, float beta, float gamma) {
+    f32x4v acc[2] = {};
+    multiply(sq[l], sq[r], acc);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      f32x4v v = acc[q] * alpha + get(sq[r], q) * beta;
+      if (gamma != 0.0f) v += get(sq[c2], q) * gamma;
+      put_symmetric(sq[d], q, v);
+    }
+    __syncthreads();
+  };
+
+  // Eight values of a chunk to a thread, as memory has them: rows of i (kept
+  // chunks and tall matrices) or of j.
+  const uint32_t row = threadIdx.x / 8, seg = threadIdx.x % 8 * 8;
+  struct Eight {
+    float v[8];
+  };
+  const auto fetch = [&](uint32_t chunk, bool first, Eight& to) {
+    const uint32_t j0 = chunk * 64;
+    if (!first) {
+#pragma unroll
+      for (int e = 0; e < 8; e += 4) {
+        const f32x4v v = *reinterpret_cast<const f32x4v*>(kept + (uint64_t)(j0 + row) * 64 + seg + e);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) to.v[e + k] = v[k];
+      }
+      return;
+    }
+    const uint32_t r = tall ? j0 + row : row, col = tall ? seg : j0 + seg;
+    typename Pack<S>::V w[8 / V];
+#pragma unroll
+    for (int q = 0; q < 8 / V; ++q)
+      w[q] = load_pack(x + (uint64_t)r * g.cols + col + q * V, r < g.rows ? (int64_t)g.cols - col - q * V : 0);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      to.v[e] = r < g.rows && col + e < g.cols ? (float)((double)to_f32((S)w[e / V][e % V]) * by) : 0.0f;
+  };
+  const auto lay = [&](const Eight& from, bool straight, Part (&to)[2]) {  // [row][seg ..], or turned
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      f16 hi, lo;
+      split(from.v[e], hi, lo);
+      const uint32_t at = straight ? row * kRow + seg + e : (seg + e) * kRow + row;
+      to[0][at] = hi;
+      to[1][at] = lo;
+    }
+  };
+
+  const auto cost = [&](const SmallPlan& p) {  // in chunks and products, about 0.5 us each
+    uint32_t all = (p.count + 1) * chunks;
+    return all + (p.count - 1) * (4 * p.each - 3) + 4 * p.last - 3;
+  };
+  const SmallPlan plan = cost(paired) < cost(alone) ? paired : alone;
+
+  f32x4v gram[2] = {};
+  Eight next;
+  fetch(0, true, next);
+  for (uint32_t chunk = 0; chunk < chunks; ++chunk) {
+    __syncthreads();
+    lay(next, !tall, xi);
+    if (chunk + 1 < chunks) fetch(chunk + 1, true, next);
+    __syncthreads();
+    multiply(xi, xi, gram);
+  }
+  const float to_m = kScaleM / kScaleX;
+  for (uint32_t k = 0; k < plan.count; ++k) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) put_symmetric(sq[A], q, gram[q] * (1.0f / kScaleX));
+    __syncthreads();
+    int mm = P0, pp = P0;  // the step's M; P - p0 I
+    float p0 = a;
+    for (uint32_t j = 0; j < plan.steps(k); ++j) {
+      if (j > 0) {
+        square(mm, A, A, Q, 1.0f / kScaleM, a, 0.0f);
+        square(mm, Q, Q, A, 1.0f / kScaleM, a, 0.0f);
+        mm = M;
+      }
+      square(A, A, A, mm, c * to_m / kScaleX, b * to_m, 0.0f);
+      if (j > 0) {
+        square(mm, pp, mm, pp == P0 ? P1 : P0, 1.0f / kScaleM, a, p0);
+        pp = pp == P0 ? P1 : P0;
+        p0 *= a;
+      }
+    }
+    const bool last = k + 1 == plan.count;
+    gram[0] = gram[1] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+    fetch(0, k == 0, next);
+    for (uint32_t chunk = 0; chunk < chunks; ++chunk) {
+      lay(next, k > 0 || tall, xt);
+      if (chunk + 1 < chunks) fetch(chunk + 1, k == 0, next);
+      __syncthreads();
+      f32x4v moved[2] = {};
+      multiply(sq[pp], xt, moved);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        moved[q] = moved[q] * (1.0f / kScaleM) + get(xt, q) * p0;
+        const uint32_t j = chunk * 64 + column(q);
+        if (!last) {
+          *reinterpret_cast<f32x4v*>(kept + (uint64_t)j * 64 + i) = moved[q];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f16 hi, lo;
+            split(moved[q][e], hi, lo);
+            xi[0][(i + e) * kRow + column(q)] = hi;
+            xi[1][(i + e) * kRow + column(q)] = lo;
+          }
+        } else {
+          const float move = mv.move * sqrtf(fmaxf(1.0f, (float)g.rows / (float)g.cols));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (i + e >= m || j >= n) continue;
+            const float v = moved[q][e] * (1.0f / kScaleX);
+            T* at = o + (tall ? (uint64_t)j * g.cols + i + e : (uint64_t)(i + e) * g.cols + j);
+            *at = from_f32<T>(OUT == kWeight ? fmaf(mv.keep, to_f32(*at), -move * v) : v);
+          }
+        }
+      }
+      __syncthreads();
+      if (!last) multiply(xi, xi, gram);
+    }
+  }
+}
+
 // No steps: the normalised update itself.
 template <int OUT, class S, class T>
 __global__ __launch_bounds__(kThreads) void k_normalised(Groups gs, const S* update, float eps, unsigned char* ws,
@@ -621,9 +857,14 @@ __global__ __launch_bounds__(kThreads) void k_normalised(Groups gs, const S* upd
   }
 }
 
-// The two kinds of matrices, by the shorter side: see plan_of.
-enum Kind { kNarrow, kWide, kKinds };
-Kind kind_of(uint32_t rows, uint32_t cols) { return std::min(rows, cols) <= 128 ? kNarrow : kWide; }
+// The kinds of matrices: those that one workgroup takes through its steps, up
+// to where the chip's other CUs would be faster (64 x 2048 takes about as long
+// either way), and by the shorter side the narrow and the wide ones (plan_of).
+enum Kind { kSmall, kNarrow, kWide, kKinds };
+Kind kind_of(uint32_t rows, uint32_t cols) {
+  const uint32_t m = std::min(rows, cols), n = std::max(rows, cols);
+  return m <= kSmallSide && n <= kSmallLong ? kSmall : m <= 128 ? kNarrow : kWide;
+}
 
 // Cuts the matrices of one kind into groups of equal ones that follow each
 // other, and lays their buffers out in the workspace from `used` on. Calls
@@ -647,7 +888,7 @@ uint64_t for_groups(const OrthoMatrices& ms, Kind kind, uint64_t used, F&& f) {
     }
     Group& g = gs.g[gs.count++];
     g = Group{ms.offsets[k], used, 0, 1, rows, cols, 0};
-    g.ws_of = buffers_bytes(g.m(), g.n());
+    g.ws_of = kind == kSmall ? small_bytes(g.n()) : buffers_bytes(g.m(), g.n());
     used += g.ws_of;
   }
   if (gs.count) f(gs);
@@ -714,18 +955,16 @@ struct Plan {
 // result is off by 1e-5 .. 2e-4 and 2e-4 .. 9e-4 of its norm, against 2.1e-4
 // and 1.7e-3 by the rounding to the type itself; narrower matrices (up to 128),
 // where it would be more and costs little, take two parts always.
-// Two steps taken as one, or three at the end, keep fp32's accuracy (5e-7 ..
-// 1.2e-6 of the norm; step by step 4e-7 .. 5e-7; fp32 products 1e-6 .. 2e-6);
-// more do not, as A's small entries would be lost beside its large ones.
+// Two steps taken as one keep fp32's accuracy (4e-7 .. 1.2e-6 of the norm); at
+// three (2e-6 .. 6e-6, enough for fp16) A's small singular values begin to be
+// lost beside its large ones.
 // `paired`: steps taken together.
 Plan plan_of(uint32_t steps, uint32_t type, Kind kind, bool paired) {
   const Block one{1, 1, 1, 1}, two{2, 1, 1, 1}, exact{1, 2, 2, 2};
   Plan p;
-  if (kind == kNarrow || type == SPARCML_F32) {
-    const uint32_t last = !paired ? 0 : steps % 2 ? std::min(steps, 3u) : 0;
-    if (!paired) p.add(steps, exact);
-    else p.add((steps - last) / 2, Block{2, 2, 2, 2});
-    if (last) p.add(1, Block{last, 2, 2, 2});
+  if (kind != kWide || type == SPARCML_F32) {
+    if (paired) p.add(steps / 2, Block{2, 2, 2, 2});
+    p.add(paired ? steps % 2 : steps, exact);
     return p;
   }
   const bool bf16 = type == SPARCML_BF16;
@@ -757,6 +996,17 @@ double plan_cost(const Plan& p, const Groups& gs) {
 template <int OUT, class S, class T>
 hipError_t run(Groups& gs, Kind kind, const OrthoSteps& s, uint32_t type, const S* update, T* out, Move mv,
                unsigned char* ws, hipStream_t stream) {
+  if (kind == kSmall && s.steps > 0) {
+    SmallPlan plans[2];
+    for (int paired = 0; paired < 2; ++paired) {
+      const Plan p = plan_of(s.steps, type, kind, paired != 0);
+      plans[paired] = SmallPlan{p.count, p.b[0].steps, p.b[p.count - 1].steps};
+    }
+    const uint32_t blocks = tiled(gs, [](const Group&) { return 1u; });
+    hipLaunchKernelGGL((k_small<OUT, S, T>), dim3(blocks), dim3(kSmallThreads), 0, stream, gs, plans[0], plans[1], s.a,
+                       s.b, s.c, s.eps, update, ws, out, mv);
+    return hipGetLastError();
+  }
   // the longest sums first, so that they do not start when the others end
   std::sort(gs.g, gs.g + gs.count, [](const Group& x, const Group& y) { return x.n() > y.n(); });
   uint32_t blocks = tiled(gs, parts_of_host);
