@@ -495,8 +495,10 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
   if (p.gamma != 0.0f) add(p.c2, 1, p.gamma);
 
   // A wave turns its blocks of 32 x 32 through LDS: lane l stores row l / 2,
-  // half l % 2, of the block's 32 rows of 32, 32 bytes at a time.
-  __syncthreads();
+  // half l % 2, of the block's 32 rows of 32, 32 bytes at a time. The loads past
+  // the last pass also end in LDS: every wave waits for its own before the
+  // waves meet, so that none of them lands on another's turned blocks.
+  wait_and_meet<0>();
   constexpr int PITCH = 36;
   uint32_t* turn = reinterpret_cast<uint32_t*>(lds0) + wid * 32 * PITCH;
   const uint32_t row = lane / 2, half = lane % 2 * 16;
@@ -1084,7 +1086,7 @@ uint64_t ortho_tiles(uint64_t rows, uint64_t cols) {
 size_t ortho_workspace_bytes(const OrthoMatrices& ms) {
   uint64_t used = 0;
   for (int kind = 0; kind < kKinds; ++kind) used = for_groups(ms, (Kind)kind, used, [](Groups&) {});
-  return (size_t)used + 1024;  // passes past the last load up to 256 bytes past a buffer
+  return (size_t)used + 1024;  // passes past the last load up to 512 bytes past a buffer
 }
 
 hipError_t ortho_launch(const OrthoMatrices& ms, const OrthoSteps& steps, uint32_t update_type, const void* update,
