@@ -612,230 +612,371 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
 
 // ---- matrices of a shorter side of at most 64 ---------------------------------
 //
-// One workgroup takes a matrix through all of its steps, so the chain of some
-// twenty dependent products costs no launches. The square matrices stay in LDS
-// (64 x 64, hi and lo). X passes by in chunks of 64 columns: the first pass makes
-// X X^T; every further one moves a chunk by P, keeps it in the workspace, fp32,
-// for the next pass, and adds the moved chunk's products to the next X X^T while
-// it is in LDS. Each of the 8 waves holds two blocks of 16 x 16 of a product.
-// Bound by latency: 20 matrices of 16 x 16 .. 64 x 576 take as long as the
-// largest one.
-constexpr int kSmallThreads = 512;
+// One workgroup takes a matrix through all of its steps, two taken as one, so
+// the chain of some twenty dependent products costs no launches. The square
+// matrices stay in LDS (64 x 64, hi and lo). X passes by in blocks of 32
+// columns, a block to a wave at a time, and never through LDS: the index that a
+// product sums over may run in any order that both operands share, and in the
+// order below the registers that hold a product's result are, once split into
+// parts, the operand of the next one. That needs X the way P X leaves it (a
+// lane holds rows of one column) for the next P X, and the way X^T P leaves it
+// (columns of one row) for X X^T. Both are computed from the same operands:
+// the second product is cheaper than turning the first one's result through
+// LDS, and a pass over X has no barrier but those of the last sum over the
+// waves.
+constexpr int kSmallThreads = 512, kSmallWaves = kSmallThreads / kWave;
 constexpr uint32_t kSmallSide = 64, kSmallLong = 2048;
 constexpr int kRow = 72;  // fp16 of a row in LDS: sixteen rows' 16-byte chunks fall into different banks
 
 typedef float f32x4v __attribute__((ext_vector_type(4)));
 
-// `count` blocks of `each` steps, the last one of `last`.
-struct SmallPlan {
-  uint32_t count, each, last;
-  __device__ __forceinline__ uint32_t steps(uint32_t k) const { return k + 1 < count ? each : last; }
-};
-__host__ __device__ __forceinline__ uint64_t small_bytes(uint32_t n) { return (uint64_t)up(n, 64) * 64 * sizeof(float); }
+// Blocks of 32 columns, each 64 rows in both orders, fp32.
+__host__ __device__ __forceinline__ uint64_t small_bytes(uint32_t n) { return (uint64_t)up(n, 32) / 32 * 64 * 64 * sizeof(float); }
+
+// Where a row's k-th value lies: lane group g of 16 finds k = 4 g .. 4 g + 3 and
+// 16 more, as two blocks of a result hold them, in 16 bytes.
+__device__ __forceinline__ uint32_t pos_of(uint32_t k) {
+  return (k & ~31u) | (k >> 2 & 3) << 3 | (k >> 4 & 1) << 2 | (k & 3);
+}
+
+__device__ __forceinline__ void split4(f32x4v v, f16x4& hi, f16x4& lo) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    hi[e] = (f16)v[e];
+    lo[e] = (f16)(v[e] - (float)hi[e]);
+  }
+}
+// Two of a result's blocks as an operand.
+__device__ __forceinline__ void split8(f32x4v u, f32x4v v, f16x8& hi, f16x8& lo) {
+  f16x4 h[2], l[2];
+  split4(u, h[0], l[0]);
+  split4(v, h[1], l[1]);
+  hi = __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7);
+  lo = __builtin_shufflevector(l[0], l[1], 0, 1, 2, 3, 4, 5, 6, 7);
+}
+__device__ __forceinline__ f32x4v multiply_parts(f16x8 ah, f16x8 al, f16x8 bh, f16x8 bl, f32x4v acc) {
+  acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(ah, bh, acc, 0, 0, 0);
+  acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(ah, bl, acc, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(al, bh, acc, 0, 0, 0);
+}
 
 template <int OUT, class S, class T>
-__global__ __launch_bounds__(kSmallThreads) void k_small(Groups gs, SmallPlan alone, SmallPlan paired, float a, float b,
-                                                         float c, float eps, const S* update, unsigned char* ws, T* out,
-                                                         Move mv) {
+__global__ __launch_bounds__(kSmallThreads) void k_small(Groups gs, uint32_t steps, float a, float b, float c, float eps,
+                                                         const S* update, unsigned char* ws, T* out, Move mv) {
+  typedef f16 Part[64 * kRow];
   enum { A, M, Q, P0, P1, SQUARES };
-  __shared__ __align__(16) f16 sq[SQUARES][2][64 * kRow];
-  __shared__ __align__(16) f16 xt[2][64 * kRow], xi[2][64 * kRow];  // a chunk: [j][i] as it comes, [i][j] once moved
-  __shared__ double scratch[kSmallThreads / kWave];
+  constexpr int kPairs = 10;  // blocks of 16 x 16 on and below the diagonal
+  // behind A, the waves' sums of X X^T take the place of the other squares
+  constexpr int kSums = kSmallWaves * kPairs * kWave * (int)sizeof(f32x4v), kOthers = (SQUARES - 1) * 2 * (int)sizeof(Part);
+  __shared__ __align__(16) unsigned char lds[2 * sizeof(Part) + (kSums > kOthers ? kSums : kOthers)];
+  __shared__ double scratch[kSmallWaves];
+  Part(*const sq)[2] = reinterpret_cast<Part(*)[2]>(lds);
+  f32x4v* const sums = reinterpret_cast<f32x4v*>(lds + 2 * sizeof(Part));
+
   const Item it = item_of(gs, blockIdx.x);
   const Group& g = gs.g[it.g];
   if (it.k >= g.count) return;
   const bool tall = g.tall();
-  const uint32_t m = tall ? g.cols : g.rows, n = tall ? g.rows : g.cols, chunks = (n + 63) / 64;
+  const uint32_t n = tall ? g.rows : g.cols, blocks = (n + 31) / 32;
   const uint64_t size = (uint64_t)g.rows * g.cols;
   const S* x = update + g.at + it.k * size;
   T* o = out + g.at + it.k * size;
-  float* kept = reinterpret_cast<float*>(ws + g.ws + it.k * g.ws_of);  // X, [j][64]
-  const uint32_t lane = lane_id(), wid = threadIdx.x / kWave;
-  const uint32_t bi = wid / 2 * 16, bj = wid % 2 * 32;  // this wave's blocks: rows bi, columns bj and bj + 16
+  const uint32_t lane = lane_id(), wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const uint32_t in = lane % 16, four = lane / 16 * 4;  // a result's block: this lane's column, and its rows from there
+  f32x4v* kept = reinterpret_cast<f32x4v*>(ws + g.ws + it.k * g.ws_of) + lane;
 
-  constexpr int V = Pack<S>::N;
-  double sum = 0.0;
-#pragma unroll 4
-  for (uint64_t i = threadIdx.x * V; i < size; i += kSmallThreads * V) {
-    const typename Pack<S>::V w = load_pack(x + i, (int64_t)(size - i));
+  // A block of X: xu[c][b][e] at row 16 b + four + e, column 16 c + in;
+  // xt[b][c][e] at row 16 b + in, column 16 c + four + e.
+  f32x4v xu[2][4], xt[4][2];
+  const auto keep = [&](uint32_t blk) {
+    f32x4v* p = kept + (uint64_t)blk * 16 * kWave;
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const double v = to_f32((S)w[e]);
-      sum = fma(v, v, sum);
-    }
-  }
-  const double by = (double)kScaleX / (sqrt(block_sum_f64<kSmallThreads>(sum, scratch)) + (double)eps);
-
-  const auto split = [](float v, f16& hi, f16& lo) {
-    hi = (f16)v;
-    lo = (f16)(v - (float)hi);
-  };
-  typedef f16 Part[64 * kRow];
-  // acc += rows bi of `l` times rows bj of `r`, both along the summed index
-  const auto multiply = [&](const Part (&l)[2], const Part (&r)[2], f32x4v (&acc)[2]) {
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      const uint32_t at = lane % 16 * kRow + ks * 32 + lane / 16 * 8;
-      const f16x8 lh = *reinterpret_cast<const f16x8*>(&l[0][bi * kRow + at]);
-      const f16x8 ll = *reinterpret_cast<const f16x8*>(&l[1][bi * kRow + at]);
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const f16x8 rh = *reinterpret_cast<const f16x8*>(&r[0][(bj + q * 16) * kRow + at]);
-        const f16x8 rl = *reinterpret_cast<const f16x8*>(&r[1][(bj + q * 16) * kRow + at]);
-        acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lh, rh, acc[q], 0, 0, 0);
-        acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lh, rl, acc[q], 0, 0, 0);
-        acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ll, rh, acc[q], 0, 0, 0);
+      for (int b = 0; b < 4; ++b) {
+        p[(c * 4 + b) * kWave] = xu[c][b];
+        p[(8 + b * 2 + c) * kWave] = xt[b][c];
       }
-    }
   };
-  // acc[q][e] is at row i + e, column j of the product
-  const uint32_t i = bi + lane / 16 * 4;
-  const auto column = [&](int q) { return bj + q * 16 + lane % 16; };
-  // four values along i of a matrix stored [j][i]
-  const auto get = [&](const Part (&from)[2], int q) {
-    const f16x4 h = *reinterpret_cast<const f16x4*>(&from[0][column(q) * kRow + i]);
-    const f16x4 l = *reinterpret_cast<const f16x4*>(&from[1][column(q) * kRow + i]);
-    f32x4v v;
+  const auto fetch_u = [&](uint32_t blk) {
+    const f32x4v* p = kept + (uint64_t)blk * 16 * kWave;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = (float)h[e] + (float)l[e];
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) xu[c][b] = p[(c * 4 + b) * kWave];
+  };
+  const auto fetch_t = [&](uint32_t blk) {
+    const f32x4v* p = kept + (uint64_t)blk * 16 * kWave;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) xt[b][c] = p[(8 + b * 2 + c) * kWave];
+  };
+
+  // Blocks of 16 x 16 of the update, by its own rows and columns: `along`
+  // holds 4 columns of a row, `down` 4 rows of a column. Every load is made, at
+  // a place inside, so that all are under way at once.
+  const auto along = [&](uint32_t r0, uint32_t c0) {
+    const uint32_t r = r0 + in, c = c0 + four;
+    const S* p = x + (uint64_t)min(r, g.rows - 1) * g.cols;
+    f32x4v v;
+    if (c0 + 16 <= g.cols) {
+      typedef S S4 __attribute__((ext_vector_type(4)));
+      typedef S4 S4u __attribute__((aligned(sizeof(S))));
+      const S4 w = *reinterpret_cast<const S4u*>(p + c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = to_f32((S)w[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = to_f32(p[min(c + e, g.cols - 1)]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = r < g.rows && c + e < g.cols ? v[e] : 0.0f;
     return v;
   };
-  // A symmetric matrix from its values on and below the diagonal.
-  const auto put_symmetric = [&](Part (&to)[2], int q, f32x4v v) {
-    const uint32_t j = column(q);
+  const auto down = [&](uint32_t r0, uint32_t c0) {
+    const uint32_t r = r0 + four, c = c0 + in;
+    f32x4v v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      v[e] = to_f32(x[(uint64_t)min(r + e, g.rows - 1) * g.cols + min(c, g.cols - 1)]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = r + e < g.rows && c < g.cols ? v[e] : 0.0f;
+    return v;
+  };
+  double sum = 0.0;
+  for (uint32_t blk = wid; blk < blocks; blk += kSmallWaves) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const uint32_t i0 = b * 16, j0 = blk * 32 + c * 16;
+        if (tall) {
+          xu[c][b] = along(j0, i0);
+          xt[b][c] = down(j0, i0);
+        } else {
+          xu[c][b] = down(i0, j0);
+          xt[b][c] = along(i0, j0);
+        }
+      }
+    keep(blk);
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const double v = xu[c][b][e];
+          sum = fma(v, v, sum);
+        }
+  }
+  const double by = (double)kScaleX / (sqrt(block_sum_f64<kSmallThreads>(sum, scratch)) + (double)eps);
+  const auto normalise = [&](f32x4v& v) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = (float)((double)v[e] * by);
+  };
+
+  // X X^T: block (b, q), q <= b, of this wave's columns
+  f32x4v gram[kPairs];
+  const auto clear_gram = [&] {
+#pragma unroll
+    for (int t = 0; t < kPairs; ++t) gram[t] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+  };
+  const auto add_to_gram = [&] {
+    f16x8 h[4], l[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) split8(xt[b][0], xt[b][1], h[b], l[b]);
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int q = 0; q <= b; ++q)
+        gram[b * (b + 1) / 2 + q] = multiply_parts(h[b], l[b], h[q], l[q], gram[b * (b + 1) / 2 + q]);
+  };
+
+  // Rows i .. i + 3 of column j of a symmetric matrix, those on and below the
+  // diagonal, and their mirror.
+  const auto put_symmetric = [&](Part (&to)[2], uint32_t i, uint32_t j, f32x4v v) {
+    f16x4 hi, lo;
+    split4(v, hi, lo);
+    if (i >= j) {
+      *reinterpret_cast<f16x4*>(&to[0][j * kRow + pos_of(i)]) = hi;
+      *reinterpret_cast<f16x4*>(&to[1][j * kRow + pos_of(i)]) = lo;
+    }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (i + e < j) continue;
-      f16 hi, lo;
-      split(v[e], hi, lo);
-      to[0][j * kRow + i + e] = hi;
-      to[1][j * kRow + i + e] = lo;
-      to[0][(i + e) * kRow + j] = hi;
-      to[1][(i + e) * kRow + j] = lo;
+      to[0][(i + e) * kRow + pos_of(j)] = hi[e];
+      to[1][(i + e) * kRow + pos_of(j)] = lo[e];
+      if (i < j) {
+        to[0][j * kRow + pos_of(i + e)] = hi[e];
+        to[1][j * kRow + pos_of(i + e)] = lo[e];
+      }
     }
   };
-  // d = alpha l r + beta r + gamma c2, all symmetric
+  // A = X X^T of the waves' parts of it, in the order of the waves
+  const auto join_gram = [&] {
+    __syncthreads();  // the squares have been read
+    const uint32_t waves = min(blocks, (uint32_t)kSmallWaves);
+    if (wid < waves) {
+#pragma unroll
+      for (int t = 0; t < kPairs; ++t) sums[(wid * kPairs + t) * kWave + lane] = gram[t];
+    }
+    __syncthreads();
+    for (uint32_t t = wid; t < (uint32_t)kPairs; t += kSmallWaves) {
+      f32x4v v = sums[t * kWave + lane];
+      for (uint32_t w = 1; w < waves; ++w) v += sums[(w * kPairs + t) * kWave + lane];
+      uint32_t b, q;
+      pair_at(t, b, q);
+      put_symmetric(sq[A], b * 16 + four, q * 16 + in, v * (1.0f / kScaleX));
+    }
+    __syncthreads();
+  };
+
+  // d = alpha l r + beta r + gamma c2, all symmetric: a wave takes the blocks
+  // below the diagonal of (row bi, columns bj and bj + 1)
+  const uint32_t bi = wid / 2, bj = wid % 2 * 2;
   const auto square = [&](int l, int r, int c2, int d, float alpha, float beta, float gamma) {
-    f32x4v acc[2] = {};
-    multiply(sq[l], sq[r], acc);
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      f32x4v v = acc[q] * alpha + get(sq[r], q) * beta;
-      if (gamma != 0.0f) v += get(sq[c2], q) * gamma;
-      put_symmetric(sq[d], q, v);
-    }
-    __syncthreads();
-  };
-
-  // Eight values of a chunk to a thread, as memory has them: rows of i (kept
-  // chunks and tall matrices) or of j.
-  const uint32_t row = threadIdx.x / 8, seg = threadIdx.x % 8 * 8;
-  struct Eight {
-    float v[8];
-  };
-  const auto fetch = [&](uint32_t chunk, bool first, Eight& to) {
-    const uint32_t j0 = chunk * 64;
-    if (!first) {
-#pragma unroll
-      for (int e = 0; e < 8; e += 4) {
-        const f32x4v v = *reinterpret_cast<const f32x4v*>(kept + (uint64_t)(j0 + row) * 64 + seg + e);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) to.v[e + k] = v[k];
-      }
-      return;
-    }
-    const uint32_t r = tall ? j0 + row : row, col = tall ? seg : j0 + seg;
-    typename Pack<S>::V w[8 / V];
-#pragma unroll
-    for (int q = 0; q < 8 / V; ++q)
-      w[q] = load_pack(x + (uint64_t)r * g.cols + col + q * V, r < g.rows ? (int64_t)g.cols - col - q * V : 0);
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      to.v[e] = r < g.rows && col + e < g.cols ? (float)((double)to_f32((S)w[e / V][e % V]) * by) : 0.0f;
-  };
-  const auto lay = [&](const Eight& from, bool straight, Part (&to)[2]) {  // [row][seg ..], or turned
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      f16 hi, lo;
-      split(from.v[e], hi, lo);
-      const uint32_t at = straight ? row * kRow + seg + e : (seg + e) * kRow + row;
-      to[0][at] = hi;
-      to[1][at] = lo;
-    }
-  };
-
-  const auto cost = [&](const SmallPlan& p) {  // in chunks and products, about 0.5 us each
-    uint32_t all = (p.count + 1) * chunks;
-    return all + (p.count - 1) * (4 * p.each - 3) + 4 * p.last - 3;
-  };
-  const SmallPlan plan = cost(paired) < cost(alone) ? paired : alone;
-
-  f32x4v gram[2] = {};
-  Eight next;
-  fetch(0, true, next);
-  for (uint32_t chunk = 0; chunk < chunks; ++chunk) {
-    __syncthreads();
-    lay(next, !tall, xi);
-    if (chunk + 1 < chunks) fetch(chunk + 1, true, next);
-    __syncthreads();
-    multiply(xi, xi, gram);
-  }
-  const float to_m = kScaleM / kScaleX;
-  for (uint32_t k = 0; k < plan.count; ++k) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q) put_symmetric(sq[A], q, gram[q] * (1.0f / kScaleX));
-    __syncthreads();
-    int mm = P0, pp = P0;  // the step's M; P - p0 I
-    float p0 = a;
-    for (uint32_t j = 0; j < plan.steps(k); ++j) {
-      if (j > 0) {
-        square(mm, A, A, Q, 1.0f / kScaleM, a, 0.0f);
-        square(mm, Q, Q, A, 1.0f / kScaleM, a, 0.0f);
-        mm = M;
-      }
-      square(A, A, A, mm, c * to_m / kScaleX, b * to_m, 0.0f);
-      if (j > 0) {
-        square(mm, pp, mm, pp == P0 ? P1 : P0, 1.0f / kScaleM, a, p0);
-        pp = pp == P0 ? P1 : P0;
-        p0 *= a;
-      }
-    }
-    const bool last = k + 1 == plan.count;
-    gram[0] = gram[1] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
-    fetch(0, k == 0, next);
-    for (uint32_t chunk = 0; chunk < chunks; ++chunk) {
-      lay(next, k > 0 || tall, xt);
-      if (chunk + 1 < chunks) fetch(chunk + 1, k == 0, next);
-      __syncthreads();
-      f32x4v moved[2] = {};
-      multiply(sq[pp], xt, moved);
+    const uint32_t at = in * kRow + lane / 16 * 8;
+    const auto operand = [&](int of, int part, uint32_t blk, int s) {
+      return *reinterpret_cast<const f16x8*>(&sq[of][part][blk * 16 * kRow + at + s * 32]);
+    };
+    if (bj <= bi) {
+      f32x4v v[2];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        moved[q] = moved[q] * (1.0f / kScaleM) + get(xt, q) * p0;
-        const uint32_t j = chunk * 64 + column(q);
-        if (!last) {
-          *reinterpret_cast<f32x4v*>(kept + (uint64_t)j * 64 + i) = moved[q];
+        const uint32_t i = bi * 16 + four, j = (bj + q) * 16 + in, of = j * kRow + pos_of(i);
+        const auto get = [&](int m) {
+          const f16x4 h = *reinterpret_cast<const f16x4*>(&sq[m][0][of]);
+          const f16x4 o4 = *reinterpret_cast<const f16x4*>(&sq[m][1][of]);
+          f32x4v w;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            f16 hi, lo;
-            split(moved[q][e], hi, lo);
-            xi[0][(i + e) * kRow + column(q)] = hi;
-            xi[1][(i + e) * kRow + column(q)] = lo;
+          for (int e = 0; e < 4; ++e) w[e] = (float)h[e] + (float)o4[e];
+          return w;
+        };
+        v[q] = get(r) * beta;
+        if (gamma != 0.0f) v[q] += get(c2) * gamma;
+        f32x4v acc = {};
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          acc = multiply_parts(operand(l, 0, bi, s), operand(l, 1, bi, s), operand(r, 0, bj + q, s),
+                               operand(r, 1, bj + q, s), acc);
+        v[q] += acc * alpha;
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        if (bj + q <= bi) put_symmetric(sq[d], bi * 16 + four, (bj + q) * 16 + in, v[q]);
+    }
+    __syncthreads();
+  };
+
+  clear_gram();
+  for (uint32_t blk = wid; blk < blocks; blk += kSmallWaves) {
+    fetch_t(blk);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      normalise(xt[b][0]);
+      normalise(xt[b][1]);
+    }
+    add_to_gram();
+  }
+  join_gram();
+  const float to_m = kScaleM / kScaleX;
+  for (uint32_t done = 0; done < steps; done += 2) {
+    const bool pair = done + 1 < steps, last = done + 2 >= steps;
+    // P - p0 I, P the product of the one or two steps' Q = a I + M
+    square(A, A, A, P0, c * to_m / kScaleX, b * to_m, 0.0f);
+    if (pair) {
+      square(P0, A, A, Q, 1.0f / kScaleM, a, 0.0f);
+      square(P0, Q, Q, A, 1.0f / kScaleM, a, 0.0f);
+      square(A, A, A, M, c * to_m / kScaleX, b * to_m, 0.0f);
+      square(M, P0, M, P1, 1.0f / kScaleM, a, a);
+    }
+    const float p0 = (pair ? a * a : a) * kScaleM;
+    f16x8 ph[4][2], pl[4][2];
+    {
+      const Part(&p)[2] = sq[pair ? P1 : P0];
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const uint32_t at = (b * 16 + in) * kRow + lane / 16 * 8 + s * 32;
+          ph[b][s] = *reinterpret_cast<const f16x8*>(&p[0][at]);
+          pl[b][s] = *reinterpret_cast<const f16x8*>(&p[1][at]);
+        }
+    }
+    clear_gram();
+    for (uint32_t blk = wid; blk < blocks; blk += kSmallWaves) {
+      fetch_u(blk);
+      fetch_t(blk);
+      if (done == 0) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            normalise(xu[c][b]);
+            normalise(xt[b][c]);
           }
-        } else {
-          const float move = mv.move * sqrtf(fmaxf(1.0f, (float)g.rows / (float)g.cols));
+      }
+      f16x8 h[2][2], l[2][2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (i + e >= m || j >= n) continue;
-            const float v = moved[q][e] * (1.0f / kScaleX);
-            T* at = o + (tall ? (uint64_t)j * g.cols + i + e : (uint64_t)(i + e) * g.cols + j);
-            *at = from_f32<T>(OUT == kWeight ? fmaf(mv.keep, to_f32(*at), -move * v) : v);
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) split8(xu[c][2 * s], xu[c][2 * s + 1], h[c][s], l[c][s]);
+      if (!last || tall) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            f32x4v v = xu[c][b] * p0;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) v = multiply_parts(ph[b][s], pl[b][s], h[c][s], l[c][s], v);
+            xu[c][b] = v * (1.0f / kScaleM);
+          }
+      }
+      if (!last || !tall) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            f32x4v v = xt[b][c] * p0;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) v = multiply_parts(h[c][s], l[c][s], ph[b][s], pl[b][s], v);
+            xt[b][c] = v * (1.0f / kScaleM);
+          }
+      }
+      if (!last) {
+        keep(blk);
+        add_to_gram();
+        continue;
+      }
+      const float move = mv.move * sqrtf(fmaxf(1.0f, (float)g.rows / (float)g.cols));
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const uint32_t i0 = b * 16, j0 = blk * 32 + c * 16;
+          const uint32_t r = (tall ? j0 : i0) + in, col = (tall ? i0 : j0) + four;
+          if (r >= g.rows) continue;
+          T* at = o + (uint64_t)r * g.cols + col;
+          const f32x4v v = (tall ? xu[c][b] : xt[b][c]) * (1.0f / kScaleX);
+          typedef T T4 __attribute__((ext_vector_type(4)));
+          typedef T4 T4u __attribute__((aligned(sizeof(T))));
+          if (col + 4 <= g.cols) {
+            T4 w = {};
+            if (OUT == kWeight) w = *reinterpret_cast<const T4u*>(at);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = from_f32<T>(OUT == kWeight ? fmaf(mv.keep, to_f32((T)w[e]), -move * v[e]) : v[e]);
+            *reinterpret_cast<T4u*>(at) = w;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (col + e < g.cols)
+                at[e] = from_f32<T>(OUT == kWeight ? fmaf(mv.keep, to_f32(at[e]), -move * v[e]) : v[e]);
           }
         }
-      }
-      __syncthreads();
-      if (!last) multiply(xi, xi, gram);
     }
+    if (!last) join_gram();
   }
 }
 
@@ -999,14 +1140,9 @@ template <int OUT, class S, class T>
 hipError_t run(Groups& gs, Kind kind, const OrthoSteps& s, uint32_t type, const S* update, T* out, Move mv,
                unsigned char* ws, hipStream_t stream) {
   if (kind == kSmall && s.steps > 0) {
-    SmallPlan plans[2];
-    for (int paired = 0; paired < 2; ++paired) {
-      const Plan p = plan_of(s.steps, type, kind, paired != 0);
-      plans[paired] = SmallPlan{p.count, p.b[0].steps, p.b[p.count - 1].steps};
-    }
     const uint32_t blocks = tiled(gs, [](const Group&) { return 1u; });
-    hipLaunchKernelGGL((k_small<OUT, S, T>), dim3(blocks), dim3(kSmallThreads), 0, stream, gs, plans[0], plans[1], s.a,
-                       s.b, s.c, s.eps, update, ws, out, mv);
+    hipLaunchKernelGGL((k_small<OUT, S, T>), dim3(blocks), dim3(kSmallThreads), 0, stream, gs, s.steps, s.a, s.b, s.c,
+                       s.eps, update, ws, out, mv);
     return hipGetLastError();
   }
   // the longest sums first, so that they do not start when the others end
