@@ -290,6 +290,8 @@ struct Shape {
   static constexpr int W = WI * WJ, NT = W * kWave, I = WI * TI * 32, J = WJ * TJ * 32;
   static constexpr int DEPTH = 64 / PARTS;  // summed index of a pass: rows of 128 bytes
   static constexpr int SIZE = (I + J) * 8;
+  static constexpr int PITCH = 36;  // of a block of 32 x 32 that a wave turns
+  static constexpr int FIRST = SIZE > W * 32 * PITCH / 4 ? SIZE : W * 32 * PITCH / 4;  // the first buffer: the turned blocks too
   static_assert(W % 2 == 0, "a lane's chunk is the same in every load");
 };
 
@@ -314,7 +316,7 @@ struct Spread {
 template <class S, int OUT, class T>
 __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups gs, Product p, unsigned char* ws,
                                                                         T* out, Move mv) {
-  __shared__ f16x8 lds0[S::SIZE], lds1[S::SIZE], lds2[S::BUFFERS > 2 ? S::SIZE : 1], lds3[S::BUFFERS > 2 ? S::SIZE : 1];
+  __shared__ f16x8 lds0[S::FIRST], lds1[S::SIZE], lds2[S::BUFFERS > 2 ? S::SIZE : 1], lds3[S::BUFFERS > 2 ? S::SIZE : 1];
   const Item it = item_of(gs, blockIdx.x);
   const Group& g = gs.g[it.g];
   if (it.k >= g.count) return;
@@ -499,7 +501,7 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
   // the last pass also end in LDS: every wave waits for its own before the
   // waves meet, so that none of them lands on another's turned blocks.
   wait_and_meet<0>();
-  constexpr int PITCH = 36;
+  constexpr int PITCH = S::PITCH;
   uint32_t* turn = reinterpret_cast<uint32_t*>(lds0) + wid * 32 * PITCH;
   const uint32_t row = lane / 2, half = lane % 2 * 16;
   u32x4* put = reinterpret_cast<u32x4*>(turn + lane % 32 * PITCH + lane / 32 * 4);
@@ -1061,15 +1063,19 @@ template <int PARTS, int OUT, class T>
 hipError_t launch_product(Groups& gs, const Product& p, unsigned char* ws, T* out, Move mv, hipStream_t stream) {
   using Large = Shape<2, 4, 4, 2, PARTS, 2>;  // 256 x 256, 8 waves
   using Small = Shape<2, 2, 2, 2, PARTS, 4>;  // 128 x 128, 4 waves
-  uint64_t large = 0;
-  for (uint32_t k = 0; k < gs.count; ++k) large += (uint64_t)gs.g[k].count * product_tiles<Large>(gs.g[k], p);
+  using Tiny = Shape<2, 2, 1, 1, PARTS, 4>;   // 64 x 64, 4 waves
+  uint64_t large = 0, tiny = 0;
+  for (uint32_t k = 0; k < gs.count; ++k) {
+    large += (uint64_t)gs.g[k].count * product_tiles<Large>(gs.g[k], p);
+    tiny += (uint64_t)gs.g[k].count * product_tiles<Tiny>(gs.g[k], p);
+  }
   const auto launch = [&](auto shape) {
     using S = decltype(shape);
     const uint32_t blocks = tiled(gs, [&](const Group& g) { return product_tiles<S>(g, p); });
     hipLaunchKernelGGL((k_product<S, OUT, T>), dim3(blocks), dim3(S::NT), 0, stream, gs, p, ws, out, mv);
     return hipGetLastError();
   };
-  return large >= 256 ? launch(Large{}) : launch(Small{});
+  return large >= 256 ? launch(Large{}) : tiny > 512 ? launch(Small{}) : launch(Tiny{});
 }
 
 // `steps` steps taken as one: with A = X X^T, Q = a I + M, M = b A + c A A,
