@@ -148,7 +148,7 @@ __device__ __forceinline__ void store_parts(const float (&v)[16], f16* hi, uint3
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     h[e / 8][e % 8] = (f16)v[e];
-    l[e / 8][e % 8] = (f16)(v[e] - (float)h[e / 8][e % 8]);
+    l[e / 8][e % 8] = (f16)fmaf((float)h[e / 8][e % 8], -1.0f, v[e]);
   }
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
@@ -534,7 +534,7 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float v = acc[x][y][q * 4 + e];
-            const f16 h = (f16)v, l = (f16)(v - (float)h);
+            const f16 h = (f16)v, l = (f16)fmaf((float)h, -1.0f, v);
             w[e] = (uint32_t)__builtin_bit_cast(uint16_t, h) | (uint32_t)__builtin_bit_cast(uint16_t, l) << 16;
           }
           put[q * 2] = w;
@@ -645,7 +645,7 @@ __device__ __forceinline__ void split4(f32x4v v, f16x4& hi, f16x4& lo) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     hi[e] = (f16)v[e];
-    lo[e] = (f16)(v[e] - (float)hi[e]);
+    lo[e] = (f16)fmaf((float)hi[e], -1.0f, v[e]);  // one instruction
   }
 }
 // Two of a result's blocks as an operand.
@@ -662,42 +662,84 @@ __device__ __forceinline__ f32x4v multiply_parts(f16x8 ah, f16x8 al, f16x8 bh, f
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(al, bh, acc, 0, 0, 0);
 }
 
-template <int OUT, class S, class T>
-__global__ __launch_bounds__(kSmallThreads) void k_small(Groups gs, uint32_t steps, float a, float b, float c, float eps,
-                                                         const S* update, unsigned char* ws, T* out, Move mv) {
-  typedef f16 Part[64 * kRow];
-  enum { A, M, Q, P0, P1, SQUARES };
-  constexpr int kPairs = 10;  // blocks of 16 x 16 on and below the diagonal
-  // behind A, the waves' sums of X X^T take the place of the other squares
-  constexpr int kSums = kSmallWaves * kPairs * kWave * (int)sizeof(f32x4v), kOthers = (SQUARES - 1) * 2 * (int)sizeof(Part);
-  __shared__ __align__(16) unsigned char lds[2 * sizeof(Part) + (kSums > kOthers ? kSums : kOthers)];
-  __shared__ double scratch[kSmallWaves];
-  Part(*const sq)[2] = reinterpret_cast<Part(*)[2]>(lds);
-  f32x4v* const sums = reinterpret_cast<f32x4v*>(lds + 2 * sizeof(Part));
+// Blocks of 16 x 16 of a row-major matrix from its first row r0 and column c0
+// on: `along` holds 4 columns of a row, `down` 4 rows of a column. Inside the
+// matrix the places are a base that the wave shares and a lane's offset; at its
+// edges every load is made all the same, at a place inside.
+template <class S>
+struct Blocks16 {
+  const S* x;
+  uint32_t rows, cols, in, four;
 
-  const Item it = item_of(gs, blockIdx.x);
-  const Group& g = gs.g[it.g];
-  if (it.k >= g.count) return;
+  __device__ __forceinline__ f32x4v along(uint32_t r0, uint32_t c0, bool inside) const {
+    f32x4v v;
+    if (inside) {
+      typedef S S4 __attribute__((ext_vector_type(4)));
+      typedef S4 S4u __attribute__((aligned(sizeof(S))));
+      const S4 w = *reinterpret_cast<const S4u*>(x + ((uint64_t)r0 * cols + c0) + (in * cols + four));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = to_f32((S)w[e]);
+      return v;
+    }
+    const uint32_t r = r0 + in, c = c0 + four;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = to_f32(x[(uint64_t)min(r, rows - 1) * cols + min(c + e, cols - 1)]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = r < rows && c + e < cols ? v[e] : 0.0f;
+    return v;
+  }
+  __device__ __forceinline__ f32x4v down(uint32_t r0, uint32_t c0, bool inside) const {
+    f32x4v v;
+    if (inside) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = to_f32((x + ((uint64_t)(r0 + e) * cols + c0))[four * cols + in]);
+      return v;
+    }
+    const uint32_t r = r0 + four, c = c0 + in;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = to_f32(x[(uint64_t)min(r + e, rows - 1) * cols + min(c, cols - 1)]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = r + e < rows && c < cols ? v[e] : 0.0f;
+    return v;
+  }
+};
+
+typedef f16 Part[64 * kRow];
+enum { kSqA, kSqM, kSqQ, kSqP, kSqP2, kSquares };
+// Behind A, the waves' sums of X X^T take the place of the other squares.
+struct SmallLds {
+  static constexpr int kSums = kSmallWaves * 10 * kWave * (int)sizeof(f32x4v);
+  static constexpr int kOthers = (kSquares - 1) * 2 * (int)sizeof(Part);
+  __align__(16) unsigned char bytes[2 * sizeof(Part) + (kSums > kOthers ? kSums : kOthers)];
+  double scratch[kSmallWaves];
+};
+
+// RB: blocks of 16 rows, 2 (a short side of up to 32) or 4.
+template <int RB, int OUT, class S, class T>
+__device__ __forceinline__ void small_steps(SmallLds& lds, const Group& g, uint32_t steps, float a, float b, float c,
+                                            float eps, const S* x, f32x4v* kept, T* o, Move mv) {
+  constexpr int kPairs = RB * (RB + 1) / 2;  // blocks of 16 x 16 on and below the diagonal
+  constexpr int SL = RB / 2;                 // slabs of 32 of the index of rows
+  Part(*const sq)[2] = reinterpret_cast<Part(*)[2]>(lds.bytes);
+  f32x4v* const sums = reinterpret_cast<f32x4v*>(lds.bytes + 2 * sizeof(Part));
   const bool tall = g.tall();
-  const uint32_t n = tall ? g.rows : g.cols, blocks = (n + 31) / 32;
-  const uint64_t size = (uint64_t)g.rows * g.cols;
-  const S* x = update + g.at + it.k * size;
-  T* o = out + g.at + it.k * size;
+  const uint32_t m = tall ? g.cols : g.rows, n = tall ? g.rows : g.cols, blocks = (n + 31) / 32;
   const uint32_t lane = lane_id(), wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const uint32_t in = lane % 16, four = lane / 16 * 4;  // a result's block: this lane's column, and its rows from there
-  f32x4v* kept = reinterpret_cast<f32x4v*>(ws + g.ws + it.k * g.ws_of) + lane;
+  // a wave has one block at most: it stays in registers, where these are not short
+  const bool held = RB == 2 && blocks <= (uint32_t)kSmallWaves;
 
   // A block of X: xu[c][b][e] at row 16 b + four + e, column 16 c + in;
   // xt[b][c][e] at row 16 b + in, column 16 c + four + e.
-  f32x4v xu[2][4], xt[4][2];
+  f32x4v xu[2][RB], xt[RB][2];
   const auto keep = [&](uint32_t blk) {
     f32x4v* p = kept + (uint64_t)blk * 16 * kWave;
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        p[(c * 4 + b) * kWave] = xu[c][b];
-        p[(8 + b * 2 + c) * kWave] = xt[b][c];
+      for (int b = 0; b < RB; ++b) {
+        p[(c * 4 + b) * kWave + lane] = xu[c][b];
+        p[(8 + b * 2 + c) * kWave + lane] = xt[b][c];
       }
   };
   const auto fetch_u = [&](uint32_t blk) {
@@ -705,77 +747,65 @@ __global__ __launch_bounds__(kSmallThreads) void k_small(Groups gs, uint32_t ste
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int b = 0; b < 4; ++b) xu[c][b] = p[(c * 4 + b) * kWave];
+      for (int b = 0; b < RB; ++b) xu[c][b] = p[(c * 4 + b) * kWave + lane];
   };
   const auto fetch_t = [&](uint32_t blk) {
     const f32x4v* p = kept + (uint64_t)blk * 16 * kWave;
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int b = 0; b < 4; ++b) xt[b][c] = p[(8 + b * 2 + c) * kWave];
+      for (int b = 0; b < RB; ++b) xt[b][c] = p[(8 + b * 2 + c) * kWave + lane];
   };
 
-  // Blocks of 16 x 16 of the update, by its own rows and columns: `along`
-  // holds 4 columns of a row, `down` 4 rows of a column. Every load is made, at
-  // a place inside, so that all are under way at once.
-  const auto along = [&](uint32_t r0, uint32_t c0) {
-    const uint32_t r = r0 + in, c = c0 + four;
-    const S* p = x + (uint64_t)min(r, g.rows - 1) * g.cols;
-    f32x4v v;
-    if (c0 + 16 <= g.cols) {
-      typedef S S4 __attribute__((ext_vector_type(4)));
-      typedef S4 S4u __attribute__((aligned(sizeof(S))));
-      const S4 w = *reinterpret_cast<const S4u*>(p + c);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = to_f32((S)w[e]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = to_f32(p[min(c + e, g.cols - 1)]);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = r < g.rows && c + e < g.cols ? v[e] : 0.0f;
-    return v;
-  };
-  const auto down = [&](uint32_t r0, uint32_t c0) {
-    const uint32_t r = r0 + four, c = c0 + in;
-    f32x4v v;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      v[e] = to_f32(x[(uint64_t)min(r + e, g.rows - 1) * g.cols + min(c, g.cols - 1)]);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = r + e < g.rows && c < g.cols ? v[e] : 0.0f;
-    return v;
-  };
   double sum = 0.0;
-  for (uint32_t blk = wid; blk < blocks; blk += kSmallWaves) {
+  const Blocks16<S> from{x, g.rows, g.cols, in, four};
+  const auto load = [&](uint32_t blk, auto inside) {
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
+      for (int b = 0; b < RB; ++b) {
         const uint32_t i0 = b * 16, j0 = blk * 32 + c * 16;
         if (tall) {
-          xu[c][b] = along(j0, i0);
-          xt[b][c] = down(j0, i0);
+          xu[c][b] = from.along(j0, i0, inside());
+          xt[b][c] = from.down(j0, i0, inside());
         } else {
-          xu[c][b] = down(i0, j0);
-          xt[b][c] = along(i0, j0);
+          xu[c][b] = from.down(i0, j0, inside());
+          xt[b][c] = from.along(i0, j0, inside());
         }
       }
-    keep(blk);
+  };
+  for (uint32_t blk = wid; blk < blocks; blk += kSmallWaves) {
+    if (m == RB * 16 && blk * 32 + 32 <= n) load(blk, std::true_type{});
+    else load(blk, std::false_type{});
+    if (!held) keep(blk);
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
+      for (int b = 0; b < RB; ++b)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const double v = xu[c][b][e];
           sum = fma(v, v, sum);
         }
   }
-  const double by = (double)kScaleX / (sqrt(block_sum_f64<kSmallThreads>(sum, scratch)) + (double)eps);
+  // v * by as v * 2^power * (hi + lo), whatever the update's magnitude
+  const double by = (double)kScaleX / (sqrt(block_sum_f64<kSmallThreads>(sum, lds.scratch)) + (double)eps);
+  int power;
+  const double rest = frexp(by, &power);
+  const float by_hi = (float)rest, by_lo = by_hi - by_hi == 0.0f ? (float)(rest - (double)by_hi) : 0.0f;
   const auto normalise = [&](f32x4v& v) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = (float)((double)v[e] * by);
+    for (int e = 0; e < 4; ++e) {
+      const float w = ldexpf(v[e], power);
+      v[e] = fmaf(w, by_hi, w * by_lo);
+    }
+  };
+  const auto normalise_t = [&] {
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      normalise(xt[b][0]);
+      normalise(xt[b][1]);
+    }
   };
 
   // X X^T: block (b, q), q <= b, of this wave's columns
@@ -785,11 +815,11 @@ __global__ __launch_bounds__(kSmallThreads) void k_small(Groups gs, uint32_t ste
     for (int t = 0; t < kPairs; ++t) gram[t] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
   };
   const auto add_to_gram = [&] {
-    f16x8 h[4], l[4];
+    f16x8 h[RB], l[RB];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) split8(xt[b][0], xt[b][1], h[b], l[b]);
+    for (int b = 0; b < RB; ++b) split8(xt[b][0], xt[b][1], h[b], l[b]);
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
+    for (int b = 0; b < RB; ++b)
 #pragma unroll
       for (int q = 0; q <= b; ++q)
         gram[b * (b + 1) / 2 + q] = multiply_parts(h[b], l[b], h[q], l[q], gram[b * (b + 1) / 2 + q]);
@@ -829,25 +859,35 @@ __global__ __launch_bounds__(kSmallThreads) void k_small(Groups gs, uint32_t ste
       for (uint32_t w = 1; w < waves; ++w) v += sums[(w * kPairs + t) * kWave + lane];
       uint32_t b, q;
       pair_at(t, b, q);
-      put_symmetric(sq[A], b * 16 + four, q * 16 + in, v * (1.0f / kScaleX));
+      put_symmetric(sq[kSqA], b * 16 + four, q * 16 + in, v * (1.0f / kScaleX));
     }
     __syncthreads();
   };
 
-  // d = alpha l r + beta r + gamma c2, all symmetric: a wave takes the blocks
-  // below the diagonal of (row bi, columns bj and bj + 1)
-  const uint32_t bi = wid / 2, bj = wid % 2 * 2;
+  // d = alpha l r + beta r + gamma c2, all symmetric: a wave takes the blocks on
+  // and below the diagonal of (row bi, columns bj and bj + 1). Each is computed
+  // both ways round, from the same operands and with the same roundings, so that
+  // a lane writes four values of a row at once: the mirror written from one of
+  // them, two bytes at a time, would take twice as long as all the rest.
+  const uint32_t bi = wid / SL, bj = wid % SL * 2;
   const auto square = [&](int l, int r, int c2, int d, float alpha, float beta, float gamma) {
     const uint32_t at = in * kRow + lane / 16 * 8;
-    const auto operand = [&](int of, int part, uint32_t blk, int s) {
-      return *reinterpret_cast<const f16x8*>(&sq[of][part][blk * 16 * kRow + at + s * 32]);
+    const auto operand = [&](int of, uint32_t blk, f16x8 (&h)[SL], f16x8 (&o)[SL]) {
+#pragma unroll
+      for (int s = 0; s < SL; ++s) {
+        h[s] = *reinterpret_cast<const f16x8*>(&sq[of][0][blk * 16 * kRow + at + s * 32]);
+        o[s] = *reinterpret_cast<const f16x8*>(&sq[of][1][blk * 16 * kRow + at + s * 32]);
+      }
     };
-    if (bj <= bi) {
-      f32x4v v[2];
+    if (bi < (uint32_t)RB && bj <= bi) {
+      f16x8 lh[SL], ll[SL];
+      operand(l, bi, lh, ll);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const uint32_t i = bi * 16 + four, j = (bj + q) * 16 + in, of = j * kRow + pos_of(i);
-        const auto get = [&](int m) {
+        if (bj + q > bi) break;
+        const uint32_t i = bi * 16, j = (bj + q) * 16;
+        const uint32_t down_at = (j + in) * kRow + pos_of(i + four), along_at = (i + in) * kRow + pos_of(j + four);
+        const auto get = [&](int m, uint32_t of) {
           const f16x4 h = *reinterpret_cast<const f16x4*>(&sq[m][0][of]);
           const f16x4 o4 = *reinterpret_cast<const f16x4*>(&sq[m][1][of]);
           f32x4v w;
@@ -855,30 +895,47 @@ __global__ __launch_bounds__(kSmallThreads) void k_small(Groups gs, uint32_t ste
           for (int e = 0; e < 4; ++e) w[e] = (float)h[e] + (float)o4[e];
           return w;
         };
-        v[q] = get(r) * beta;
-        if (gamma != 0.0f) v[q] += get(c2) * gamma;
-        f32x4v acc = {};
+        f16x8 rh[SL], rl[SL];
+        operand(r, bj + q, rh, rl);
+        f32x4v v = get(r, down_at) * beta, w = get(r, along_at) * beta;
+        if (gamma != 0.0f) {
+          v += get(c2, down_at) * gamma;
+          w += get(c2, along_at) * gamma;
+        }
+        f32x4v below = {}, above = {};  // rows i + four + e of column j + in, and row i + in's columns j + four + e
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-          acc = multiply_parts(operand(l, 0, bi, s), operand(l, 1, bi, s), operand(r, 0, bj + q, s),
-                               operand(r, 1, bj + q, s), acc);
-        v[q] += acc * alpha;
+        for (int s = 0; s < SL; ++s) {
+          below = __builtin_amdgcn_mfma_f32_16x16x32_f16(lh[s], rh[s], below, 0, 0, 0);
+          above = __builtin_amdgcn_mfma_f32_16x16x32_f16(rh[s], lh[s], above, 0, 0, 0);
+          below = __builtin_amdgcn_mfma_f32_16x16x32_f16(lh[s], rl[s], below, 0, 0, 0);
+          above = __builtin_amdgcn_mfma_f32_16x16x32_f16(rl[s], lh[s], above, 0, 0, 0);
+          below = __builtin_amdgcn_mfma_f32_16x16x32_f16(ll[s], rh[s], below, 0, 0, 0);
+          above = __builtin_amdgcn_mfma_f32_16x16x32_f16(rh[s], ll[s], above, 0, 0, 0);
+        }
+        v += below * alpha;
+        w += above * alpha;
+        if (i == j) {  // what lies above the diagonal from below it
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = in >= four + e ? w[e] : v[e];
+        }
+        f16x4 hi, lo;
+        if (i != j) {
+          split4(v, hi, lo);
+          *reinterpret_cast<f16x4*>(&sq[d][0][down_at]) = hi;
+          *reinterpret_cast<f16x4*>(&sq[d][1][down_at]) = lo;
+        }
+        split4(w, hi, lo);
+        *reinterpret_cast<f16x4*>(&sq[d][0][along_at]) = hi;
+        *reinterpret_cast<f16x4*>(&sq[d][1][along_at]) = lo;
       }
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-        if (bj + q <= bi) put_symmetric(sq[d], bi * 16 + four, (bj + q) * 16 + in, v[q]);
     }
     __syncthreads();
   };
 
   clear_gram();
   for (uint32_t blk = wid; blk < blocks; blk += kSmallWaves) {
-    fetch_t(blk);
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      normalise(xt[b][0]);
-      normalise(xt[b][1]);
-    }
+    if (!held) fetch_t(blk);
+    normalise_t();
     add_to_gram();
   }
   join_gram();
@@ -886,68 +943,64 @@ __global__ __launch_bounds__(kSmallThreads) void k_small(Groups gs, uint32_t ste
   for (uint32_t done = 0; done < steps; done += 2) {
     const bool pair = done + 1 < steps, last = done + 2 >= steps;
     // P - p0 I, P the product of the one or two steps' Q = a I + M
-    square(A, A, A, P0, c * to_m / kScaleX, b * to_m, 0.0f);
+    square(kSqA, kSqA, kSqA, kSqP, c * to_m / kScaleX, b * to_m, 0.0f);
     if (pair) {
-      square(P0, A, A, Q, 1.0f / kScaleM, a, 0.0f);
-      square(P0, Q, Q, A, 1.0f / kScaleM, a, 0.0f);
-      square(A, A, A, M, c * to_m / kScaleX, b * to_m, 0.0f);
-      square(M, P0, M, P1, 1.0f / kScaleM, a, a);
+      square(kSqP, kSqA, kSqA, kSqQ, 1.0f / kScaleM, a, 0.0f);
+      square(kSqP, kSqQ, kSqQ, kSqA, 1.0f / kScaleM, a, 0.0f);
+      square(kSqA, kSqA, kSqA, kSqM, c * to_m / kScaleX, b * to_m, 0.0f);
+      square(kSqM, kSqP, kSqM, kSqP2, 1.0f / kScaleM, a, a);
     }
     const float p0 = (pair ? a * a : a) * kScaleM;
-    f16x8 ph[4][2], pl[4][2];
-    {
-      const Part(&p)[2] = sq[pair ? P1 : P0];
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const uint32_t at = (b * 16 + in) * kRow + lane / 16 * 8 + s * 32;
-          ph[b][s] = *reinterpret_cast<const f16x8*>(&p[0][at]);
-          pl[b][s] = *reinterpret_cast<const f16x8*>(&p[1][at]);
-        }
-    }
+    const Part(&p)[2] = sq[pair ? kSqP2 : kSqP];
     clear_gram();
     for (uint32_t blk = wid; blk < blocks; blk += kSmallWaves) {
-      fetch_u(blk);
-      fetch_t(blk);
+      if (!held) {
+        fetch_u(blk);
+        fetch_t(blk);
+      }
       if (done == 0) {
+        if (!held) normalise_t();
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            normalise(xu[c][b]);
-            normalise(xt[b][c]);
-          }
+          for (int b = 0; b < RB; ++b) normalise(xu[c][b]);
       }
-      f16x8 h[2][2], l[2][2];
+      f16x8 h[2][SL], l[2][SL];
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) split8(xu[c][2 * s], xu[c][2 * s + 1], h[c][s], l[c][s]);
-      if (!last || tall) {
+        for (int s = 0; s < SL; ++s) split8(xu[c][2 * s], xu[c][2 * s + 1], h[c][s], l[c][s]);
+      uint32_t at = in * kRow + lane / 16 * 8;
+      asm volatile("" : "+v"(at));  // P is read for every block: its 64 registers are not there to hold it
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+      for (int b = 0; b < RB; ++b) {
+        f16x8 ph[SL], pl[SL];
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
+        for (int s = 0; s < SL; ++s) {
+          ph[s] = *reinterpret_cast<const f16x8*>(&p[0][at + b * 16 * kRow + s * 32]);
+          pl[s] = *reinterpret_cast<const f16x8*>(&p[1][at + b * 16 * kRow + s * 32]);
+        }
+        if (!last || tall) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
             f32x4v v = xu[c][b] * p0;
 #pragma unroll
-            for (int s = 0; s < 2; ++s) v = multiply_parts(ph[b][s], pl[b][s], h[c][s], l[c][s], v);
+            for (int s = 0; s < SL; ++s) v = multiply_parts(ph[s], pl[s], h[c][s], l[c][s], v);
             xu[c][b] = v * (1.0f / kScaleM);
           }
-      }
-      if (!last || !tall) {
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
+        }
+        if (!last || !tall) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             f32x4v v = xt[b][c] * p0;
 #pragma unroll
-            for (int s = 0; s < 2; ++s) v = multiply_parts(h[c][s], l[c][s], ph[b][s], pl[b][s], v);
+            for (int s = 0; s < SL; ++s) v = multiply_parts(h[c][s], l[c][s], ph[s], pl[s], v);
             xt[b][c] = v * (1.0f / kScaleM);
           }
+        }
       }
       if (!last) {
-        keep(blk);
+        if (!held) keep(blk);
         add_to_gram();
         continue;
       }
@@ -955,7 +1008,7 @@ __global__ __launch_bounds__(kSmallThreads) void k_small(Groups gs, uint32_t ste
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
+        for (int b = 0; b < RB; ++b) {
           const uint32_t i0 = b * 16, j0 = blk * 32 + c * 16;
           const uint32_t r = (tall ? j0 : i0) + in, col = (tall ? i0 : j0) + four;
           if (r >= g.rows) continue;
@@ -980,6 +1033,19 @@ __global__ __launch_bounds__(kSmallThreads) void k_small(Groups gs, uint32_t ste
     }
     if (!last) join_gram();
   }
+}
+
+template <int OUT, class S, class T>
+__global__ __launch_bounds__(kSmallThreads) void k_small(Groups gs, uint32_t steps, float a, float b, float c, float eps,
+                                                         const S* update, unsigned char* ws, T* out, Move mv) {
+  __shared__ SmallLds lds;
+  const Item it = item_of(gs, blockIdx.x);
+  const Group& g = gs.g[it.g];
+  if (it.k >= g.count) return;
+  const uint64_t at = g.at + it.k * (uint64_t)g.rows * g.cols;
+  f32x4v* kept = reinterpret_cast<f32x4v*>(ws + g.ws + it.k * g.ws_of);
+  if (min(g.rows, g.cols) <= 32) small_steps<2, OUT>(lds, g, steps, a, b, c, eps, update + at, kept, out + at, mv);
+  else small_steps<4, OUT>(lds, g, steps, a, b, c, eps, update + at, kept, out + at, mv);
 }
 
 // No steps: the normalised update itself.
