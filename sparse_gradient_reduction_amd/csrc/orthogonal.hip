@@ -641,11 +641,15 @@ __device__ __forceinline__ uint32_t pos_of(uint32_t k) {
   return (k & ~31u) | (k >> 2 & 3) << 3 | (k >> 4 & 1) << 2 | (k & 3);
 }
 
+// lo = v - hi in one instruction of mixed types, which the compiler takes for a
+// product and a sum but not for a difference: it does not get to know the -1.
 __device__ __forceinline__ void split4(f32x4v v, f16x4& hi, f16x4& lo) {
+  float minus = -1.0f;
+  asm("" : "+s"(minus));
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     hi[e] = (f16)v[e];
-    lo[e] = (f16)fmaf((float)hi[e], -1.0f, v[e]);  // one instruction
+    lo[e] = (f16)fmaf((float)hi[e], minus, v[e]);
   }
 }
 // Two of a result's blocks as an operand.
@@ -676,7 +680,8 @@ struct Blocks16 {
     if (inside) {
       typedef S S4 __attribute__((ext_vector_type(4)));
       typedef S4 S4u __attribute__((aligned(sizeof(S))));
-      const S4 w = *reinterpret_cast<const S4u*>(x + ((uint64_t)r0 * cols + c0) + (in * cols + four));
+      const S4 w = *reinterpret_cast<const S4u*>(reinterpret_cast<const char*>(x + ((uint64_t)r0 * cols + c0)) +
+                                                 (in * cols + four) * (uint32_t)sizeof(S));
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = to_f32((S)w[e]);
       return v;
@@ -692,7 +697,9 @@ struct Blocks16 {
     f32x4v v;
     if (inside) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = to_f32((x + ((uint64_t)(r0 + e) * cols + c0))[four * cols + in]);
+      for (int e = 0; e < 4; ++e)
+        v[e] = to_f32(*reinterpret_cast<const S*>(reinterpret_cast<const char*>(x + ((uint64_t)(r0 + e) * cols + c0)) +
+                                                  (four * cols + in) * (uint32_t)sizeof(S)));
       return v;
     }
     const uint32_t r = r0 + four, c = c0 + in;
@@ -732,29 +739,29 @@ __device__ __forceinline__ void small_steps(SmallLds& lds, const Group& g, uint3
   // A block of X: xu[c][b][e] at row 16 b + four + e, column 16 c + in;
   // xt[b][c][e] at row 16 b + in, column 16 c + four + e.
   f32x4v xu[2][RB], xt[RB][2];
+  const auto place = [&](uint32_t blk, int q) {  // a base that the wave shares, and a lane's offset
+    return reinterpret_cast<f32x4v*>(reinterpret_cast<char*>(kept) + ((uint64_t)blk * 16 + q) * 1024 + lane * 16);
+  };
   const auto keep = [&](uint32_t blk) {
-    f32x4v* p = kept + (uint64_t)blk * 16 * kWave;
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
       for (int b = 0; b < RB; ++b) {
-        p[(c * 4 + b) * kWave + lane] = xu[c][b];
-        p[(8 + b * 2 + c) * kWave + lane] = xt[b][c];
+        *place(blk, c * 4 + b) = xu[c][b];
+        *place(blk, 8 + b * 2 + c) = xt[b][c];
       }
   };
   const auto fetch_u = [&](uint32_t blk) {
-    const f32x4v* p = kept + (uint64_t)blk * 16 * kWave;
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int b = 0; b < RB; ++b) xu[c][b] = p[(c * 4 + b) * kWave + lane];
+      for (int b = 0; b < RB; ++b) xu[c][b] = *place(blk, c * 4 + b);
   };
   const auto fetch_t = [&](uint32_t blk) {
-    const f32x4v* p = kept + (uint64_t)blk * 16 * kWave;
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int b = 0; b < RB; ++b) xt[b][c] = p[(8 + b * 2 + c) * kWave + lane];
+      for (int b = 0; b < RB; ++b) xt[b][c] = *place(blk, 8 + b * 2 + c);
   };
 
   double sum = 0.0;
@@ -883,25 +890,18 @@ __device__ __forceinline__ void small_steps(SmallLds& lds, const Group& g, uint3
       f16x8 lh[SL], ll[SL];
       operand(l, bi, lh, ll);
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        if (bj + q > bi) break;
+      for (int q = 0; q < 2; ++q) {  // the second one may lie above the diagonal: computed, not stored
         const uint32_t i = bi * 16, j = (bj + q) * 16;
         const uint32_t down_at = (j + in) * kRow + pos_of(i + four), along_at = (i + in) * kRow + pos_of(j + four);
-        const auto get = [&](int m, uint32_t of) {
+        const auto add = [&](int m, uint32_t of, float by, f32x4v to) {
           const f16x4 h = *reinterpret_cast<const f16x4*>(&sq[m][0][of]);
           const f16x4 o4 = *reinterpret_cast<const f16x4*>(&sq[m][1][of]);
-          f32x4v w;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = (float)h[e] + (float)o4[e];
-          return w;
+          for (int e = 0; e < 4; ++e) to[e] = fmaf((float)h[e], by, fmaf((float)o4[e], by, to[e]));
+          return to;
         };
         f16x8 rh[SL], rl[SL];
         operand(r, bj + q, rh, rl);
-        f32x4v v = get(r, down_at) * beta, w = get(r, along_at) * beta;
-        if (gamma != 0.0f) {
-          v += get(c2, down_at) * gamma;
-          w += get(c2, along_at) * gamma;
-        }
         f32x4v below = {}, above = {};  // rows i + four + e of column j + in, and row i + in's columns j + four + e
 #pragma unroll
         for (int s = 0; s < SL; ++s) {
@@ -912,21 +912,26 @@ __device__ __forceinline__ void small_steps(SmallLds& lds, const Group& g, uint3
           below = __builtin_amdgcn_mfma_f32_16x16x32_f16(ll[s], rh[s], below, 0, 0, 0);
           above = __builtin_amdgcn_mfma_f32_16x16x32_f16(rh[s], ll[s], above, 0, 0, 0);
         }
-        v += below * alpha;
-        w += above * alpha;
+        f32x4v v = add(r, down_at, beta, below * alpha), w = add(r, along_at, beta, above * alpha);
+        if (gamma != 0.0f) {
+          v = add(c2, down_at, gamma, v);
+          w = add(c2, along_at, gamma, w);
+        }
         if (i == j) {  // what lies above the diagonal from below it
 #pragma unroll
           for (int e = 0; e < 4; ++e) w[e] = in >= four + e ? w[e] : v[e];
         }
-        f16x4 hi, lo;
-        if (i != j) {
-          split4(v, hi, lo);
-          *reinterpret_cast<f16x4*>(&sq[d][0][down_at]) = hi;
-          *reinterpret_cast<f16x4*>(&sq[d][1][down_at]) = lo;
+        f16x4 vh, vl, wh, wl;
+        split4(v, vh, vl);
+        split4(w, wh, wl);
+        if (j < i) {
+          *reinterpret_cast<f16x4*>(&sq[d][0][down_at]) = vh;
+          *reinterpret_cast<f16x4*>(&sq[d][1][down_at]) = vl;
         }
-        split4(w, hi, lo);
-        *reinterpret_cast<f16x4*>(&sq[d][0][along_at]) = hi;
-        *reinterpret_cast<f16x4*>(&sq[d][1][along_at]) = lo;
+        if (j <= i) {
+          *reinterpret_cast<f16x4*>(&sq[d][0][along_at]) = wh;
+          *reinterpret_cast<f16x4*>(&sq[d][1][along_at]) = wl;
+        }
       }
     }
     __syncthreads();
