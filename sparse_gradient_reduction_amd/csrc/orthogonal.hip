@@ -622,18 +622,18 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
 // order below the registers that hold a product's result are, once split into
 // parts, the operand of the next one. That needs X the way P X leaves it (a
 // lane holds rows of one column) for the next P X, and the way X^T P leaves it
-// (columns of one row) for X X^T. Both are computed from the same operands:
-// the second product is cheaper than turning the first one's result through
-// LDS, and a pass over X has no barrier but those of the last sum over the
-// waves.
+// (columns of one row) for X X^T. Both are computed from the same operands,
+// and a pass over X has no barrier but those of the last sum over the waves.
+// Between passes only the first is kept (a workgroup has 100 GB/s to memory,
+// which both would exhaust), in registers where a wave has one block only.
 constexpr int kSmallThreads = 512, kSmallWaves = kSmallThreads / kWave;
 constexpr uint32_t kSmallSide = 64, kSmallLong = 2048;
 constexpr int kRow = 72;  // fp16 of a row in LDS: sixteen rows' 16-byte chunks fall into different banks
 
 typedef float f32x4v __attribute__((ext_vector_type(4)));
 
-// Blocks of 32 columns, each 64 rows in both orders, fp32.
-__host__ __device__ __forceinline__ uint64_t small_bytes(uint32_t n) { return (uint64_t)up(n, 32) / 32 * 64 * 64 * sizeof(float); }
+// Blocks of 32 columns, each of 64 rows, fp32.
+__host__ __device__ __forceinline__ uint64_t small_bytes(uint32_t n) { return (uint64_t)up(n, 32) * 64 * sizeof(float); }
 
 // Where a row's k-th value lies: lane group g of 16 finds k = 4 g .. 4 g + 3 and
 // 16 more, as two blocks of a result hold them, in 16 bytes.
@@ -733,35 +733,24 @@ __device__ __forceinline__ void small_steps(SmallLds& lds, const Group& g, uint3
   const uint32_t m = tall ? g.cols : g.rows, n = tall ? g.rows : g.cols, blocks = (n + 31) / 32;
   const uint32_t lane = lane_id(), wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const uint32_t in = lane % 16, four = lane / 16 * 4;  // a result's block: this lane's column, and its rows from there
-  // a wave has one block at most: it stays in registers, where these are not short
-  const bool held = RB == 2 && blocks <= (uint32_t)kSmallWaves;
+  const bool held = blocks <= (uint32_t)kSmallWaves;  // a wave has one block at most: it stays in registers
 
-  // A block of X: xu[c][b][e] at row 16 b + four + e, column 16 c + in;
-  // xt[b][c][e] at row 16 b + in, column 16 c + four + e.
-  f32x4v xu[2][RB], xt[RB][2];
+  // A block of X: xu[c][b][e] at row 16 b + four + e, column 16 c + in.
+  f32x4v xu[2][RB];
   const auto place = [&](uint32_t blk, int q) {  // a base that the wave shares, and a lane's offset
-    return reinterpret_cast<f32x4v*>(reinterpret_cast<char*>(kept) + ((uint64_t)blk * 16 + q) * 1024 + lane * 16);
+    return reinterpret_cast<f32x4v*>(reinterpret_cast<char*>(kept) + ((uint64_t)blk * 8 + q) * 1024 + lane * 16);
   };
   const auto keep = [&](uint32_t blk) {
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int b = 0; b < RB; ++b) {
-        *place(blk, c * 4 + b) = xu[c][b];
-        *place(blk, 8 + b * 2 + c) = xt[b][c];
-      }
+      for (int b = 0; b < RB; ++b) *place(blk, c * 4 + b) = xu[c][b];
   };
-  const auto fetch_u = [&](uint32_t blk) {
+  const auto fetch = [&](uint32_t blk, f32x4v (&to)[2][RB]) {
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int b = 0; b < RB; ++b) xu[c][b] = *place(blk, c * 4 + b);
-  };
-  const auto fetch_t = [&](uint32_t blk) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int b = 0; b < RB; ++b) xt[b][c] = *place(blk, 8 + b * 2 + c);
+      for (int b = 0; b < RB; ++b) to[c][b] = *place(blk, c * 4 + b);
   };
 
   double sum = 0.0;
@@ -772,13 +761,7 @@ __device__ __forceinline__ void small_steps(SmallLds& lds, const Group& g, uint3
 #pragma unroll
       for (int b = 0; b < RB; ++b) {
         const uint32_t i0 = b * 16, j0 = blk * 32 + c * 16;
-        if (tall) {
-          xu[c][b] = from.along(j0, i0, inside());
-          xt[b][c] = from.down(j0, i0, inside());
-        } else {
-          xu[c][b] = from.down(i0, j0, inside());
-          xt[b][c] = from.along(i0, j0, inside());
-        }
+        xu[c][b] = tall ? from.along(j0, i0, inside()) : from.down(i0, j0, inside());
       }
   };
   for (uint32_t blk = wid; blk < blocks; blk += kSmallWaves) {
@@ -807,29 +790,39 @@ __device__ __forceinline__ void small_steps(SmallLds& lds, const Group& g, uint3
       v[e] = fmaf(w, by_hi, w * by_lo);
     }
   };
-  const auto normalise_t = [&] {
+  // A block's parts, h and l, are the operand of P X and X^T P. Against the unit
+  // matrix they give the block turned, exactly: columns 16 c + four + e of row
+  // 16 b + in.
+  f16x8 h[2][SL], l[2][SL], unit[2];
 #pragma unroll
-    for (int b = 0; b < RB; ++b) {
-      normalise(xt[b][0]);
-      normalise(xt[b][1]);
-    }
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int t = 0; t < 8; ++t) unit[b][t] = t / 4 == b && four + t % 4 == in ? (f16)1.0f : (f16)0.0f;
+  const auto split = [&] {
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int s = 0; s < SL; ++s) split8(xu[c][2 * s], xu[c][2 * s + 1], h[c][s], l[c][s]);
+  };
+  const auto turned = [&](int b, int c) {
+    f32x4v v = {};
+    v = __builtin_amdgcn_mfma_f32_16x16x32_f16(h[c][b / 2], unit[b % 2], v, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(l[c][b / 2], unit[b % 2], v, 0, 0, 0);
   };
 
-  // X X^T: block (b, q), q <= b, of this wave's columns
+  // X X^T: block (b, q), q <= b, of this wave's columns, from their turned parts
   f32x4v gram[kPairs];
+  f16x8 th[RB], tl[RB];
   const auto clear_gram = [&] {
 #pragma unroll
     for (int t = 0; t < kPairs; ++t) gram[t] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
   };
   const auto add_to_gram = [&] {
-    f16x8 h[RB], l[RB];
-#pragma unroll
-    for (int b = 0; b < RB; ++b) split8(xt[b][0], xt[b][1], h[b], l[b]);
 #pragma unroll
     for (int b = 0; b < RB; ++b)
 #pragma unroll
       for (int q = 0; q <= b; ++q)
-        gram[b * (b + 1) / 2 + q] = multiply_parts(h[b], l[b], h[q], l[q], gram[b * (b + 1) / 2 + q]);
+        gram[b * (b + 1) / 2 + q] = multiply_parts(th[b], tl[b], th[q], tl[q], gram[b * (b + 1) / 2 + q]);
   };
 
   // Rows i .. i + 3 of column j of a symmetric matrix, those on and below the
@@ -938,9 +931,23 @@ __device__ __forceinline__ void small_steps(SmallLds& lds, const Group& g, uint3
   };
 
   clear_gram();
+  f32x4v next[2][RB];
+  if (!held && wid < blocks) fetch(wid, next);
   for (uint32_t blk = wid; blk < blocks; blk += kSmallWaves) {
-    if (!held) fetch_t(blk);
-    normalise_t();
+    if (!held) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int b = 0; b < RB; ++b) xu[c][b] = next[c][b];
+      if (blk + kSmallWaves < blocks) fetch(blk + kSmallWaves, next);
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int b = 0; b < RB; ++b) normalise(xu[c][b]);
+    split();
+#pragma unroll
+    for (int b = 0; b < RB; ++b) split8(turned(b, 0), turned(b, 1), th[b], tl[b]);
     add_to_gram();
   }
   join_gram();
@@ -958,23 +965,22 @@ __device__ __forceinline__ void small_steps(SmallLds& lds, const Group& g, uint3
     const float p0 = (pair ? a * a : a) * kScaleM;
     const Part(&p)[2] = sq[pair ? kSqP2 : kSqP];
     clear_gram();
+    if (!held && wid < blocks) fetch(wid, next);
     for (uint32_t blk = wid; blk < blocks; blk += kSmallWaves) {
       if (!held) {
-        fetch_u(blk);
-        fetch_t(blk);
-      }
-      if (done == 0) {
-        if (!held) normalise_t();
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int b = 0; b < RB; ++b) normalise(xu[c][b]);
+          for (int b = 0; b < RB; ++b) xu[c][b] = next[c][b];
+        if (blk + kSmallWaves < blocks) fetch(blk + kSmallWaves, next);
+        if (done == 0) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int b = 0; b < RB; ++b) normalise(xu[c][b]);
+        }
       }
-      f16x8 h[2][SL], l[2][SL];
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int s = 0; s < SL; ++s) split8(xu[c][2 * s], xu[c][2 * s + 1], h[c][s], l[c][s]);
+      split();
       uint32_t at = in * kRow + lane / 16 * 8;
       asm volatile("" : "+v"(at));  // P is read for every block: its 64 registers are not there to hold it
 #pragma unroll
@@ -985,6 +991,16 @@ __device__ __forceinline__ void small_steps(SmallLds& lds, const Group& g, uint3
           ph[s] = *reinterpret_cast<const f16x8*>(&p[0][at + b * 16 * kRow + s * 32]);
           pl[s] = *reinterpret_cast<const f16x8*>(&p[1][at + b * 16 * kRow + s * 32]);
         }
+        f32x4v x_t[2];
+        if (!last || !tall) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            f32x4v v = turned(b, c) * p0;
+#pragma unroll
+            for (int s = 0; s < SL; ++s) v = multiply_parts(h[c][s], l[c][s], ph[s], pl[s], v);
+            x_t[c] = v * (1.0f / kScaleM);
+          }
+        }
         if (!last || tall) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -993,16 +1009,11 @@ __device__ __forceinline__ void small_steps(SmallLds& lds, const Group& g, uint3
             for (int s = 0; s < SL; ++s) v = multiply_parts(ph[s], pl[s], h[c][s], l[c][s], v);
             xu[c][b] = v * (1.0f / kScaleM);
           }
+        } else {
+          xu[0][b] = x_t[0];
+          xu[1][b] = x_t[1];
         }
-        if (!last || !tall) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            f32x4v v = xt[b][c] * p0;
-#pragma unroll
-            for (int s = 0; s < SL; ++s) v = multiply_parts(h[c][s], l[c][s], ph[s], pl[s], v);
-            xt[b][c] = v * (1.0f / kScaleM);
-          }
-        }
+        if (!last) split8(x_t[0], x_t[1], th[b], tl[b]);
       }
       if (!last) {
         if (!held) keep(blk);
@@ -1018,7 +1029,7 @@ __device__ __forceinline__ void small_steps(SmallLds& lds, const Group& g, uint3
           const uint32_t r = (tall ? j0 : i0) + in, col = (tall ? i0 : j0) + four;
           if (r >= g.rows) continue;
           T* at = o + (uint64_t)r * g.cols + col;
-          const f32x4v v = (tall ? xu[c][b] : xt[b][c]) * (1.0f / kScaleX);
+          const f32x4v v = xu[c][b] * (1.0f / kScaleX);
           typedef T T4 __attribute__((ext_vector_type(4)));
           typedef T4 T4u __attribute__((aligned(sizeof(T))));
           if (col + 4 <= g.cols) {
