@@ -818,11 +818,16 @@ __device__ __forceinline__ void small_steps(SmallLds& lds, const Group& g, uint3
     for (int t = 0; t < kPairs; ++t) gram[t] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
   };
   const auto add_to_gram = [&] {
+    // a part at a time: a product waits for the one before it in the same block
 #pragma unroll
-    for (int b = 0; b < RB; ++b)
+    for (int part = 0; part < 3; ++part)
 #pragma unroll
-      for (int q = 0; q <= b; ++q)
-        gram[b * (b + 1) / 2 + q] = multiply_parts(th[b], tl[b], th[q], tl[q], gram[b * (b + 1) / 2 + q]);
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int q = 0; q <= b; ++q) {
+          f32x4v& to = gram[b * (b + 1) / 2 + q];
+          to = __builtin_amdgcn_mfma_f32_16x16x32_f16(part == 2 ? tl[b] : th[b], part == 1 ? tl[q] : th[q], to, 0, 0, 0);
+        }
   };
 
   // Rows i .. i + 3 of column j of a symmetric matrix, those on and below the
@@ -964,6 +969,47 @@ __device__ __forceinline__ void small_steps(SmallLds& lds, const Group& g, uint3
     }
     const float p0 = (pair ? a * a : a) * kScaleM;
     const Part(&p)[2] = sq[pair ? kSqP2 : kSqP];
+    // P X in xu and X^T P, its columns 16 c + four + e of row 16 b + in, in xt
+    f32x4v xt[2][RB];
+    const auto move_block = [&](auto want_u, auto want_t) {
+      split();
+      uint32_t at = in * kRow + lane / 16 * 8;
+      asm volatile("" : "+v"(at));  // P is read for every block: its 64 registers are not there to hold it
+#pragma unroll
+      for (int b = 0; b < RB; ++b) {
+        f16x8 ph[SL], pl[SL];
+#pragma unroll
+        for (int s = 0; s < SL; ++s) {
+          ph[s] = *reinterpret_cast<const f16x8*>(&p[0][at + b * 16 * kRow + s * 32]);
+          pl[s] = *reinterpret_cast<const f16x8*>(&p[1][at + b * 16 * kRow + s * 32]);
+        }
+        f32x4v u[2], t[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          u[c] = xu[c][b] * p0;
+          if (want_t()) t[c] = turned(b, c) * p0;
+        }
+        // up to four chains of products side by side
+#pragma unroll
+        for (int s = 0; s < SL; ++s)
+#pragma unroll
+          for (int part = 0; part < 3; ++part)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const f16x8 of_p = part == 2 ? pl[s] : ph[s], of_x = part == 1 ? l[c][s] : h[c][s];
+              if (want_u()) u[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(of_p, of_x, u[c], 0, 0, 0);
+              if (want_t()) t[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(of_x, of_p, t[c], 0, 0, 0);
+            }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (want_u()) xu[c][b] = u[c] * (1.0f / kScaleM);
+          if (want_t()) xt[c][b] = t[c] * (1.0f / kScaleM);
+        }
+        if (want_u() && want_t()) split8(xt[0][b], xt[1][b], th[b], tl[b]);
+      }
+    };
+    constexpr std::true_type yes;
+    constexpr std::false_type no;
     clear_gram();
     if (!held && wid < blocks) fetch(wid, next);
     for (uint32_t blk = wid; blk < blocks; blk += kSmallWaves) {
@@ -980,46 +1026,14 @@ __device__ __forceinline__ void small_steps(SmallLds& lds, const Group& g, uint3
             for (int b = 0; b < RB; ++b) normalise(xu[c][b]);
         }
       }
-      split();
-      uint32_t at = in * kRow + lane / 16 * 8;
-      asm volatile("" : "+v"(at));  // P is read for every block: its 64 registers are not there to hold it
-#pragma unroll
-      for (int b = 0; b < RB; ++b) {
-        f16x8 ph[SL], pl[SL];
-#pragma unroll
-        for (int s = 0; s < SL; ++s) {
-          ph[s] = *reinterpret_cast<const f16x8*>(&p[0][at + b * 16 * kRow + s * 32]);
-          pl[s] = *reinterpret_cast<const f16x8*>(&p[1][at + b * 16 * kRow + s * 32]);
-        }
-        f32x4v x_t[2];
-        if (!last || !tall) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            f32x4v v = turned(b, c) * p0;
-#pragma unroll
-            for (int s = 0; s < SL; ++s) v = multiply_parts(h[c][s], l[c][s], ph[s], pl[s], v);
-            x_t[c] = v * (1.0f / kScaleM);
-          }
-        }
-        if (!last || tall) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            f32x4v v = xu[c][b] * p0;
-#pragma unroll
-            for (int s = 0; s < SL; ++s) v = multiply_parts(ph[s], pl[s], h[c][s], l[c][s], v);
-            xu[c][b] = v * (1.0f / kScaleM);
-          }
-        } else {
-          xu[0][b] = x_t[0];
-          xu[1][b] = x_t[1];
-        }
-        if (!last) split8(x_t[0], x_t[1], th[b], tl[b]);
-      }
       if (!last) {
+        move_block(yes, yes);
         if (!held) keep(blk);
         add_to_gram();
         continue;
       }
+      if (tall) move_block(yes, no);
+      else move_block(no, yes);
       const float move = mv.move * sqrtf(fmaxf(1.0f, (float)g.rows / (float)g.cols));
 #pragma unroll
       for (int c = 0; c < 2; ++c)
@@ -1029,7 +1043,7 @@ __device__ __forceinline__ void small_steps(SmallLds& lds, const Group& g, uint3
           const uint32_t r = (tall ? j0 : i0) + in, col = (tall ? i0 : j0) + four;
           if (r >= g.rows) continue;
           T* at = o + (uint64_t)r * g.cols + col;
-          const f32x4v v = xu[c][b] * (1.0f / kScaleX);
+          const f32x4v v = (tall ? xu[c][b] : xt[c][b]) * (1.0f / kScaleX);
           typedef T T4 __attribute__((ext_vector_type(4)));
           typedef T4 T4u __attribute__((aligned(sizeof(T))));
           if (col + 4 <= g.cols) {
