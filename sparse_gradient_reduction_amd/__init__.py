@@ -174,7 +174,7 @@ def _check_dev(t: torch.Tensor, dtype, name: str):
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None or t.numel() == 0 else t.data_ptr()
+    return None if t is None else t.data_ptr()  # 0 where there are no elements
 
 
 def _raise(status: int, what: str):

@@ -627,7 +627,7 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
 // Between passes only the first is kept (a workgroup has 100 GB/s to memory,
 // which both would exhaust), in registers where a wave has one block only.
 constexpr int kSmallThreads = 512, kSmallWaves = kSmallThreads / kWave;
-constexpr uint32_t kSmallSide = 64, kSmallLong = 2048;
+constexpr uint32_t kSmallSide = 64, kSmallLong = 2048, kSmallLong32 = 4096;
 constexpr int kRow = 72;  // fp16 of a row in LDS: sixteen rows' 16-byte chunks fall into different banks
 
 typedef float f32x4v __attribute__((ext_vector_type(4)));
@@ -1099,12 +1099,13 @@ __global__ __launch_bounds__(kThreads) void k_normalised(Groups gs, const S* upd
 }
 
 // The kinds of matrices: those that one workgroup takes through its steps, up
-// to where the chip's other CUs would be faster (64 x 2048 takes about as long
-// either way), and by the shorter side the narrow and the wide ones (plan_of).
+// to where the chip's other CUs are faster (64 x 2048: 122 us, against 130 by
+// products over all CUs; 16 x 4096: 100 against 170), and by the shorter side
+// the narrow and the wide ones (plan_of).
 enum Kind { kSmall, kNarrow, kWide, kKinds };
 Kind kind_of(uint32_t rows, uint32_t cols) {
   const uint32_t m = std::min(rows, cols), n = std::max(rows, cols);
-  return m <= kSmallSide && n <= kSmallLong ? kSmall : m <= 128 ? kNarrow : kWide;
+  return m <= kSmallSide && n <= (m <= 32 ? kSmallLong32 : kSmallLong) ? kSmall : m <= 128 ? kNarrow : kWide;
 }
 
 // Cuts the matrices of one kind into groups of equal ones that follow each
@@ -1171,6 +1172,11 @@ hipError_t launch_product(Groups& gs, const Product& p, unsigned char* ws, T* ou
     hipLaunchKernelGGL((k_product<S, OUT, T>), dim3(blocks), dim3(S::NT), 0, stream, gs, p, ws, out, mv);
     return hipGetLastError();
   };
+  // The larger the tile, the fewer bytes a product takes; the smaller, the more
+  // CUs share the work: large ones where they fill the chip (two matrices of
+  // 4096 x 4096), the 64 x 64 ones where all run at once, two to a CU (one
+  // matrix of 1000 x 1537, fp32 result: 241 us, against 441 with 128 x 128;
+  // six of 1024 x 1024, 816 such tiles: 667 against 625).
   return large >= 256 ? launch(Large{}) : tiny > 512 ? launch(Small{}) : launch(Tiny{});
 }
 
