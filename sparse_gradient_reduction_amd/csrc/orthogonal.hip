@@ -385,7 +385,24 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
     }
   }
 
-  f32x16 acc[S::TI][S::TJ] = {};
+  // Products of both parts add up 8 passes (256 of the summed index, 48 additions)
+  // at a time: in one chain of thousands of roundings an fp32 result of 196 x 8000
+  // is off by 7e-6 of its norm, not 2e-6. Tiles of 256 x 256 have no registers
+  // left for it; they are for sums of a large square matrix, whose own
+  // roundings weigh less.
+  constexpr bool STAGES = S::PARTS == 2 && S::BUFFERS > 2;
+  f32x16 acc[S::TI][S::TJ] = {}, total[STAGES ? S::TI : 1][STAGES ? S::TJ : 1] = {};
+  const auto stage = [&] {
+#pragma unroll
+    for (int x = 0; x < S::TI; ++x)
+#pragma unroll
+      for (int y = 0; y < S::TJ; ++y)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          total[x][y][e] += acc[x][y][e];
+          acc[x][y][e] = 0.0f;
+        }
+  };
   struct Parts {
     f16x8 a[S::PARTS][S::TI], b[S::PARTS][S::TJ];
   } f[2];
@@ -467,10 +484,21 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
       pass(lds0, lds1, lds2);
       pass(lds1, lds2, lds3);
       pass(lds2, lds3, lds0);
+      if constexpr (STAGES) {
+        if (k % 8 == 4) stage();
+      }
     }
     if (k < passes) pass(lds3, lds0, lds1);
     if (k + 1 < passes) pass(lds0, lds1, lds2);
     if (k + 2 < passes) pass(lds1, lds2, lds3);
+    if constexpr (STAGES) {
+#pragma unroll
+      for (int x = 0; x < S::TI; ++x)
+#pragma unroll
+        for (int y = 0; y < S::TJ; ++y)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[x][y][e] += total[x][y][e];
+    }
   }
 
 #pragma unroll
@@ -869,13 +897,13 @@ __device__ __forceinline__ void small_steps(SmallLds& lds, const Group& g, uint3
     __syncthreads();
   };
 
-  // d = alpha l r + beta r + gamma c2, all symmetric: a wave takes the blocks on
+  // d = alpha l r + beta r + diagonal I, all symmetric: a wave takes the blocks on
   // and below the diagonal of (row bi, columns bj and bj + 1). Each is computed
   // both ways round, from the same operands and with the same roundings, so that
   // a lane writes four values of a row at once: the mirror written from one of
   // them, two bytes at a time, would take twice as long as all the rest.
   const uint32_t bi = wid / SL, bj = wid % SL * 2;
-  const auto square = [&](int l, int r, int c2, int d, float alpha, float beta, float gamma) {
+  const auto square = [&](int l, int r, int d, float alpha, float beta, float diagonal) {
     const uint32_t at = in * kRow + lane / 16 * 8;
     const auto operand = [&](int of, uint32_t blk, f16x8 (&h)[SL], f16x8 (&o)[SL]) {
 #pragma unroll
@@ -910,14 +938,14 @@ __device__ __forceinline__ void small_steps(SmallLds& lds, const Group& g, uint3
           below = __builtin_amdgcn_mfma_f32_16x16x32_f16(ll[s], rh[s], below, 0, 0, 0);
           above = __builtin_amdgcn_mfma_f32_16x16x32_f16(rh[s], ll[s], above, 0, 0, 0);
         }
-        f32x4v v = add(r, down_at, beta, below * alpha), w = add(r, along_at, beta, above * alpha);
-        if (gamma != 0.0f) {
-          v = add(c2, down_at, gamma, v);
-          w = add(c2, along_at, gamma, w);
+        f32x4v v = below * alpha, w = above * alpha;
+        if (beta != 0.0f) {
+          v = add(r, down_at, beta, v);
+          w = add(r, along_at, beta, w);
         }
         if (i == j) {  // what lies above the diagonal from below it
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = in >= four + e ? w[e] : v[e];
+          for (int e = 0; e < 4; ++e) w[e] = in == four + e ? w[e] + diagonal : in > four + e ? w[e] : v[e];
         }
         f16x4 vh, vl, wh, wl;
         split4(v, vh, vl);
@@ -959,15 +987,14 @@ __device__ __forceinline__ void small_steps(SmallLds& lds, const Group& g, uint3
   const float to_m = kScaleM / kScaleX;
   for (uint32_t done = 0; done < steps; done += 2) {
     const bool pair = done + 1 < steps, last = done + 2 >= steps;
-    // P - p0 I, P the product of the one or two steps' Q = a I + M
-    square(kSqA, kSqA, kSqA, kSqP, c * to_m / kScaleX, b * to_m, 0.0f);
+    // P, the product of the one or two steps' Q = a I + b A + c A A
+    square(kSqA, kSqA, kSqP, c * to_m / kScaleX, b * to_m, a * kScaleM);
     if (pair) {
-      square(kSqP, kSqA, kSqA, kSqQ, 1.0f / kScaleM, a, 0.0f);
-      square(kSqP, kSqQ, kSqQ, kSqA, 1.0f / kScaleM, a, 0.0f);
-      square(kSqA, kSqA, kSqA, kSqM, c * to_m / kScaleX, b * to_m, 0.0f);
-      square(kSqM, kSqP, kSqM, kSqP2, 1.0f / kScaleM, a, a);
+      square(kSqP, kSqA, kSqQ, 1.0f / kScaleM, 0.0f, 0.0f);
+      square(kSqP, kSqQ, kSqA, 1.0f / kScaleM, 0.0f, 0.0f);
+      square(kSqA, kSqA, kSqM, c * to_m / kScaleX, b * to_m, a * kScaleM);
+      square(kSqM, kSqP, kSqP2, 1.0f / kScaleM, 0.0f, 0.0f);
     }
-    const float p0 = (pair ? a * a : a) * kScaleM;
     const Part(&p)[2] = sq[pair ? kSqP2 : kSqP];
     // P X in xu and X^T P, its columns 16 c + four + e of row 16 b + in, in xt
     f32x4v xt[2][RB];
@@ -983,12 +1010,7 @@ __device__ __forceinline__ void small_steps(SmallLds& lds, const Group& g, uint3
           ph[s] = *reinterpret_cast<const f16x8*>(&p[0][at + b * 16 * kRow + s * 32]);
           pl[s] = *reinterpret_cast<const f16x8*>(&p[1][at + b * 16 * kRow + s * 32]);
         }
-        f32x4v u[2], t[2];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          u[c] = xu[c][b] * p0;
-          if (want_t()) t[c] = turned(b, c) * p0;
-        }
+        f32x4v u[2] = {}, t[2] = {};
         // up to four chains of products side by side
 #pragma unroll
         for (int s = 0; s < SL; ++s)
