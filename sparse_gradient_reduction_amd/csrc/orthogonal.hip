@@ -688,12 +688,6 @@ __device__ __forceinline__ void split8(f32x4v u, f32x4v v, f16x8& hi, f16x8& lo)
   hi = __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7);
   lo = __builtin_shufflevector(l[0], l[1], 0, 1, 2, 3, 4, 5, 6, 7);
 }
-__device__ __forceinline__ f32x4v multiply_parts(f16x8 ah, f16x8 al, f16x8 bh, f16x8 bl, f32x4v acc) {
-  acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(ah, bh, acc, 0, 0, 0);
-  acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(ah, bl, acc, 0, 0, 0);
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(al, bh, acc, 0, 0, 0);
-}
-
 // Blocks of 16 x 16 of a row-major matrix from its first row r0 and column c0
 // on: `along` holds 4 columns of a row, `down` 4 rows of a column. Inside the
 // matrix the places are a base that the wave shares and a lane's offset; at its
@@ -846,16 +840,21 @@ __device__ __forceinline__ void small_steps(SmallLds& lds, const Group& g, uint3
     for (int t = 0; t < kPairs; ++t) gram[t] = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
   };
   const auto add_to_gram = [&] {
-    // a part at a time: a product waits for the one before it in the same block
+    // a part at a time: a product waits for the one before it in the same block;
+    // hi lo and lo hi first, whose sums' roundings are small
+    f32x4v t[kPairs];
 #pragma unroll
     for (int part = 0; part < 3; ++part)
 #pragma unroll
       for (int b = 0; b < RB; ++b)
 #pragma unroll
         for (int q = 0; q <= b; ++q) {
-          f32x4v& to = gram[b * (b + 1) / 2 + q];
-          to = __builtin_amdgcn_mfma_f32_16x16x32_f16(part == 2 ? tl[b] : th[b], part == 1 ? tl[q] : th[q], to, 0, 0, 0);
+          f32x4v& to = t[b * (b + 1) / 2 + q];
+          if (part == 0) to = f32x4v{0.0f, 0.0f, 0.0f, 0.0f};
+          to = __builtin_amdgcn_mfma_f32_16x16x32_f16(part == 1 ? tl[b] : th[b], part == 0 ? tl[q] : th[q], to, 0, 0, 0);
         }
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) gram[k] += t[k];
   };
 
   // Rows i .. i + 3 of column j of a symmetric matrix, those on and below the
@@ -930,14 +929,13 @@ __device__ __forceinline__ void small_steps(SmallLds& lds, const Group& g, uint3
         operand(r, bj + q, rh, rl);
         f32x4v below = {}, above = {};  // rows i + four + e of column j + in, and row i + in's columns j + four + e
 #pragma unroll
-        for (int s = 0; s < SL; ++s) {
-          below = __builtin_amdgcn_mfma_f32_16x16x32_f16(lh[s], rh[s], below, 0, 0, 0);
-          above = __builtin_amdgcn_mfma_f32_16x16x32_f16(rh[s], lh[s], above, 0, 0, 0);
-          below = __builtin_amdgcn_mfma_f32_16x16x32_f16(lh[s], rl[s], below, 0, 0, 0);
-          above = __builtin_amdgcn_mfma_f32_16x16x32_f16(rl[s], lh[s], above, 0, 0, 0);
-          below = __builtin_amdgcn_mfma_f32_16x16x32_f16(ll[s], rh[s], below, 0, 0, 0);
-          above = __builtin_amdgcn_mfma_f32_16x16x32_f16(rh[s], ll[s], above, 0, 0, 0);
-        }
+        for (int part = 0; part < 3; ++part)  // hi hi last, as above
+#pragma unroll
+          for (int s = 0; s < SL; ++s) {
+            const f16x8 of_l = part == 1 ? ll[s] : lh[s], of_r = part == 0 ? rl[s] : rh[s];
+            below = __builtin_amdgcn_mfma_f32_16x16x32_f16(of_l, of_r, below, 0, 0, 0);
+            above = __builtin_amdgcn_mfma_f32_16x16x32_f16(of_r, of_l, above, 0, 0, 0);
+          }
         f32x4v v = below * alpha, w = above * alpha;
         if (beta != 0.0f) {
           v = add(r, down_at, beta, v);
@@ -1013,12 +1011,12 @@ __device__ __forceinline__ void small_steps(SmallLds& lds, const Group& g, uint3
         f32x4v u[2] = {}, t[2] = {};
         // up to four chains of products side by side
 #pragma unroll
-        for (int s = 0; s < SL; ++s)
+        for (int part = 0; part < 3; ++part)
 #pragma unroll
-          for (int part = 0; part < 3; ++part)
+          for (int s = 0; s < SL; ++s)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const f16x8 of_p = part == 2 ? pl[s] : ph[s], of_x = part == 1 ? l[c][s] : h[c][s];
+              const f16x8 of_p = part == 1 ? pl[s] : ph[s], of_x = part == 0 ? l[c][s] : h[c][s];
               if (want_u()) u[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(of_p, of_x, u[c], 0, 0, 0);
               if (want_t()) t[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(of_x, of_p, t[c], 0, 0, 0);
             }
