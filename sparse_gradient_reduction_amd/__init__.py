@@ -825,6 +825,8 @@ def _matrices(matrices):
     """Host arrays of [(position, rows, cols)], in ascending order."""
     n = len(matrices)
     at, rows, cols = zip(*matrices) if n else ((), (), ())
+    if n and (min(at) < 0 or min(min(rows), min(cols)) < 0 or max(max(rows), max(cols)) >= 1 << 32):
+        raise ValueError("positions must not be negative, rows and columns must lie in [0, 2^32)")
     return n, (ctypes.c_uint64 * n)(*at), (ctypes.c_uint32 * n)(*rows), (ctypes.c_uint32 * n)(*cols)
 
 

@@ -52,6 +52,31 @@ def test_one_matrix(dev, rows, cols, t):
     _check(sg.orthogonalize(u, where, dtype=t), u, where, t)
 
 
+BORDERS = [(32, 32), (33, 33), (32, 257), (32, 4096), (32, 4097), (17, 256), (16, 8), (48, 289), (64, 256), (64, 2048),
+           (64, 2049), (63, 1000), (1, 300), (300, 1), (130, 4100)]
+
+
+@pytest.mark.parametrize("turn", [False, True])
+@pytest.mark.parametrize("rows,cols", BORDERS)
+def test_borders_of_the_kinds(dev, rows, cols, turn):
+    """Short sides around 16, 32 and 64, long ones around a workgroup's reach; wide and tall."""
+    if turn:
+        rows, cols = cols, rows
+    u, where = _update([(rows, cols)] * 2, rows + 7 * cols)
+    u = u.to(dev)
+    _check(sg.orthogonalize(u, where), u, where, torch.float32)
+    _check(sg.orthogonalize(u.bfloat16(), where), u.bfloat16(), where, torch.bfloat16)
+
+
+def test_long_sums(dev):
+    """fp32 results keep their accuracy over sums of thousands of terms, one
+    side's and several matrices' together (tiles of 64 and of 128)."""
+    for shapes in ([(100, 9000)], [(1300, 2100)], [(700, 900)] * 4):
+        u, where = _update(shapes, len(shapes))
+        u = u.to(dev)
+        _check(sg.orthogonalize(u, where), u, where[:1], torch.float32)
+
+
 @pytest.mark.parametrize("source", TYPES, ids=str)
 @pytest.mark.parametrize("gap", [0, 1, 5])
 def test_several_matrices(dev, source, gap):

@@ -128,6 +128,13 @@ def test_python_checks():
         sg.orthogonal_step(v, v, [(0, 2, 4)], lr=0.1)
 
 
+@pytest.mark.parametrize("wrong", [(-1, 2, 4), (0, -2, 4), (0, 2, 1 << 32), (0, (1 << 32) + 2, 4)])
+def test_matrices_out_of_range(wrong):
+    """Numbers that a C integer would wrap are refused before the call."""
+    with pytest.raises(ValueError):
+        sg.orthogonalize_workspace_bytes(1 << 20, [wrong])
+
+
 @pytest.mark.gpu
 def test_python_checks_on_the_gpu(dev):
     x = torch.zeros(4, 8, device=dev)
