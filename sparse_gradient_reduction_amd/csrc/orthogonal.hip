@@ -1181,9 +1181,10 @@ hipError_t launch_product(Groups& gs, const Product& p, unsigned char* ws, T* ou
   using Large = Shape<2, 4, 4, 2, PARTS, 2>;  // 256 x 256, 8 waves
   using Small = Shape<2, 2, 2, 2, PARTS, 4>;  // 128 x 128, 4 waves
   using Tiny = Shape<2, 2, 1, 1, PARTS, 4>;   // 64 x 64, 4 waves
-  uint64_t large = 0, tiny = 0;
+  uint64_t large = 0, small = 0, tiny = 0;
   for (uint32_t k = 0; k < gs.count; ++k) {
     large += (uint64_t)gs.g[k].count * product_tiles<Large>(gs.g[k], p);
+    small += (uint64_t)gs.g[k].count * product_tiles<Small>(gs.g[k], p);
     tiny += (uint64_t)gs.g[k].count * product_tiles<Tiny>(gs.g[k], p);
   }
   const auto launch = [&](auto shape) {
@@ -1193,11 +1194,16 @@ hipError_t launch_product(Groups& gs, const Product& p, unsigned char* ws, T* ou
     return hipGetLastError();
   };
   // The larger the tile, the fewer bytes a product takes; the smaller, the more
-  // CUs share the work: large ones where they fill the chip (two matrices of
-  // 4096 x 4096), the 64 x 64 ones where all run at once, two to a CU (one
-  // matrix of 1000 x 1537, fp32 result: 241 us, against 441 with 128 x 128;
-  // six of 1024 x 1024, 816 such tiles: 667 against 625).
-  return large >= 256 ? launch(Large{}) : tiny > 512 ? launch(Small{}) : launch(Tiny{});
+  // CUs share the work. 64 x 64 tiles where all run at once, two to a CU (one
+  // matrix of 1000 x 1537, fp32 result: 241 us, against 441 with 128 x 128; six
+  // of 1024 x 1024, 816 such tiles: 667 against 625). Else by turns of the 256
+  // CUs: a 256 x 256 tile does the work of four of 128 x 128 in 1 / 1.2 of the
+  // time (12 of 2048 x 2048, 8 turns' worth each: 6.4 ms against 7.4), but 273
+  // of them take two turns where 975 smaller ones take four (three matrices of
+  // 3085 x 6855: 11.5 ms against 9.4).
+  const auto turns = [](uint64_t tiles) { return (tiles + 255) / 256; };
+  if (tiny <= 512) return launch(Tiny{});
+  return 4 * turns(large) * 10 <= turns(small) * 12 ? launch(Large{}) : launch(Small{});
 }
 
 // `steps` steps taken as one: with A = X X^T, Q = a I + M, M = b A + c A A,
