@@ -661,7 +661,8 @@ def _type(dtype, name: str) -> int:
 def _row_stride(t: torch.Tensor, like: torch.Tensor, name: str) -> int:
     """Elements from one row to the next of `t`, a GPU tensor of `like`'s shape
     and type whose rows (the last dimension) are contiguous and evenly spaced."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != like.dtype or t.shape != like.shape:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or (t is not like and (t.dtype != like.dtype or
+                                                                               t.shape != like.shape)):
         raise TypeError(f"{name} must be a {like.dtype} tensor of shape {tuple(like.shape)} on a GPU")
     if t.is_contiguous():
         return t.shape[-1]
@@ -721,8 +722,11 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     _vector(bias, cols, "bias")
     dev = x.device
     y = _given(y, x, "y")
-    mean = _given(mean, x, "mean", x.shape[:-1], torch.float32)
-    rstd = _given(rstd, x, "rstd", x.shape[:-1], torch.float32)
+    if mean is None and rstd is None:  # one allocation
+        mean, rstd = x.new_empty((2,) + x.shape[:-1], dtype=torch.float32).unbind()
+    else:
+        mean = _given(mean, x, "mean", x.shape[:-1], torch.float32)
+        rstd = _given(rstd, x, "rstd", x.shape[:-1], torch.float32)
     if residual is not None:
         total = _given(total, x, "total")
     elif total is not None:
@@ -776,8 +780,12 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
         raise ValueError(f"mean and rstd must have {rows} elements")
     dev = x.device
     dx = _given(dx, x, "dx")
-    dweight, ws = _node_rows(dweight, nodes, cols, x, "dweight")
-    dbias, bs = _node_rows(dbias, nodes, cols, x, "dbias")
+    if dweight is None and dbias is None:  # one allocation
+        dweight, dbias = x.new_empty((2, nodes, cols), dtype=torch.float32).unbind()
+        ws = bs = cols
+    else:
+        dweight, ws = _node_rows(dweight, nodes, cols, x, "dweight")
+        dbias, bs = _node_rows(dbias, nodes, cols, x, "dbias")
     L = _load()
     if workspace is None:
         need = L.sparcml_layer_norm_backward_workspace(nodes, rows // nodes, cols)

@@ -1324,7 +1324,8 @@ hipError_t run(Groups& gs, Kind kind, const OrthoSteps& s, uint32_t type, const 
     // symmetric: D = alpha * A B + beta * B + gamma * C2, read by products of `inner` parts
     const auto square = [&](uint32_t parts, uint32_t a, uint32_t b, uint32_t c2, uint32_t d, float alpha, float beta,
                             float gamma) {
-      planes(parts, Product{a, b, b, c2, d, d, 1, 1, mix, mix, mix, alpha, beta, gamma});
+      // Single products read lo parts as C only, which lies above the diagonal.
+      planes(parts, Product{a, b, b, c2, d, d, 1, mix, mix, mix, mix, alpha, beta, gamma});
     };
     square(blk.gram, x, x, x, kA, 1.0f / kScaleX, 0.0f, 0.0f);
     uint32_t mm = kP, pp = kP;  // the step's M; P - p0 I
