@@ -359,22 +359,34 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
   const auto outside = [&](int x, int y) {  // blocks of 32 lie inside or outside
     return i0 + wi + x * 32 >= m || j0 + wj + y * 32 >= J;
   };
+  // A lane loads 16 bytes of a column, the halves of the wave different eights
+  // of its 32 rows, and they swap fours when these are used: half the loads of
+  // 8 bytes each.
   struct Columns {
-    f16x4 hi[S::TI][4], lo[S::TI][4];
+    f16x8 hi[S::TI][2], lo[S::TI][2];
   };
   const auto load_c = [&](const Plane& c, int y, Columns& to) {
     to = Columns{};
-    const uint32_t j = j0 + wj + y * 32 + lane % 32, i = i0 + wi + lane / 32 * 4, to_lo = c.to_lo(p.mix_c);
+    const uint32_t j = j0 + wj + y * 32 + lane % 32, i = i0 + wi + lane / 32 * 16, to_lo = c.to_lo(p.mix_c);
 #pragma unroll
     for (int x = 0; x < S::TI; ++x)
       if (!outside(x, y)) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 2; ++q) {
           const f16* at = c.hi(j, i + x * 32 + q * 8, p.mix_c);
-          to.hi[x][q] = *reinterpret_cast<const f16x4*>(at);
-          to.lo[x][q] = *reinterpret_cast<const f16x4*>(at + to_lo);
+          to.hi[x][q] = *reinterpret_cast<const f16x8*>(at);
+          to.lo[x][q] = *reinterpret_cast<const f16x8*>(at + to_lo);
         }
       }
+  };
+  // rows 8 q + 4 (lane / 32) + e of eights q and q + 2
+  const auto fours = [&](f16x8 eight, f16x4 (&to)[4], int q) {
+    const u32x4 w = __builtin_bit_cast(u32x4, eight);
+    const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    to[q] = __builtin_bit_cast(f16x4, u32x2{a[0], b[0]});
+    to[q + 2] = __builtin_bit_cast(f16x4, u32x2{a[1], b[1]});
   };
   Columns ahead[2][AHEAD ? S::TJ : 1];
   if constexpr (AHEAD) {
@@ -514,10 +526,17 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
       if constexpr (AHEAD) c = ahead[which][y];
       else load_c(plane(base, m, n, buffer), y, c);
 #pragma unroll
-      for (int x = 0; x < S::TI; ++x)
+      for (int x = 0; x < S::TI; ++x) {
+        f16x4 hi[4], lo[4];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          fours(c.hi[x][q], hi, q);
+          fours(c.lo[x][q], lo, q);
+        }
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          acc[x][y][e] = fmaf(by, (float)c.hi[x][e / 4][e % 4] + (float)c.lo[x][e / 4][e % 4], acc[x][y][e]);
+          acc[x][y][e] = fmaf(by, (float)hi[e / 4][e % 4] + (float)lo[e / 4][e % 4], acc[x][y][e]);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
