@@ -1011,8 +1011,10 @@ __device__ __forceinline__ void small_steps(SmallLds& lds, const Group& g, uint3
   }
   join_gram();
   const float to_m = kScaleM / kScaleX;
-  for (uint32_t done = 0; done < steps; done += 2) {
-    const bool pair = done + 1 < steps, last = done + 2 >= steps;
+  // The smallest matrices take as long one step at a time, and come out nearer.
+  const uint32_t together = RB == 2 && held ? 1 : 2;
+  for (uint32_t done = 0; done < steps; done += together) {
+    const bool pair = together == 2 && done + 1 < steps, last = done + together >= steps;
     // P, the product of the one or two steps' Q = a I + b A + c A A
     square(kSqA, kSqA, kSqP, c * to_m / kScaleX, b * to_m, a * kScaleM);
     if (pair) {
