@@ -683,7 +683,7 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
 // keep step. 16 x 27 takes 14 us, 64 x 576 48 us, and 20 matrices of 16 x 16 ..
 // 64 x 576 take 54 us, as long as the largest one.
 constexpr int kSmallThreads = 512, kSmallWaves = kSmallThreads / kWave;
-constexpr uint32_t kSmallSide = 64, kSmallLong = 2048, kSmallLong32 = 4096;
+constexpr uint32_t kSmallSide = 64, kSmallLong = 2048, kSmallLong32 = 16384;
 constexpr int kRow = 72;  // fp16 of a row in LDS: sixteen rows' 16-byte chunks fall into different banks
 
 typedef float f32x4v __attribute__((ext_vector_type(4)));
@@ -1150,7 +1150,7 @@ __global__ __launch_bounds__(kThreads) void k_normalised(Groups gs, const S* upd
 
 // The kinds of matrices: those that one workgroup takes through its steps, up
 // to where the chip's other CUs are faster (64 x 2048: 122 us, against 130 by
-// products over all CUs; 16 x 4096: 100 against 170), and by the shorter side
+// products over all CUs; 16 x 16384: 347 against 489), and by the shorter side
 // the narrow and the wide ones (plan_of).
 enum Kind { kSmall, kNarrow, kWide, kKinds };
 Kind kind_of(uint32_t rows, uint32_t cols) {
