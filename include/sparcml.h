@@ -595,10 +595,11 @@ sparcml_status sparcml_momentum_step(uint64_t N, const sparcml_reduce_result* d_
  * sparcml_orthogonalize_workspace returns 0 for arguments the calls reject.
  *
  * The products run on the matrix cores, two fp16 parts to a value and fp32
- * sums: an fp32 result is about as near to the formula as with fp32 products
- * (0.5e-6 .. 2.5e-6 of its norm). For 16-bit results the early steps take
- * single fp16 products where the later ones wear their error off; it stays
- * below the rounding to the type. The
+ * sums, whatever the types: before a 16-bit result's one rounding to its type
+ * it is about as near to the formula as with fp32 products, off by 0.5e-6 ..
+ * 4e-6 of its norm and by up to 2e-5 where a few directions hold nearly all of
+ * an update, since the steps amplify the others' roundings (there fp32 products
+ * leave as much). The
  * iterates are held in parts of a power of two of their size, which leaves
  * room for entries of X up to 15 (they stay below 1.3 with the usual
  * coefficients 3.4445, -4.7750, 2.0315); beyond it the matrix becomes NaN. A

@@ -34,7 +34,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr uint32_t kPad = 64;        // sides are padded with zeros to this
 constexpr uint32_t kGroups = 24;     // groups of equal matrices in one set of launches
-constexpr uint32_t kMaxSteps = 64;
 constexpr uint32_t kParts = 1024;    // partial sums of squares of one matrix, at most
 constexpr float kScaleX = 4096.0f;   // of X, X^T, A
 constexpr float kScaleM = 256.0f;    // of M
@@ -64,22 +63,19 @@ struct Groups {
 
 // A matrix's buffers: partial sums, then X, X^T, the next X and X^T, and the
 // square ones: A, the step's M, Q A, and the product of the steps' Q (two).
-// A row of `ld` values holds 2 * ld fp16. What single products read is stored
-// as the hi parts, then the lo parts; what products of both parts read is mixed,
-// 32 hi, 32 lo and so on: either way 128 bytes of a row are a pass's operands
-// (64 bytes at a time, memory gives a workgroup 59 GB/s instead of 100).
+// A row of `ld` values holds 2 * ld fp16: 32 hi, 32 lo and so on, so that 128
+// bytes of a row are a pass's operands (64 bytes at a time, memory gives a
+// workgroup 59 GB/s instead of 100).
 enum Buffer : uint32_t { kX0, kXT0, kX1, kXT1, kA, kM, kT, kP, kP2, kBuffers };
 
 struct Plane {
   f16* p;
   uint32_t ld;
   __device__ __forceinline__ f16* row(uint64_t r) const { return p + r * 2 * ld; }
-  // element e's hi part, and from there to its lo part
-  __device__ __forceinline__ f16* hi(uint64_t r, uint32_t e, bool mixed) const {
-    return row(r) + e + (mixed ? e / 32 * 32 : 0);
-  }
-  __device__ __forceinline__ uint32_t to_lo(bool mixed) const { return mixed ? 32 : ld; }
+  // element e's hi part; its lo part is kToLo further on
+  __device__ __forceinline__ f16* hi(uint64_t r, uint32_t e) const { return row(r) + e + e / 32 * 32; }
 };
+constexpr uint32_t kToLo = 32;
 __host__ __device__ __forceinline__ uint64_t buffers_bytes(uint32_t m, uint32_t n) {
   return kParts * sizeof(double) + 4ull * (4ull * m * n + (uint64_t)(kBuffers - kA) * m * m);
 }
@@ -142,8 +138,8 @@ __global__ __launch_bounds__(kThreads) void k_squares(Groups gs, const T* update
   if (threadIdx.x == 0) reinterpret_cast<double*>(ws + g.ws + it.k * g.ws_of)[it.tile] = s;
 }
 
-// 16 values to a row's elements e .. e + 15 as hi and lo parts (to_lo 0: hi alone).
-__device__ __forceinline__ void store_parts(const float (&v)[16], f16* hi, uint32_t to_lo) {
+// 16 values to a row's elements e .. e + 15 as hi and lo parts.
+__device__ __forceinline__ void store_parts(const float (&v)[16], f16* hi) {
   f16x8 h[2], l[2];
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
@@ -153,16 +149,14 @@ __device__ __forceinline__ void store_parts(const float (&v)[16], f16* hi, uint3
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     reinterpret_cast<f16x8*>(hi)[q] = h[q];
-    if (to_lo) reinterpret_cast<f16x8*>(hi + to_lo)[q] = l[q];
+    reinterpret_cast<f16x8*>(hi + kToLo)[q] = l[q];
   }
 }
 
 // X0 and its transpose, one 64 x 64 tile of the padded matrix; a thread takes
-// 16 elements of a row, then 16 of a row of the transpose. mix_x, mix_xt: how
-// they are stored; lo_x: whether X's lo parts are wanted (X^T's always are).
+// 16 elements of a row, then 16 of a row of the transpose.
 template <class T>
-__global__ __launch_bounds__(kThreads) void k_split(Groups gs, const T* update, float eps, bool mix_x, bool mix_xt,
-                                                    bool lo_x, unsigned char* ws) {
+__global__ __launch_bounds__(kThreads) void k_split(Groups gs, const T* update, float eps, unsigned char* ws) {
   __shared__ float t[64][65];
   __shared__ double scratch[kThreads / kWave];
   const Item it = item_of(gs, blockIdx.x);
@@ -193,12 +187,11 @@ __global__ __launch_bounds__(kThreads) void k_split(Groups gs, const T* update, 
   // as stored: the wide X if rows <= cols, else X^T
   const bool tall = g.tall();
   const Plane same = plane(base, g.m(), g.n(), tall ? kXT0 : kX0), turned = plane(base, g.m(), g.n(), tall ? kX0 : kXT0);
-  const bool mix_same = tall ? mix_xt : mix_x, mix_turned = tall ? mix_x : mix_xt;
-  store_parts(v, same.hi(r, c, mix_same), tall || lo_x ? same.to_lo(mix_same) : 0);
+  store_parts(v, same.hi(r, c));
   __syncthreads();
 #pragma unroll
   for (int e = 0; e < 16; ++e) v[e] = t[seg + e][row];
-  store_parts(v, turned.hi(c0 + row, r0 + seg, mix_turned), !tall || lo_x ? turned.to_lo(mix_turned) : 0);
+  store_parts(v, turned.hi(c0 + row, r0 + seg));
 }
 
 // One product of every matrix: D = alpha * A B^T + beta * C + gamma * C2 in stored units.
@@ -208,8 +201,6 @@ struct Product {
   uint32_t c_ji, c2;    // C, stored [j][i]; C2, symmetric
   uint32_t d_ij, d_ji;  // D in both orders (planes only)
   uint32_t sym;         // D symmetric: what lies above the diagonal is the mirror of what lies below
-  uint32_t lo_ij;       // the lo parts are wanted in the order [i][j] too
-  uint32_t mix_c, mix_ij, mix_ji;  // C and C2, D in either order: mixed
   float alpha, beta, gamma;
 };
 enum Out { kPlanes, kResult, kWeight };
@@ -282,13 +273,12 @@ __device__ __forceinline__ void wait_and_meet() {
 }
 
 // The shape of a workgroup's tile: WI x WJ waves, each TI x TJ blocks of
-// 32 x 32, the parts of its operands (2 multiplies hi and lo, three products,
-// 1 hi alone) and the LDS buffers.
-template <int WI_, int WJ_, int TI_, int TJ_, int PARTS_, int BUFFERS_>
+// 32 x 32, and the LDS buffers.
+template <int WI_, int WJ_, int TI_, int TJ_, int BUFFERS_>
 struct Shape {
-  static constexpr int WI = WI_, WJ = WJ_, TI = TI_, TJ = TJ_, PARTS = PARTS_, BUFFERS = BUFFERS_;
+  static constexpr int WI = WI_, WJ = WJ_, TI = TI_, TJ = TJ_, BUFFERS = BUFFERS_;
   static constexpr int W = WI * WJ, NT = W * kWave, I = WI * TI * 32, J = WJ * TJ * 32;
-  static constexpr int DEPTH = 64 / PARTS;  // summed index of a pass: rows of 128 bytes
+  static constexpr int DEPTH = 32;  // summed index of a pass: rows of 128 bytes, hi and lo
   static constexpr int SIZE = (I + J) * 8;
   static constexpr int PITCH = 36;  // of a block of 32 x 32 that a wave turns
   static constexpr int FIRST = SIZE > W * 32 * PITCH / 4 ? SIZE : W * 32 * PITCH / 4;  // the first buffer: the turned blocks too
@@ -341,15 +331,12 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
     const uint32_t r = ((t < LA ? t : t - LA) * S::W + wid) * 8 + lane / 8;
     src[t] = (min(r, (t < LA ? m - i0 : J - j0) - 1) * 2 * K + from) * sizeof(f16);
   }
-  const auto load = [&](f16x8* lds, auto first, auto last) {  // loads [first, last) of a pass
+  const auto load = [&](f16x8* lds) {  // of a pass
 #pragma unroll
-    for (int t = first(); t < last(); ++t)
-      load_to_lds((t < LA ? pa : pb) + src[t], lds + (t * S::W + wid) * kWave);
-    if constexpr (last() == LN) {
-      pa += 128;
-      pb += 128;
-      asm("" : "+s"(pa), "+s"(pb));  // stays a scalar base and 32-bit offsets
-    }
+    for (int t = 0; t < LN; ++t) load_to_lds((t < LA ? pa : pb) + src[t], lds + (t * S::W + wid) * kWave);
+    pa += 128;
+    pb += 128;
+    asm("" : "+s"(pa), "+s"(pb));  // stays a scalar base and 32-bit offsets
   };
 
   // C and C2, 32 columns at a time. A tile of few registers loads them ahead of
@@ -367,15 +354,15 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
   };
   const auto load_c = [&](const Plane& c, int y, Columns& to) {
     to = Columns{};
-    const uint32_t j = j0 + wj + y * 32 + lane % 32, i = i0 + wi + lane / 32 * 16, to_lo = c.to_lo(p.mix_c);
+    const uint32_t j = j0 + wj + y * 32 + lane % 32, i = i0 + wi + lane / 32 * 16;
 #pragma unroll
     for (int x = 0; x < S::TI; ++x)
       if (!outside(x, y)) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const f16* at = c.hi(j, i + x * 32 + q * 8, p.mix_c);
+          const f16* at = c.hi(j, i + x * 32 + q * 8);
           to.hi[x][q] = *reinterpret_cast<const f16x8*>(at);
-          to.lo[x][q] = *reinterpret_cast<const f16x8*>(at + to_lo);
+          to.lo[x][q] = *reinterpret_cast<const f16x8*>(at + kToLo);
         }
       }
   };
@@ -397,12 +384,11 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
     }
   }
 
-  // Products of both parts add up 8 passes (256 of the summed index, 48 additions)
-  // at a time: in one chain of thousands of roundings an fp32 result of 196 x 8000
+  // The sums add up 8 passes (256 of the summed index, 48 additions) at a time: in one chain of thousands of roundings an fp32 result of 196 x 8000
   // is off by 7e-6 of its norm, not 2e-6. Tiles of 256 x 256 have no registers
   // left for it; they are for sums of a large square matrix, whose own
   // roundings weigh less.
-  constexpr bool STAGES = S::PARTS == 2 && S::BUFFERS > 2;
+  constexpr bool STAGES = S::BUFFERS > 2;
   f32x16 acc[S::TI][S::TJ] = {}, total[STAGES ? S::TI : 1][STAGES ? S::TJ : 1] = {};
   const auto stage = [&] {
 #pragma unroll
@@ -416,12 +402,11 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
         }
   };
   struct Parts {
-    f16x8 a[S::PARTS][S::TI], b[S::PARTS][S::TJ];
+    f16x8 a[2][S::TI], b[2][S::TJ];  // hi and lo of 16 of a pass's 32: its first half in f[0], its second in f[1]
   } f[2];
-  constexpr int KS = S::DEPTH / 16;  // parts of a pass; even, so that a pass starts with f[0]
   const auto read = [&](const f16x8* lds, int ks, Parts& to) {
 #pragma unroll
-    for (int h = 0; h < S::PARTS; ++h) {
+    for (int h = 0; h < 2; ++h) {
       const uint32_t c = (ks * 2 + h * 4 + lane / 32) ^ lane / 2 % 8;
 #pragma unroll
       for (int q = 0; q < S::TI; ++q) to.a[h][q] = lds[(wi + q * 32 + lane % 32) * 8 + c];
@@ -435,74 +420,63 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
 #pragma unroll
       for (int y = 0; y < S::TJ; ++y) {
         acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(by.a[0][x], by.b[0][y], acc[x][y], 0, 0, 0);
-        if constexpr (S::PARTS == 2) {
-          acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(by.a[0][x], by.b[1][y], acc[x][y], 0, 0, 0);
-          acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(by.a[1][x], by.b[0][y], acc[x][y], 0, 0, 0);
-        }
+        acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(by.a[0][x], by.b[1][y], acc[x][y], 0, 0, 0);
+        acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(by.a[1][x], by.b[0][y], acc[x][y], 0, 0, 0);
       }
   };
 
-  // The operands of a part of a pass are read while the part before it is
+  // The operands of half a pass are read while the half before it is
   // multiplied. So at a pass's barrier all of its operands are in registers:
-  // its buffer is free for the pass BUFFERS later, and the last part is
+  // its buffer is free for the pass BUFFERS later, and the second half is
   // multiplied behind the barrier, while the next pass's first operands arrive.
   // The barrier waits for the next pass's loads only. The loads are spread
   // between the multiplications: issued at once, a pass's 64 hold the waves up
   // for a thousand cycles. Passes past the last load what follows in the
   // workspace, and nothing reads it.
-  constexpr int NM = S::TI * S::TJ * (S::PARTS == 2 ? 3 : 1), ND = S::PARTS * (S::TI + S::TJ);
-  constexpr int LH = S::PARTS == 2 ? LN : LN / 2;  // loads behind the barrier; the others with the next part
-  constexpr std::integral_constant<int, 0> l0;
-  constexpr std::integral_constant<int, LH> l1;
-  constexpr std::integral_constant<int, LN> l2;
+  constexpr int NM = S::TI * S::TJ * 3, ND = 2 * (S::TI + S::TJ);
   const uint32_t passes = K / S::DEPTH;
-  const auto pass = [&](f16x8* before, f16x8* now, const f16x8* next) {
-#pragma unroll
-    for (int ks = 0; ks + 1 < KS; ++ks) {
-      read(now, ks + 1, f[(ks + 1) % 2]);
-      if (ks == 0 && LH < LN) load(before, l1, l2);
-      multiply(f[ks % 2]);
-      if (ks == 0) Spread<0, NM, LN - LH, ND>::over();
-      else Spread<0, NM, 0, ND>::over();
-      __builtin_amdgcn_sched_barrier(0);
-    }
+  const auto pass = [&](f16x8* now, const f16x8* next) {
+    read(now, 1, f[1]);
+    multiply(f[0]);
+    Spread<0, NM, 0, ND>::over();
+    __builtin_amdgcn_sched_barrier(0);
     wait_and_meet<(S::BUFFERS - 2) * LN>();
-    load(now, l0, l1);
+    load(now);
     read(next, 0, f[0]);
     multiply(f[1]);
-    Spread<0, NM, LH, ND>::over();
+    Spread<0, NM, LN, ND>::over();
     __builtin_amdgcn_sched_barrier(0);
   };
-  load(lds0, l0, l2);
+  load(lds0);
   if constexpr (S::BUFFERS == 2) {
-    load(lds1, l0, l1);
-    wait_and_meet<LH>();
+    load(lds1);
+    wait_and_meet<LN>();
     read(lds0, 0, f[0]);
     uint32_t k = 0;
     for (; k + 2 <= passes; k += 2) {
-      pass(lds1, lds0, lds1);
-      pass(lds0, lds1, lds0);
+      pass(lds0, lds1);
+      pass(lds1, lds0);
     }
-    if (k < passes) pass(lds1, lds0, lds1);
+    if (k < passes) pass(lds0, lds1);
   } else {
-    load(lds1, l0, l2);
-    load(lds2, l0, l2);
-    load(lds3, l0, l1);
-    wait_and_meet<2 * LN + LH>();
+    load(lds1);
+    load(lds2);
+    load(lds3);
+    wait_and_meet<3 * LN>();
     read(lds0, 0, f[0]);
     uint32_t k = 0;
     for (; k + 4 <= passes; k += 4) {
-      pass(lds3, lds0, lds1);
-      pass(lds0, lds1, lds2);
-      pass(lds1, lds2, lds3);
-      pass(lds2, lds3, lds0);
+      pass(lds0, lds1);
+      pass(lds1, lds2);
+      pass(lds2, lds3);
+      pass(lds3, lds0);
       if constexpr (STAGES) {
         if (k % 8 == 4) stage();
       }
     }
-    if (k < passes) pass(lds3, lds0, lds1);
-    if (k + 1 < passes) pass(lds0, lds1, lds2);
-    if (k + 2 < passes) pass(lds1, lds2, lds3);
+    if (k < passes) pass(lds0, lds1);
+    if (k + 1 < passes) pass(lds1, lds2);
+    if (k + 2 < passes) pass(lds2, lds3);
     if constexpr (STAGES) {
 #pragma unroll
       for (int x = 0; x < S::TI; ++x)
@@ -556,7 +530,7 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
   const uint32_t* across = turn + half * PITCH + row;
   if constexpr (OUT == kPlanes) {
     const Plane dij = plane(base, m, n, p.d_ij), dji = plane(base, m, n, p.d_ji);
-    const auto store = [&](const uint32_t (&w)[16], f16* hi, uint32_t to_lo) {  // 0: hi alone
+    const auto store = [&](const uint32_t (&w)[16], f16* hi) {
       f16x8 h[2], l[2];
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
@@ -566,7 +540,7 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         reinterpret_cast<f16x8*>(hi)[q] = h[q];
-        if (to_lo) reinterpret_cast<f16x8*>(hi + to_lo)[q] = l[q];
+        reinterpret_cast<f16x8*>(hi + kToLo)[q] = l[q];
       }
     };
 #pragma unroll
@@ -598,11 +572,11 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
 #pragma unroll
           for (int e = 0; e < 16; ++e) w[e] = half + e >= row ? w[e] : across[e * PITCH];
         }
-        store(w, dji.hi(jx + row, ix + half, p.mix_ji), dji.to_lo(p.mix_ji));
+        store(w, dji.hi(jx + row, ix + half));
         if (!(p.sym && ix == jx)) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) w[e] = across[e * PITCH];
-          store(w, dij.hi(ix + row, jx + half, p.mix_ij), p.lo_ij ? dij.to_lo(p.mix_ij) : 0);
+          store(w, dij.hi(ix + row, jx + half));
         }
         wave_fence();  // before the next block's values
         __builtin_amdgcn_sched_barrier(0);
@@ -1151,7 +1125,7 @@ __global__ __launch_bounds__(kThreads) void k_normalised(Groups gs, const S* upd
 // The kinds of matrices: those that one workgroup takes through its steps, up
 // to where the chip's other CUs are faster (64 x 2048: 122 us, against 130 by
 // products over all CUs; 16 x 16384: 347 against 489), and by the shorter side
-// the narrow and the wide ones (plan_of).
+// the narrow and the wide ones, whose steps are paired or not on their own.
 enum Kind { kSmall, kNarrow, kWide, kKinds };
 Kind kind_of(uint32_t rows, uint32_t cols) {
   const uint32_t m = std::min(rows, cols), n = std::max(rows, cols);
@@ -1206,11 +1180,11 @@ uint32_t product_tiles(const Group& g, const Product& p) {
   return tiles_of((g.m() + S::I - 1) / S::I, ((p.sym ? g.m() : g.n()) + S::J - 1) / S::J, p.sym);
 }
 
-template <int PARTS, int OUT, class T>
+template <int OUT, class T>
 hipError_t launch_product(Groups& gs, const Product& p, unsigned char* ws, T* out, Move mv, hipStream_t stream) {
-  using Large = Shape<2, 4, 4, 2, PARTS, 2>;  // 256 x 256, 8 waves
-  using Small = Shape<2, 2, 2, 2, PARTS, 4>;  // 128 x 128, 4 waves
-  using Tiny = Shape<2, 2, 1, 1, PARTS, 4>;   // 64 x 64, 4 waves
+  using Large = Shape<2, 4, 4, 2, 2>;  // 256 x 256, 8 waves
+  using Small = Shape<2, 2, 2, 2, 4>;  // 128 x 128, 4 waves
+  using Tiny = Shape<2, 2, 1, 1, 4>;   // 64 x 64, 4 waves
   uint64_t large = 0, small = 0, tiny = 0;
   for (uint32_t k = 0; k < gs.count; ++k) {
     large += (uint64_t)gs.g[k].count * product_tiles<Large>(gs.g[k], p);
@@ -1236,72 +1210,37 @@ hipError_t launch_product(Groups& gs, const Product& p, unsigned char* ws, T* ou
   return 4 * turns(large) * 10 <= turns(small) * 12 ? launch(Large{}) : launch(Small{});
 }
 
-// `steps` steps taken as one: with A = X X^T, Q = a I + M, M = b A + c A A,
+// One step, or two taken as one: with A = X X^T, Q = a I + M, M = b A + c A A,
 // the next step's A is Q A Q = Q (Q A) (they commute, so both products are
-// symmetric) and X moves once, by the product P of the Q. Beyond one step that
-// trades two of X's products (3 m m n) for three halves more of m x m ones.
-// gram, inner, move: parts (1 or 2) of the operands of X X^T, of the m x m
-// products and of P X; inner == move, as P is read by both.
-struct Block {
-  uint32_t steps, gram, inner, move;
-};
-struct Plan {
-  Block b[kMaxSteps];
-  uint32_t count = 0;
-  void add(uint32_t times, Block x) {
-    for (; times > 0; --times) b[count++] = x;
-  }
-};
-
-// What the result's type asks for. fp32: two parts everywhere. 16 bits: the
-// error of a product of single fp16 values (2^-12 of it) in an early step is
-// worn off, because the later steps move every singular value towards the same
-// one: over matrices of 128 to 1024 the last two steps alone account for nearly
-// all of it. So fp16 results take two parts in the last two steps (three where
-// they are taken as one) and bf16 results in the last one but for its A: the
-// result is off by 1e-5 .. 2e-4 and 2e-4 .. 9e-4 of its norm, against 2.1e-4
-// and 1.7e-3 by the rounding to the type itself; narrower matrices (up to 128),
-// where it would be more and costs little, take two parts always.
-// Two steps taken as one keep fp32's accuracy (4e-7 .. 1.2e-6 of the norm); at
-// three (2e-6 .. 6e-6, enough for fp16) A's small singular values begin to be
-// lost beside its large ones.
-// `paired`: steps taken together.
-Plan plan_of(uint32_t steps, uint32_t type, Kind kind, bool paired) {
-  const Block one{1, 1, 1, 1}, two{2, 1, 1, 1}, exact{1, 2, 2, 2};
-  Plan p;
-  if (kind != kWide || type == SPARCML_F32) {
-    if (paired) p.add(steps / 2, Block{2, 2, 2, 2});
-    p.add(paired ? steps % 2 : steps, exact);
-    return p;
-  }
-  const bool bf16 = type == SPARCML_BF16;
-  const uint32_t tail = std::min(steps, bf16 ? 1u : paired ? 3u : 2u), head = steps - tail;
-  p.add(paired ? head % 2 : head, one);
-  if (paired) p.add(head / 2, two);
-  if (bf16) p.add(tail, Block{1, 1, 2, 2});
-  else if (paired) p.add(1, Block{tail, 2, 2, 2});
-  else p.add(tail, exact);
-  return p;
-}
-
-// Operations of a plan, and what its launches cost in operations: about 5 us
-// each at 5e14 a second.
-double plan_cost(const Plan& p, const Groups& gs) {
-  const auto times = [](uint32_t parts) { return parts == 2 ? 3.0 : 1.0; };
+// symmetric) and X moves once, by the product of the two Q. That trades two of
+// X's products (3 m m n) for three halves more of m x m ones and keeps the
+// accuracy (fp32 results: 4e-7 .. 1.2e-6 of the norm); at three (2e-6 .. 6e-6)
+// A's small singular values begin to be lost beside its large ones.
+//
+// Every product takes both parts of its operands, whatever the result's type.
+// The error that single fp16 products (a third of the multiplications) leave in
+// a step is a matter of the spectrum: with two of five steps in both parts it
+// was 8e-4 of the norm for noise, 1.5e-3 for noise thinned to 0.5%, 4e-5 for
+// noise with a few strong directions, where fp16's rounding is 2.1e-4; four of
+// five still left 1.5e-4 where rows differ in size.
+//
+// Operations of `steps` steps with or without pairs, and what their launches
+// cost in operations: about 5 us each at 5e14 a second.
+double steps_cost(uint32_t steps, bool paired, const Groups& gs) {
   double all = 0.0;
-  for (uint32_t k = 0; k < p.count; ++k) {
-    const Block& b = p.b[k];
+  for (uint32_t done = 0; done < steps; done += paired ? 2 : 1) {
+    const double squares = paired && done + 1 < steps ? 5 : 1;
     for (uint32_t j = 0; j < gs.count; ++j) {
       const double m = gs.g[j].m(), n = gs.g[j].n();
-      all += gs.g[j].count * m * m * (n * (times(b.gram) + 2 * times(b.move)) + m * times(b.inner) * (4 * b.steps - 3));
+      all += gs.g[j].count * 3 * m * m * (3 * n + squares * m);
     }
-    all += 2.5e9 * (2 + 4 * b.steps - 3);
+    all += 2.5e9 * (2 + squares);
   }
   return all;
 }
 
 template <int OUT, class S, class T>
-hipError_t run(Groups& gs, Kind kind, const OrthoSteps& s, uint32_t type, const S* update, T* out, Move mv,
+hipError_t run(Groups& gs, Kind kind, const OrthoSteps& s, const S* update, T* out, Move mv,
                unsigned char* ws, hipStream_t stream) {
   if (kind == kSmall && s.steps > 0) {
     const uint32_t blocks = tiled(gs, [](const Group&) { return 1u; });
@@ -1320,58 +1259,40 @@ hipError_t run(Groups& gs, Kind kind, const OrthoSteps& s, uint32_t type, const 
                        mv);
     return hipGetLastError();
   }
-  const Plan alone = plan_of(s.steps, type, kind, false), paired = plan_of(s.steps, type, kind, true);
-  const Plan& plan = plan_cost(paired, gs) < plan_cost(alone, gs) ? paired : alone;
+  const bool paired = steps_cost(s.steps, true, gs) < steps_cost(s.steps, false, gs);
   blocks = tiled(gs, [](const Group& g) { return g.m() / 64 * (g.n() / 64); });
-  hipLaunchKernelGGL(k_split<S>, dim3(blocks), dim3(kThreads), 0, stream, gs, update, s.eps, plan.b[0].gram == 2,
-                     plan.b[0].move == 2, plan.b[0].gram == 2, ws);
+  hipLaunchKernelGGL(k_split<S>, dim3(blocks), dim3(kThreads), 0, stream, gs, update, s.eps, ws);
   e = hipGetLastError();
 
-  const auto planes = [&](uint32_t parts, const Product& p) {
-    if (e != hipSuccess) return;
-    e = parts == 2 ? launch_product<2, kPlanes, float>(gs, p, ws, nullptr, mv, stream)
-                   : launch_product<1, kPlanes, float>(gs, p, ws, nullptr, mv, stream);
-  };
-  const auto result = [&](uint32_t parts, const Product& p) {
-    if (e != hipSuccess) return;
-    e = parts == 2 ? launch_product<2, OUT, T>(gs, p, ws, out, mv, stream)
-                   : launch_product<1, OUT, T>(gs, p, ws, out, mv, stream);
+  // symmetric: D = alpha * A B + beta * B + gamma * C2
+  const auto square = [&](uint32_t a, uint32_t b, uint32_t c2, uint32_t d, float alpha, float beta, float gamma) {
+    if (e == hipSuccess)
+      e = launch_product<kPlanes, float>(gs, Product{a, b, b, c2, d, d, 1, alpha, beta, gamma}, ws, nullptr, mv, stream);
   };
   const float to_m = kScaleM / kScaleX;
-  for (uint32_t k = 0; k < plan.count; ++k) {
-    const Block& blk = plan.b[k];
-    const uint32_t x = k % 2 ? kX1 : kX0, y = k % 2 ? kX0 : kX1;  // this block's X and the next
-    const uint32_t mix = blk.inner == 2;
-    // symmetric: D = alpha * A B + beta * B + gamma * C2, read by products of `inner` parts
-    const auto square = [&](uint32_t parts, uint32_t a, uint32_t b, uint32_t c2, uint32_t d, float alpha, float beta,
-                            float gamma) {
-      // Single products read lo parts as C only, which lies above the diagonal.
-      planes(parts, Product{a, b, b, c2, d, d, 1, mix, mix, mix, mix, alpha, beta, gamma});
-    };
-    square(blk.gram, x, x, x, kA, 1.0f / kScaleX, 0.0f, 0.0f);
-    uint32_t mm = kP, pp = kP;  // the step's M; P - p0 I
+  uint32_t x = kX0, y = kX1;  // X and the next
+  for (uint32_t done = 0; done < s.steps;) {
+    square(x, x, x, kA, 1.0f / kScaleX, 0.0f, 0.0f);
+    square(kA, kA, kA, kP, s.c * to_m / kScaleX, s.b * to_m, 0.0f);
+    uint32_t pp = kP;  // P - p0 I
     float p0 = s.a;
-    for (uint32_t j = 0; j < blk.steps; ++j) {
-      if (j > 0) {  // the next step's A
-        square(blk.inner, mm, kA, kA, kT, 1.0f / kScaleM, s.a, 0.0f);
-        square(blk.inner, mm, kT, kT, kA, 1.0f / kScaleM, s.a, 0.0f);
-        mm = kM;
-      }
-      square(blk.inner, kA, kA, kA, mm, s.c * to_m / kScaleX, s.b * to_m, 0.0f);
-      if (j > 0) {  // (a I + M) (p0 I + P)
-        const uint32_t next = pp == kP ? kP2 : kP;
-        square(blk.inner, mm, pp, mm, next, 1.0f / kScaleM, s.a, p0);
-        pp = next;
-        p0 *= s.a;
-      }
+    ++done;
+    if (paired && done < s.steps) {
+      square(kP, kA, kA, kT, 1.0f / kScaleM, s.a, 0.0f);
+      square(kP, kT, kT, kA, 1.0f / kScaleM, s.a, 0.0f);  // the next step's A
+      square(kA, kA, kA, kM, s.c * to_m / kScaleX, s.b * to_m, 0.0f);
+      square(kM, kP, kM, kP2, 1.0f / kScaleM, s.a, p0);  // (a I + M) (p0 I + P)
+      pp = kP2;
+      p0 *= s.a;
+      ++done;
     }
-    const bool last = k + 1 == plan.count;
+    const bool last = done == s.steps;
     const float unit = last ? 1.0f / kScaleX : 1.0f;
-    const uint32_t gram = last ? 1 : plan.b[k + 1].gram, move = last ? 1 : plan.b[k + 1].move;  // what reads X, X^T
-    const Product px{pp, x + 1, x + 1, x, y, y + 1, 0, gram == 2, blk.move == 2, gram == 2, move == 2,
-                     unit / kScaleM, unit * p0, 0.0f};
-    if (last) result(blk.move, px);
-    else planes(blk.move, px);
+    const Product px{pp, x + 1, x + 1, x, y, y + 1, 0, unit / kScaleM, unit * p0, 0.0f};
+    if (e == hipSuccess)
+      e = last ? launch_product<OUT, T>(gs, px, ws, out, mv, stream)
+               : launch_product<kPlanes, float>(gs, px, ws, nullptr, mv, stream);
+    std::swap(x, y);
   }
   return e;
 }
@@ -1405,8 +1326,8 @@ hipError_t ortho_launch(const OrthoMatrices& ms, const OrthoSteps& steps, uint32
           using T = decltype(t);
           unsigned char* w = static_cast<unsigned char*>(ws);
           return is_weight
-                     ? run<kWeight, S, T>(gs, (Kind)kind, steps, out_type, (const S*)update, (T*)out, mv, w, stream)
-                     : run<kResult, S, T>(gs, (Kind)kind, steps, out_type, (const S*)update, (T*)out, mv, w, stream);
+                     ? run<kWeight, S, T>(gs, (Kind)kind, steps, (const S*)update, (T*)out, mv, w, stream)
+                     : run<kResult, S, T>(gs, (Kind)kind, steps, (const S*)update, (T*)out, mv, w, stream);
         });
       });
     });
