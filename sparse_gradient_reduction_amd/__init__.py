@@ -688,6 +688,14 @@ def _vector(t: Optional[torch.Tensor], n: int, name: str):
             raise ValueError(f"{name} must have {n} elements")
 
 
+def _workspace(t: Optional[torch.Tensor], need: int, like: torch.Tensor) -> torch.Tensor:
+    """The caller's workspace, or a new one on `like`'s device."""
+    if t is None:
+        return like.new_empty(need, dtype=torch.uint8)
+    _check_dev(t, torch.uint8, "workspace")
+    return t
+
+
 def _given(t: Optional[torch.Tensor], like: torch.Tensor, name: str, shape=None, dtype=None) -> torch.Tensor:
     """The caller's output, or a new one, contiguous, on `like`'s device; of
     its shape and type where none are given."""
@@ -787,9 +795,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
         dweight, ws = _node_rows(dweight, nodes, cols, x, "dweight")
         dbias, bs = _node_rows(dbias, nodes, cols, x, "dbias")
     L = _load()
-    if workspace is None:
-        need = L.sparcml_layer_norm_backward_workspace(nodes, rows // nodes, cols)
-        workspace = x.new_empty(need, dtype=torch.uint8)
+    workspace = _workspace(workspace, L.sparcml_layer_norm_backward_workspace(nodes, rows // nodes, cols), x)
     st = L.sparcml_layer_norm_backward(t, nodes, rows // nodes, cols, _ptr(dy), ds, _ptr(x), xs, _ptr(dresidual), rs,
                                        _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(dweight), ws,
                                        _ptr(dbias), bs, _ptr(workspace), workspace.numel(), _stream(dev))
@@ -861,15 +867,13 @@ def orthogonalize(update: torch.Tensor, matrices, dtype: Optional[torch.dtype] =
     dev = update.device
     args = _matrices(matrices)
     L = _load()
-    need = L.sparcml_orthogonalize_workspace(N, *args)
+    workspace = _workspace(workspace, L.sparcml_orthogonalize_workspace(N, *args), update)
     if out is None:
         whole = sum(m[1] * m[2] for m in matrices) == N
         out = (torch.empty_like if whole else torch.zeros_like)(update, dtype=dtype)
     okind = _flat(out, "out")
     if out.numel() != N or (dtype is not None and out.dtype != dtype):
         raise ValueError(f"out must hold {N} elements of the dtype asked for")
-    if workspace is None:
-        workspace = update.new_empty(need, dtype=torch.uint8)
     st = L.sparcml_orthogonalize(N, *args, steps, *coefficients, eps, kind, _ptr(update), okind, _ptr(out),
                                  _ptr(workspace), workspace.numel(), _stream(dev))
     _raise(st, "sparcml_orthogonalize")
@@ -888,9 +892,7 @@ def orthogonal_step(weight: torch.Tensor, update: torch.Tensor, matrices, lr: fl
         raise ValueError(f"weight must hold {N} elements")
     args = _matrices(matrices)
     L = _load()
-    if workspace is None:
-        need = L.sparcml_orthogonalize_workspace(N, *args)
-        workspace = weight.new_empty(need, dtype=torch.uint8)
+    workspace = _workspace(workspace, L.sparcml_orthogonalize_workspace(N, *args), weight)
     st = L.sparcml_orthogonal_step(N, *args, steps, *coefficients, eps, kind, _ptr(update), wkind, _ptr(weight), lr,
                                    weight_decay, _ptr(workspace), workspace.numel(), _stream(weight.device))
     _raise(st, "sparcml_orthogonal_step")
