@@ -658,6 +658,15 @@ def _type(dtype, name: str) -> int:
     return t
 
 
+def _row_length(x: torch.Tensor) -> int:
+    if not isinstance(x, torch.Tensor) or x.dim() == 0:
+        raise TypeError("x must be a tensor of rows")
+    cols = x.shape[-1]
+    if cols >= 1 << 31:  # more than 2^32 would wrap in the call
+        raise ValueError("x's rows must be shorter than 2^31")
+    return cols
+
+
 def _row_stride(t: torch.Tensor, like: torch.Tensor, name: str) -> int:
     """Elements from one row to the next of `t`, a GPU tensor of `like`'s shape
     and type whose rows (the last dimension) are contiguous and evenly spaced."""
@@ -719,11 +728,9 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     be slices of a wider buffer), with fp32 `weight` and `bias`. Returns (y,
     mean, rstd), mean and rstd fp32 of x.shape[:-1]; with `residual`, x +
     residual is what is normed, and (y, mean, rstd, total) come back with that sum."""
-    if not isinstance(x, torch.Tensor) or x.dim() == 0:
-        raise TypeError("x must be a tensor of rows")
+    cols = _row_length(x)
     t = _type(x.dtype, "x")
     xs = _row_stride(x, x, "x")
-    cols = x.shape[-1]
     rows = x.numel() // cols if cols else 0
     rs = 0 if residual is None else _row_stride(residual, x, "residual")
     _vector(weight, cols, "weight")
@@ -746,6 +753,8 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
 
 
 def layer_norm_backward_workspace_bytes(nodes: int, rows: int, cols: int) -> int:
+    if not 0 <= nodes < 1 << 32 or not 0 <= rows < 1 << 64 or not 0 <= cols < 1 << 32:
+        raise ValueError("nodes and cols must lie in [0, 2^32), rows in [0, 2^64)")
     return int(_load().sparcml_layer_norm_backward_workspace(nodes, rows, cols))
 
 
@@ -769,18 +778,16 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
     rows belong to `nodes` nodes in equal parts, one after the other.
     `dresidual`, the gradient that reaches the residual stream from elsewhere,
     is added to dx. dweight and dbias may be columns of the [P, N] gradients."""
-    if not isinstance(x, torch.Tensor) or x.dim() == 0:
-        raise TypeError("x must be a tensor of rows")
+    cols = _row_length(x)
     t = _type(x.dtype, "x")
     xs = _row_stride(x, x, "x")
     ds = _row_stride(dy, x, "dy")
     rs = 0 if dresidual is None else _row_stride(dresidual, x, "dresidual")
-    cols = x.shape[-1]
     if cols == 0:
         raise ValueError("x's rows are empty")
     rows = x.numel() // cols
-    if nodes < 1 or rows % nodes:
-        raise ValueError(f"{rows} rows do not belong to {nodes} nodes in equal parts")
+    if not 1 <= nodes <= 65535 or rows % nodes:
+        raise ValueError(f"{rows} rows do not belong to {nodes} nodes (up to 65535) in equal parts")
     _vector(weight, cols, "weight")
     _check_dev(mean, torch.float32, "mean")
     _check_dev(rstd, torch.float32, "rstd")
@@ -839,13 +846,22 @@ def _matrices(matrices):
     """Host arrays of [(position, rows, cols)], in ascending order."""
     n = len(matrices)
     at, rows, cols = zip(*matrices) if n else ((), (), ())
-    if n and (min(at) < 0 or min(min(rows), min(cols)) < 0 or max(max(rows), max(cols)) >= 1 << 32):
-        raise ValueError("positions must not be negative, rows and columns must lie in [0, 2^32)")
+    if n and (min(at) < 0 or max(at) >= 1 << 64 or min(min(rows), min(cols)) < 0 or max(max(rows), max(cols)) >= 1 << 32):
+        raise ValueError("positions must lie in [0, 2^64), rows and columns in [0, 2^32)")
     return n, (ctypes.c_uint64 * n)(*at), (ctypes.c_uint32 * n)(*rows), (ctypes.c_uint32 * n)(*cols)
+
+
+def _steps(steps: int, coefficients):
+    a, b, c = coefficients
+    if not 0 <= steps <= 64:
+        raise ValueError("steps must lie in [0, 64]")
+    return steps, a, b, c
 
 
 def orthogonalize_workspace_bytes(N: int, matrices) -> int:
     """Bytes of the workspace that orthogonalize and orthogonal_step need."""
+    if not 0 <= N < 1 << 64:
+        raise ValueError("N must lie in [0, 2^64)")
     return int(_load().sparcml_orthogonalize_workspace(N, *_matrices(matrices)))
 
 
@@ -874,7 +890,7 @@ def orthogonalize(update: torch.Tensor, matrices, dtype: Optional[torch.dtype] =
     okind = _flat(out, "out")
     if out.numel() != N or (dtype is not None and out.dtype != dtype):
         raise ValueError(f"out must hold {N} elements of the dtype asked for")
-    st = L.sparcml_orthogonalize(N, *args, steps, *coefficients, eps, kind, _ptr(update), okind, _ptr(out),
+    st = L.sparcml_orthogonalize(N, *args, *_steps(steps, coefficients), eps, kind, _ptr(update), okind, _ptr(out),
                                  _ptr(workspace), workspace.numel(), _stream(dev))
     _raise(st, "sparcml_orthogonalize")
     return out
@@ -893,7 +909,8 @@ def orthogonal_step(weight: torch.Tensor, update: torch.Tensor, matrices, lr: fl
     args = _matrices(matrices)
     L = _load()
     workspace = _workspace(workspace, L.sparcml_orthogonalize_workspace(N, *args), weight)
-    st = L.sparcml_orthogonal_step(N, *args, steps, *coefficients, eps, kind, _ptr(update), wkind, _ptr(weight), lr,
-                                   weight_decay, _ptr(workspace), workspace.numel(), _stream(weight.device))
+    st = L.sparcml_orthogonal_step(N, *args, *_steps(steps, coefficients), eps, kind, _ptr(update), wkind,
+                                   _ptr(weight), lr, weight_decay, _ptr(workspace), workspace.numel(),
+                                   _stream(weight.device))
     _raise(st, "sparcml_orthogonal_step")
     return weight
