@@ -1113,7 +1113,8 @@ __global__ __launch_bounds__(kThreads) void k_normalised(Groups gs, const S* upd
   const uint64_t size = (uint64_t)g.rows * g.cols, each = (size + g.tiles - 1) / g.tiles;
   const double* part = reinterpret_cast<const double*>(ws + g.ws + it.k * g.ws_of);
   const double sum = sum_of_parts(part, g.tiles, scratch);
-  const double by = 1.0 / (sqrt(sum) + (double)eps);
+  // an infinite norm would leave zeros beside the infinities: no direction is left, so all are NaN
+  const double by = isinf(sum) ? (double)NAN : 1.0 / (sqrt(sum) + (double)eps);
   const float move = mv.move * sqrtf(fmaxf(1.0f, (float)g.rows / (float)g.cols));
   const uint64_t begin = it.tile * each, end = min(begin + each, size), at = g.at + it.k * size;
   for (uint64_t i = at + begin + threadIdx.x; i < at + end; i += kThreads) {
