@@ -599,11 +599,13 @@ sparcml_status sparcml_momentum_step(uint64_t N, const sparcml_reduce_result* d_
  * it is about as near to the formula as with fp32 products, off by 0.5e-6 ..
  * 4e-6 of its norm and by up to 2e-5 where a few directions hold nearly all of
  * an update, since the steps amplify the others' roundings (there fp32 products
- * leave as much). The
- * iterates are held in parts of a power of two of their size, which leaves
- * room for entries of X up to 15 (they stay below 1.3 with the usual
- * coefficients 3.4445, -4.7750, 2.0315); beyond it the matrix becomes NaN. A
- * NaN or an infinity in G makes that matrix NaN and touches no other.
+ * leave as much). The parts are those of a power of two times the value, which
+ * leaves room while, after every step but the last, the rows of X (as turned)
+ * have norms below 4, the entries of Q = a I + b A + c A A and of the product of
+ * two steps' Q stay below 255 and those of Q A below 16; with the usual
+ * coefficients 3.4445, -4.7750, 2.0315 these are below 1.3, 13 and 1.3. Beyond
+ * that the matrix becomes NaN or infinite. A NaN or an infinity in G makes that
+ * matrix NaN and touches no other.
  * ---------------------------------------------------------------------- */
 size_t sparcml_orthogonalize_workspace(uint64_t N, uint32_t count, const uint64_t* h_offsets, const uint32_t* h_rows,
                                        const uint32_t* h_cols);

@@ -19,8 +19,9 @@
 // product of two values is hi hi + hi lo + lo hi: the dropped lo lo is below
 // 2^-22 of it, the same order as fp32's own rounding of a long sum. The scale
 // is a power of two (2^12 for X and A, 2^8 for M) that keeps lo out of fp16's
-// underflow for the small entries of large matrices; entries of X reach 1.3
-// with the usual coefficients and may reach 15 before hi overflows.
+// underflow for the small entries of large matrices. hi overflows at 65504: A's
+// entries may reach 16 and so X's rows a norm of 4 (1.3 with the usual
+// coefficients), those of Q = a I + M and of the product of two steps' Q 255 (13).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
