@@ -28,12 +28,12 @@
 
 #include "kernels.hpp"
 #include "numeric.hpp"
+#include "orthogonal_tiles.hpp"
 
 namespace sparcml {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr uint32_t kPad = 64;        // sides are padded with zeros to this
 constexpr uint32_t kGroups = 24;     // groups of equal matrices in one set of launches
 constexpr uint32_t kParts = 1024;    // partial sums of squares of one matrix, at most
 constexpr float kScaleX = 4096.0f;   // of X, X^T, A
@@ -43,8 +43,6 @@ typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 typedef f16 f16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
-__host__ __device__ __forceinline__ uint32_t up(uint32_t v, uint32_t to) { return (v + to - 1) / to * to; }
 
 // Equal matrices that follow each other in the flat update.
 struct Group {
@@ -218,9 +216,6 @@ struct Move {
 // such among 288 made a product of six matrices of width 1024 take 34 us, not
 // 21).
 constexpr uint32_t kBand = 4;
-__host__ __device__ __forceinline__ uint32_t tiles_of(uint32_t I, uint32_t J, bool sym) {
-  return sym ? I * (I + 1) / 2 : I * J;
-}
 // (i, j), j <= i, of the t-th pair in the order (0, 0), (1, 0), (1, 1), (2, 0) ...
 __host__ __device__ __forceinline__ void pair_at(uint32_t t, uint32_t& i, uint32_t& j) {
   i = (uint32_t)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
@@ -435,7 +430,7 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
   // for a thousand cycles. Passes past the last load what follows in the
   // workspace, and nothing reads it.
   constexpr int NM = S::TI * S::TJ * 3, ND = 2 * (S::TI + S::TJ);
-  const uint32_t passes = K / S::DEPTH;
+  const uint32_t passes = K / S::DEPTH;  // even, as K is padded to 64
   const auto pass = [&](f16x8* now, const f16x8* next) {
     read(now, 1, f[1]);
     multiply(f[0]);
@@ -453,12 +448,10 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
     load(lds1);
     wait_and_meet<LN>();
     read(lds0, 0, f[0]);
-    uint32_t k = 0;
-    for (; k + 2 <= passes; k += 2) {
+    for (uint32_t k = 0; k < passes; k += 2) {
       pass(lds0, lds1);
       pass(lds1, lds0);
     }
-    if (k < passes) pass(lds0, lds1);
   } else {
     load(lds1);
     load(lds2);
@@ -475,9 +468,10 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
         if (k % 8 == 4) stage();
       }
     }
-    if (k < passes) pass(lds0, lds1);
-    if (k + 1 < passes) pass(lds1, lds2);
-    if (k + 2 < passes) pass(lds2, lds3);
+    if (k < passes) {
+      pass(lds0, lds1);
+      pass(lds1, lds2);
+    }
     if constexpr (STAGES) {
 #pragma unroll
       for (int x = 0; x < S::TI; ++x)
@@ -1177,39 +1171,29 @@ uint32_t parts_of_host(const Group& g) {
   return (uint32_t)std::min<uint64_t>(((uint64_t)g.rows * g.cols + 8191) / 8192, kParts);
 }
 
-template <class S>
-uint32_t product_tiles(const Group& g, const Product& p) {
-  return tiles_of((g.m() + S::I - 1) / S::I, ((p.sym ? g.m() : g.n()) + S::J - 1) / S::J, p.sym);
-}
-
 template <int OUT, class T>
 hipError_t launch_product(Groups& gs, const Product& p, unsigned char* ws, T* out, Move mv, hipStream_t stream) {
   using Large = Shape<2, 4, 4, 2, 2>;  // 256 x 256, 8 waves
   using Small = Shape<2, 2, 2, 2, 4>;  // 128 x 128, 4 waves
   using Tiny = Shape<2, 2, 1, 1, 4>;   // 64 x 64, 4 waves
-  uint64_t large = 0, small = 0, tiny = 0;
-  for (uint32_t k = 0; k < gs.count; ++k) {
-    large += (uint64_t)gs.g[k].count * product_tiles<Large>(gs.g[k], p);
-    small += (uint64_t)gs.g[k].count * product_tiles<Small>(gs.g[k], p);
-    tiny += (uint64_t)gs.g[k].count * product_tiles<Tiny>(gs.g[k], p);
-  }
+  const auto tiles = [&](uint32_t side) {
+    uint64_t all = 0;
+    for (uint32_t k = 0; k < gs.count; ++k)
+      all += (uint64_t)gs.g[k].count * tiles_by(gs.g[k].m(), gs.g[k].n(), p.sym, side);
+    return all;
+  };
   const auto launch = [&](auto shape) {
     using S = decltype(shape);
-    const uint32_t blocks = tiled(gs, [&](const Group& g) { return product_tiles<S>(g, p); });
+    static_assert(S::I == S::J, "square tiles");
+    const uint32_t blocks = tiled(gs, [&](const Group& g) { return tiles_by(g.m(), g.n(), p.sym, S::I); });
     hipLaunchKernelGGL((k_product<S, OUT, T>), dim3(blocks), dim3(S::NT), 0, stream, gs, p, ws, out, mv);
     return hipGetLastError();
   };
-  // The larger the tile, the fewer bytes a product takes; the smaller, the more
-  // CUs share the work. 64 x 64 tiles where all run at once, two to a CU (one
-  // matrix of 1000 x 1537, fp32 result: 241 us, against 441 with 128 x 128; six
-  // of 1024 x 1024, 816 such tiles: 667 against 625). Else by turns of the 256
-  // CUs: a 256 x 256 tile does the work of four of 128 x 128 in 1 / 1.2 of the
-  // time (12 of 2048 x 2048, 8 turns' worth each: 6.4 ms against 7.4), but 273
-  // of them take two turns where 975 smaller ones take four (three matrices of
-  // 3085 x 6855: 11.5 ms against 9.4).
-  const auto turns = [](uint64_t tiles) { return (tiles + 255) / 256; };
-  if (tiny <= 512) return launch(Tiny{});
-  return 4 * turns(large) * 10 <= turns(small) * 12 ? launch(Large{}) : launch(Small{});
+  switch (tile_side(tiles(64), tiles(128), tiles(256))) {
+    case 64: return launch(Tiny{});
+    case 128: return launch(Small{});
+    default: return launch(Large{});
+  }
 }
 
 // One step, or two taken as one: with A = X X^T, Q = a I + M, M = b A + c A A,
