@@ -163,9 +163,12 @@ def bench_lib():
     return _bench_lib
 
 
+# the current stream's handle without a Stream object, which takes 3 us; not every torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device) -> int:
-    # the handle that torch.cuda.current_stream(device).cuda_stream holds, without the Stream object (3 us)
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream if _raw_stream is None else _raw_stream(device.index)
 
 
 def _check_dev(t: torch.Tensor, dtype, name: str):
