@@ -375,8 +375,8 @@ sparcml_status sparcml_sparse_reduce_qsgd_runs(uint32_t bits, uint32_t bucket, u
 }
 
 // --------------------------------------------------------------------------
-// Measurement entry points: the calls above with caller-owned events
-// attached to their kernel dispatches.
+// The dense operators around the reduction: arguments are checked here, before
+// anything is launched.
 // --------------------------------------------------------------------------
 static bool type_ok(uint32_t type) { return type <= SPARCML_F16; }
 static bool typed_ok(const void* p, uint32_t type) {
@@ -495,6 +495,10 @@ sparcml_status sparcml_orthogonal_step(uint64_t N, uint32_t count, const uint64_
                       weight, true, (float)(1.0 - lr * decay), (float)lr, ws, ws_bytes, stream);
 }
 
+// --------------------------------------------------------------------------
+// Measurement entry points: the calls above with caller-owned events
+// attached to their kernel dispatches.
+// --------------------------------------------------------------------------
 static sparcml::OpEvents op_events(const sparcml_bench_events* ev) {
   sparcml::OpEvents e;
   if (ev) {
