@@ -605,7 +605,9 @@ sparcml_status sparcml_momentum_step(uint64_t N, const sparcml_reduce_result* d_
  * two steps' Q stay below 255 and those of Q A below 16; with the usual
  * coefficients 3.4445, -4.7750, 2.0315 these are below 1.3, 13 and 1.3. Beyond
  * that the matrix becomes NaN or infinite. A NaN or an infinity in G makes that
- * matrix NaN and touches no other.
+ * matrix NaN and touches no other. A call repeated gives the same bits; the last
+ * bits of a matrix can depend on the sizes of the others in the call, by which
+ * the order of the sums is chosen.
  * ---------------------------------------------------------------------- */
 size_t sparcml_orthogonalize_workspace(uint64_t N, uint32_t count, const uint64_t* h_offsets, const uint32_t* h_rows,
                                        const uint32_t* h_cols);

@@ -818,8 +818,9 @@ def momentum_step(reduced: "ReduceOutput", momentum: torch.Tensor, mu: float, sc
                   nesterov: bool = False, dtype: torch.dtype = torch.float32,
                   update: Optional[torch.Tensor] = None) -> torch.Tensor:
     """momentum = mu * momentum + scale * g in place, g the reduction's result
-    (sparse or dense, as the device knows). Returns the update in `dtype`: the
-    momentum, or scale * g + mu * momentum with `nesterov`."""
+    (sparse or dense, as the device knows). Returns the update in `dtype` (a
+    given `update`: in its own): the momentum, or scale * g + mu * momentum
+    with `nesterov`."""
     _check_dev(momentum, torch.float32, "momentum")
     _check_dev(reduced.result, torch.uint8, "result")
     _check_dev(reduced.out_idx, torch.int32, "out_idx")
@@ -842,7 +843,8 @@ def momentum_step(reduced: "ReduceOutput", momentum: torch.Tensor, mu: float, sc
 
 
 # ---------------------------------------------------------------------------
-NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)  # quintic whose iterates take (0, 1] to about 0.7 .. 1.2
+# quintic whose iterates take (0, 1] to about 0.7 .. 1.2, as published with the Muon optimizer (Jordan et al., 2024)
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
 
 
 def _matrices(matrices):

@@ -378,7 +378,9 @@ bool held_by(uint32_t cols, F&& f) {
 // to fill the chip, and no more, since each writes and the last kernel reads
 // 8 bytes a column. A chunk takes at least two turns of the rows that its
 // workgroup holds at a time (one chunk needs no last kernel: 4 nodes of 16
-// rows of 1024 fp32 are one launch).
+// rows of 1024 fp32 are one launch). Past 1024 columns that is two rows, whose
+// sums are more bytes than the rows: 2048 rows of 4096 bf16 take 40 us where
+// their bytes alone take 10, 8192 rows of 16384 319 us where they take 163.
 uint32_t chunks_of(uint32_t nodes, uint64_t rows, uint32_t cols) {
   const uint64_t at_once = cols <= 1024 ? kBackRows * kWave / std::max(8u, std::min(64u, cols / 8)) : 1;
   const uint64_t most = (1024 + nodes - 1) / nodes, wanted = (rows + 2 * at_once - 1) / (2 * at_once);

@@ -380,10 +380,11 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
     }
   }
 
-  // The sums add up 8 passes (256 of the summed index, 48 additions) at a time: in one chain of thousands of roundings an fp32 result of 196 x 8000
+  // The sums add up 8 passes (256 of the summed index, 48 additions) at a time:
+  // in one chain of thousands of roundings an fp32 result of 196 x 8000
   // is off by 7e-6 of its norm, not 2e-6. Tiles of 256 x 256 have no registers
-  // left for it; they are for sums of a large square matrix, whose own
-  // roundings weigh less.
+  // left for it: 25 matrices of 1024 x 8192, which take them, are off by 3.2e-6
+  // each and 4 of them, which do not, by 2.2e-6 (fp32 products: 3.9e-6).
   constexpr bool STAGES = S::BUFFERS > 2;
   f32x16 acc[S::TI][S::TJ] = {}, total[STAGES ? S::TI : 1][STAGES ? S::TJ : 1] = {};
   const auto stage = [&] {
@@ -647,10 +648,10 @@ __global__ __launch_bounds__(S::NT, S::NT == 512 ? 2 : 1) void k_product(Groups 
 // next to a a X they would cancel to a tenth of their size. The products of the
 // lo parts are added up before those of the hi parts, whose sums round more.
 //
-// Bound by the chain: at 64 x 2048 (117 us) the matrix cores work a third of the
+// Bound by the chain: at 64 x 2048 (116 us) the matrix cores work a third of the
 // time and the vector units two fifths, one after the other, since the waves
 // keep step. 16 x 27 takes 14 us, 64 x 576 48 us, and 20 matrices of 16 x 16 ..
-// 64 x 576 take 54 us, as long as the largest one.
+// 64 x 576 take 55 us, little more than the largest one.
 constexpr int kSmallThreads = 512, kSmallWaves = kSmallThreads / kWave;
 constexpr uint32_t kSmallSide = 64, kSmallLong = 2048, kSmallLong32 = 16384;
 constexpr int kRow = 72;  // fp16 of a row in LDS: sixteen rows' 16-byte chunks fall into different banks
@@ -1119,8 +1120,8 @@ __global__ __launch_bounds__(kThreads) void k_normalised(Groups gs, const S* upd
 }
 
 // The kinds of matrices: those that one workgroup takes through its steps, up
-// to where the chip's other CUs are faster (64 x 2048: 122 us, against 130 by
-// products over all CUs; 16 x 16384: 347 against 489), and by the shorter side
+// to where the chip's other CUs are nearly as fast (64 x 2048: 116 us, against
+// 128 by products over all CUs; 32 x 16384: 361 against 492), and by the shorter side
 // the narrow and the wide ones, whose steps are paired or not on their own.
 enum Kind { kSmall, kNarrow, kWide, kKinds };
 Kind kind_of(uint32_t rows, uint32_t cols) {
@@ -1200,8 +1201,8 @@ hipError_t launch_product(Groups& gs, const Product& p, unsigned char* ws, T* ou
 // the next step's A is Q A Q = Q (Q A) (they commute, so both products are
 // symmetric) and X moves once, by the product of the two Q. That trades two of
 // X's products (3 m m n) for three halves more of m x m ones and keeps the
-// accuracy (fp32 results: 4e-7 .. 1.2e-6 of the norm); at three (2e-6 .. 6e-6)
-// A's small singular values begin to be lost beside its large ones.
+// accuracy; at three (2e-6 .. 6e-6 of the norm where one and two leave 4e-7 ..
+// 1.2e-6) A's small singular values begin to be lost beside its large ones.
 //
 // Every product takes both parts of its operands, whatever the result's type.
 // The error that single fp16 products (a third of the multiplications) leave in
