@@ -545,6 +545,133 @@ sparcml_status sparcml_layer_norm_backward(uint32_t type, uint32_t nodes, uint64
                                            size_t ws_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * The heads of a batch's tokens: element e of head h of token t of sequence b
+ * is data[b * batch + t * token + h * head + e]. Strides in elements, below
+ * 2^40, any values for what is read (0 repeats), for what is written such that
+ * no two elements share a place. Arrays need the alignment of their elements
+ * only; heads on 16-byte borders are the fast case.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  void* data;
+  uint64_t batch, token, head;
+} sparcml_heads;
+
+/* ------------------------------------------------------------------------
+ * Norms of the queries and keys of every head and their rotation by position,
+ * and the gradients of both, for `nodes` nodes of `tokens` tokens each (token
+ * p * tokens + t is token t of node p; the strides named `batch` are not used):
+ *   r = 1 / sqrt(sum(x^2) / dim + eps),  y = R(x * r * weight)
+ * R turns the pairs (a, b) of a head's first `rotated` elements, pair i being
+ * elements i and i + rotated / 2 or, interleaved, 2 i and 2 i + 1, by the angle
+ * w = positions[token] * frequencies[i]:
+ *   (a, b) -> (a cos w - b sin w, b cos w + a sin w)
+ * The gradients, with u = R^T dy, h = x * r and g = u * weight:
+ *   dx        = r * (g - h * sum(g * h) / dim)
+ *   dweight_p = sum of u * h over the tokens and heads of node p
+ * The sums over tokens are added in an order that depends on the sizes alone,
+ * so a call repeated gives the same bits.
+ *
+ *   nodes       1 <= nodes <= 65535 (forward: 1), nodes * tokens < 2^31
+ *   heads, groups  of q and of k: 1 .. 65535
+ *   dim         1 <= dim <= 256
+ *   rotated     even, <= dim; 0: nothing turns, positions and frequencies are
+ *               not read and may be NULL
+ *   eps         finite, >= 0
+ *   q, k        device, typed, read only
+ *   q_weight, k_weight  device, [dim] fp32; NULL: ones
+ *   positions   device, [nodes * tokens] int32
+ *   frequencies device, [rotated / 2] fp64, radians a position
+ *   q_out, k_out  device, typed: y; backward: dx
+ *   dq, dk      device, typed, read only: dy (backward)
+ *   dq_weight, dk_weight  device, fp32, node p's at dq_weight + p * dq_stride
+ *               (dq_stride >= dim): for instance columns of the [P][N]
+ *               gradients that sparcml_topk_ef takes, with dq_stride = N;
+ *               NULL: not wanted (backward)
+ *   ws          device workspace of sparcml_head_norm_rotate_backward_workspace
+ *               (nodes, tokens, dim) bytes, 256-byte aligned; content does not
+ *               matter
+ * q_out and k_out may be q and k (the backward's also dq and dk) with the same
+ * strides; apart from that nothing written may overlap anything else. A NaN or
+ * an infinity in a head touches no other head's results.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  uint32_t type, nodes, heads, groups, dim, rotated, interleaved;
+  float eps;
+  uint64_t tokens;
+  sparcml_heads q, k, q_out, k_out;
+  const float *q_weight, *k_weight;
+  const int32_t* positions;
+  const double* frequencies;
+  sparcml_heads dq, dk;
+  float *dq_weight, *dk_weight;
+  uint64_t dq_stride, dk_stride;
+} sparcml_head_norm_args;
+
+sparcml_status sparcml_head_norm_rotate(const sparcml_head_norm_args* args, hipStream_t stream);
+
+size_t sparcml_head_norm_rotate_backward_workspace(uint32_t nodes, uint64_t tokens, uint32_t dim);
+
+sparcml_status sparcml_head_norm_rotate_backward(const sparcml_head_norm_args* args, void* ws, size_t ws_bytes,
+                                                 hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Attention of `queries` queries over `keys` keys in each of `batch`
+ * sequences, and its gradients, which compute the probabilities again. Query
+ * heads h * heads / groups .. (h + 1) * heads / groups - 1 read key and value
+ * head h. With n and m the sequence's own queries and keys, query i < n sees the
+ * keys j < m with  i + m - n - before <= j <= i + m - n + after:
+ *   s   = scale * q k^T over the keys seen
+ *   lse = log(sum(exp(s))),  out = exp(s - lse) v
+ *   p   = exp(s - lse),  ds = p * (dout v^T - sum(dout * out))
+ *   dv  = p^T dout,  dq = scale * ds k,  dk = scale * ds^T q
+ * dk and dv are summed over the query heads that read them. A query that sees
+ * nothing, and every query i >= n, gets out = 0 and lse = -inf, dq = 0 and adds
+ * nothing to dk and dv; dk and dv of keys j >= m are 0. What lies behind n or m
+ * is not read, so it may hold anything. A call repeated gives the same bits.
+ *
+ *   batch       0 .. 65535 (0: nothing is done)
+ *   queries, keys  0 .. 2^29 - 1
+ *   heads       1 .. 65535, a multiple of groups
+ *   dim         1 .. 128
+ *   before, after  UINT32_MAX (or any that reach past the keys): all of them;
+ *               after = 0: causal
+ *   scale       finite, > 0
+ *   q_lengths, k_lengths  device, [batch] int32, n and m of each sequence,
+ *               taken as 0 and as queries or keys where they lie outside;
+ *               NULL: all of them
+ *   q, k, v     device, typed, read only
+ *   out         device, typed; read only in the backward call
+ *   lse         device, [batch][heads][queries] fp32; likewise
+ *   dout        device, typed, read only (backward)
+ *   dq, dk, dv  device, typed, like q, k, v (backward)
+ *   ws          device workspace of sparcml_attention_workspace(args) or
+ *               sparcml_attention_backward_workspace(args) bytes, which read
+ *               the sizes only, 256-byte aligned; content does not matter
+ * Nothing written may overlap anything else. With 16-bit types the products'
+ * probabilities and ds are rounded to the type, their sums are fp32; with fp32
+ * nothing is rounded further. Keys and values that some query of a sequence sees
+ * have to be finite: a NaN or an infinity in one of them may reach all its
+ * sequence's rows, also those that do not see it. It touches no other sequence.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  uint32_t type, batch, queries, keys, heads, groups, dim, before, after;
+  float scale;
+  const int32_t *q_lengths, *k_lengths;
+  sparcml_heads q, k, v, out;
+  float* lse;
+  sparcml_heads dout, dq, dk, dv;
+} sparcml_attention_args;
+
+size_t sparcml_attention_workspace(const sparcml_attention_args* args);
+
+sparcml_status sparcml_attention(const sparcml_attention_args* args, void* ws, size_t ws_bytes, hipStream_t stream);
+
+size_t sparcml_attention_backward_workspace(const sparcml_attention_args* args);
+
+sparcml_status sparcml_attention_backward(const sparcml_attention_args* args, void* ws, size_t ws_bytes,
+                                          hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * Momentum from a reduction's result. With g the sum that the reduction
  * left, sparse or dense as d_result says on the device (no host wait):
  *   m      = mu * m + scale * g              (in place)

@@ -1,7 +1,7 @@
 """MI355X (gfx950) SparCML hot path: error-feedback Top-k, 2/4/8-bit stochastic
 quantization and sparse reduction with the dense switch; and around it, layer
-norm with per-node gradients, momentum from a reduction's result and
-orthogonalised updates.
+norm and the norms of queries and keys with per-node gradients, attention and
+its gradients, momentum from a reduction's result and orthogonalised updates.
 
 Thin ctypes binding over the C ABI in include/sparcml.h: it checks tensor
 dtype/device/contiguity, allocates outputs and workspaces with torch, and
@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -98,6 +99,20 @@ def _load():
     L.sparcml_layer_norm_backward.argtypes = [u32, u32, u64, u32, vp, u64, vp, u64, vp, u64, vp, vp, vp, vp, vp, u64,
                                               vp, u64, vp, sz, vp]
     L.sparcml_layer_norm_backward.restype = st
+    L.sparcml_head_norm_rotate.argtypes = [vp, vp]
+    L.sparcml_head_norm_rotate.restype = st
+    L.sparcml_head_norm_rotate_backward_workspace.argtypes = [u32, u64, u32]
+    L.sparcml_head_norm_rotate_backward_workspace.restype = sz
+    L.sparcml_head_norm_rotate_backward.argtypes = [vp, vp, sz, vp]
+    L.sparcml_head_norm_rotate_backward.restype = st
+    L.sparcml_attention_workspace.argtypes = [vp]
+    L.sparcml_attention_workspace.restype = sz
+    L.sparcml_attention.argtypes = [vp, vp, sz, vp]
+    L.sparcml_attention.restype = st
+    L.sparcml_attention_backward_workspace.argtypes = [vp]
+    L.sparcml_attention_backward_workspace.restype = sz
+    L.sparcml_attention_backward.argtypes = [vp, vp, sz, vp]
+    L.sparcml_attention_backward.restype = st
     L.sparcml_momentum_step.argtypes = [u64, vp, vp, u64, vp, vp, f32, f32, u32, u32, vp, vp]
     L.sparcml_momentum_step.restype = st
     L.sparcml_orthogonalize_workspace.argtypes = [u64, u32, vp, vp, vp]
@@ -811,6 +826,261 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
                                        _ptr(dbias), bs, _ptr(workspace), workspace.numel(), _stream(dev))
     _raise(st, "sparcml_layer_norm_backward")
     return dx, dweight, dbias
+
+
+# ---------------------------------------------------------------------------
+# sparcml_head_norm_args and sparcml_attention_args; a sparcml_heads is four words
+_HEAD_NORM_ARGS = struct.Struct("@7If33Q")
+_ATTENTION_ARGS = struct.Struct("@9If35Q")
+_NO_HEADS = (0, 0, 0, 0)
+
+
+def _head_tensor(t: torch.Tensor, dtype, shape, device, name: str):
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or not t.is_cuda:
+        raise TypeError(f"{name} must be a {dtype} tensor on {device if device.type == 'cuda' else 'a GPU'}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+
+
+def _apart(t: torch.Tensor, name: str):
+    """Raises unless every element of `t` has a place of its own."""
+    end = 1
+    for step, n in sorted(zip(t.stride(), t.shape)):
+        if n > 1:
+            if step < end:
+                raise ValueError(f"{name}'s elements must not share a place")
+            end = step * n
+    return t
+
+
+def _output_heads(t: Optional[torch.Tensor], like: torch.Tensor, name: str) -> torch.Tensor:
+    """The caller's output, of any strides, or a new contiguous one, of `like`'s shape and type."""
+    if t is None:
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
+    _head_tensor(t, like.dtype, like.shape, like.device, name)
+    return t if t.numel() == 0 else _apart(t, name)
+
+
+def _on(device, call, *args) -> int:
+    """call(*args, the current stream of `device`) with that device the current one."""
+    if torch.cuda.current_device() == device.index:
+        return call(*args, _stream(device))
+    with torch.cuda.device(device):
+        return call(*args, _stream(device))
+
+
+def _token_heads(t: torch.Tensor, name: str):
+    """sparcml_heads of [..., heads, D] whose tokens are evenly spaced."""
+    if t.dim() == 3:
+        return t.data_ptr(), 0, t.stride(0), t.stride(1)
+    step, size = 0, 1  # of the tokens' dimensions from the inside out
+    for d in range(t.dim() - 3, -1, -1):
+        n = t.shape[d]
+        if n == 1:
+            continue
+        if size == 1:
+            step = t.stride(d)
+        elif t.stride(d) != step * size:
+            raise ValueError(f"{name}'s tokens must be evenly spaced")
+        size *= n
+    return t.data_ptr(), 0, step, t.stride(-2)
+
+
+def _head_norm_checks(q, k, q_weight, k_weight, positions, frequencies):
+    """(type, tokens, heads, groups, D, rotated) of head_norm_rotate's arguments."""
+    if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or q.dim() < 2 or k.dim() < 2:
+        raise TypeError("q and k must be tensors of [..., heads, D]")
+    heads, cols, groups = q.shape[-2], q.shape[-1], k.shape[-2]
+    _head_tensor(q, q.dtype, q.shape, q.device, "q")
+    _head_tensor(k, q.dtype, q.shape[:-2] + (groups, cols), q.device, "k")
+    tokens = q.shape[:-2].numel()
+    if tokens >= 1 << 31 or max(heads, groups) >= 1 << 16 or min(heads, groups, cols) < 1 or cols > 256:
+        raise ValueError("q and k must have 1 to 65535 heads of 1 to 256 elements and fewer than 2^31 tokens")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _check_dev(w, torch.float32, name)
+            if w.device != q.device or w.numel() != cols:
+                raise ValueError(f"{name} must have {cols} elements on {q.device}")
+    rotated = 0
+    if frequencies is not None:
+        rotated = 2 * frequencies.numel()
+        _check_dev(frequencies, torch.float64, "frequencies")
+        _check_dev(positions, torch.int32, "positions")
+        if rotated > cols or positions.numel() != tokens:
+            raise ValueError(f"frequencies must have at most {cols // 2} elements, positions {tokens}")
+        if frequencies.device != q.device or positions.device != q.device:
+            raise ValueError(f"positions and frequencies must be on {q.device}")
+    return _type(q.dtype, "q"), tokens, heads, groups, cols, rotated
+
+
+def rotation_frequencies(rotated: int, base: float = 10000.0, device=None) -> torch.Tensor:
+    """base^(-2 i / rotated), i < rotated / 2: the usual frequencies of head_norm_rotate, fp64."""
+    if rotated % 2:
+        raise ValueError("rotated must be even")
+    return base ** (-2.0 * torch.arange(rotated // 2, dtype=torch.float64, device=device) / max(rotated, 1))
+
+
+def head_norm_rotate(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+                     k_weight: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                     frequencies: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+                     q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None):
+    """Norms every head of `q` [..., heads, D] and `k` [..., groups, D] (fp32, bf16
+    or fp16; views of one projection, say): x / sqrt(mean(x^2) + eps) * weight,
+    with fp32 weights of D elements, then turns pair i of its first
+    2 * len(frequencies) elements by position * frequencies[i] (int32 positions of
+    q.shape[:-2], fp64 frequencies; none: nothing turns). Pair i is elements i and
+    i + len(frequencies), or 2 i and 2 i + 1 where `interleaved`. Returns (q_out,
+    k_out), which may be q and k themselves."""
+    t, tokens, heads, groups, cols, rotated = _head_norm_checks(q, k, q_weight, k_weight, positions, frequencies)
+    q_out, k_out = _output_heads(q_out, q, "q_out"), _output_heads(k_out, k, "k_out")
+    args = _HEAD_NORM_ARGS.pack(t, 1, heads, groups, cols, rotated, interleaved, eps, tokens, *_token_heads(q, "q"),
+                                *_token_heads(k, "k"), *_token_heads(q_out, "q_out"), *_token_heads(k_out, "k_out"),
+                                _ptr(q_weight) or 0, _ptr(k_weight) or 0, _ptr(positions) or 0, _ptr(frequencies) or 0,
+                                *_NO_HEADS, *_NO_HEADS, 0, 0, 0, 0)
+    _raise(_on(q.device, _load().sparcml_head_norm_rotate, args), "sparcml_head_norm_rotate")
+    return q_out, k_out
+
+
+def head_norm_rotate_backward_workspace_bytes(nodes: int, tokens: int, cols: int) -> int:
+    """Bytes of the workspace for `tokens` tokens a node."""
+    if not 0 <= nodes < 1 << 32 or not 0 <= tokens < 1 << 64 or not 0 <= cols < 1 << 32:
+        raise ValueError("nodes and cols must lie in [0, 2^32), tokens in [0, 2^64)")
+    return int(_load().sparcml_head_norm_rotate_backward_workspace(nodes, tokens, cols))
+
+
+def head_norm_rotate_backward(dq: torch.Tensor, dk: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                              q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                              positions: Optional[torch.Tensor] = None, frequencies: Optional[torch.Tensor] = None,
+                              eps: float = 1e-6, interleaved: bool = False, nodes: int = 1,
+                              q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                              dq_weight: Optional[torch.Tensor] = None, dk_weight: Optional[torch.Tensor] = None,
+                              workspace: Optional[torch.Tensor] = None):
+    """Gradients of head_norm_rotate, with `dq` and `dk` those of its results and
+    `q` and `k` its inputs: (like q, like k, dq_weight [nodes, D], dk_weight
+    [nodes, D], both fp32). The tokens belong to `nodes` nodes in equal parts, one
+    after the other. q_out and k_out may be dq and dk (or q and k); dq_weight and
+    dk_weight may be columns of the [P, N] gradients."""
+    t, tokens, heads, groups, cols, rotated = _head_norm_checks(q, k, q_weight, k_weight, positions, frequencies)
+    _head_tensor(dq, q.dtype, q.shape, q.device, "dq")
+    _head_tensor(dk, k.dtype, k.shape, q.device, "dk")
+    if not 1 <= nodes <= 65535 or tokens % nodes:
+        raise ValueError(f"{tokens} tokens do not belong to {nodes} nodes (up to 65535) in equal parts")
+    q_out, k_out = _output_heads(q_out, q, "q_out"), _output_heads(k_out, k, "k_out")
+    if dq_weight is None and dk_weight is None:  # one allocation
+        dq_weight, dk_weight = q.new_empty((2, nodes, cols), dtype=torch.float32).unbind()
+        qs = ks = cols
+    else:
+        dq_weight, qs = _node_rows(dq_weight, nodes, cols, q, "dq_weight")
+        dk_weight, ks = _node_rows(dk_weight, nodes, cols, q, "dk_weight")
+    L = _load()
+    workspace = _workspace(workspace, L.sparcml_head_norm_rotate_backward_workspace(nodes, tokens // nodes, cols), q)
+    args = _HEAD_NORM_ARGS.pack(t, nodes, heads, groups, cols, rotated, interleaved, eps, tokens // nodes,
+                                *_token_heads(q, "q"), *_token_heads(k, "k"), *_token_heads(q_out, "q_out"),
+                                *_token_heads(k_out, "k_out"), _ptr(q_weight) or 0, _ptr(k_weight) or 0,
+                                _ptr(positions) or 0, _ptr(frequencies) or 0, *_token_heads(dq, "dq"),
+                                *_token_heads(dk, "dk"), dq_weight.data_ptr(), dk_weight.data_ptr(), qs, ks)
+    st = _on(q.device, L.sparcml_head_norm_rotate_backward, args, workspace.data_ptr(), workspace.numel())
+    _raise(st, "sparcml_head_norm_rotate_backward")
+    return q_out, k_out, dq_weight, dk_weight
+
+
+# ---------------------------------------------------------------------------
+def _attention_checks(q, k, v, causal, window, scale, q_lengths, k_lengths):
+    """The first words of sparcml_attention_args: sizes, mask, scale and lengths."""
+    if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or q.dim() != 4 or k.dim() != 4:
+        raise TypeError("q, k and v must be tensors of [batch, tokens, heads, D]")
+    batch, queries, heads, cols = q.shape
+    keys, groups = k.shape[1], k.shape[2]
+    dev = q.device
+    _head_tensor(q, q.dtype, q.shape, dev, "q")
+    _head_tensor(k, q.dtype, (batch, keys, groups, cols), dev, "k")
+    _head_tensor(v, q.dtype, (batch, keys, groups, cols), dev, "v")
+    if batch > 65535 or max(queries, keys) >= 1 << 29 or max(heads, groups) > 65535 or not 1 <= cols <= 128:
+        raise ValueError("up to 65535 sequences and heads of 1 to 128 elements, fewer than 2^29 queries and keys")
+    if groups < 1 or heads < 1 or heads % groups:
+        raise ValueError(f"{heads} heads do not share {groups} groups of keys and values in equal parts")
+    if window is not None and window < 1:
+        raise ValueError("window must be at least 1")
+    if scale is None:
+        scale = cols ** -0.5
+    if not 0.0 < scale < math.inf:
+        raise ValueError("scale must be finite and positive")
+    for t, name in ((q_lengths, "q_lengths"), (k_lengths, "k_lengths")):
+        if t is not None:
+            _check_dev(t, torch.int32, name)
+            if t.device != dev or t.numel() != batch:
+                raise ValueError(f"{name} must have {batch} elements on {dev}")
+    before = 0xFFFFFFFF if window is None else min(window - 1, 0xFFFFFFFF)
+    return (_type(q.dtype, "q"), batch, queries, keys, heads, groups, cols, before, 0 if causal else before, scale,
+            _ptr(q_lengths) or 0, _ptr(k_lengths) or 0)
+
+
+def _batch_heads(t: torch.Tensor):
+    b, n, h, _ = t.stride()
+    return t.data_ptr(), b, n, h
+
+
+def attention_workspace_bytes(q: torch.Tensor, k: torch.Tensor, backward: bool = False) -> int:
+    """Bytes of the workspace that attention or, `backward`, attention_backward
+    needs for queries and keys like these."""
+    args = _ATTENTION_ARGS.pack(*_attention_checks(q, k, k, False, None, None, None, None), *([0] * 33))
+    return int((_load().sparcml_attention_backward_workspace if backward else _load().sparcml_attention_workspace)(args))
+
+
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = False, window: Optional[int] = None,
+              scale: Optional[float] = None, q_lengths: Optional[torch.Tensor] = None,
+              k_lengths: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+              lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """softmax(scale * q k^T) v for `q` [batch, queries, heads, D] and `k`, `v`
+    [batch, keys, groups, D] (fp32, bf16 or fp16, D up to 128, any strides); heads /
+    groups query heads share a key and value head. Returns (out like q, lse
+    [batch, heads, queries] fp32), lse the logarithm of each row's sum.
+
+    Query i of n sees the keys j of m with j <= i + m - n where `causal`, and less
+    than `window` away from i + m - n where that is given. `q_lengths`, `k_lengths`
+    [batch] int32 are each sequence's own n and m: what lies behind is not read,
+    rows of out there are 0 and lse -inf, as where a query sees nothing. scale:
+    1 / sqrt(D) if none is given."""
+    head = _attention_checks(q, k, v, causal, window, scale, q_lengths, k_lengths)
+    out = _output_heads(out, q, "out")
+    lse = _given(lse, q, "lse", (head[1], head[4], head[2]), torch.float32)
+    args = _ATTENTION_ARGS.pack(*head, *_batch_heads(q), *_batch_heads(k), *_batch_heads(v), *_batch_heads(out),
+                                lse.data_ptr(), *_NO_HEADS, *_NO_HEADS, *_NO_HEADS, *_NO_HEADS)
+    L = _load()
+    workspace = _workspace(workspace, L.sparcml_attention_workspace(args), q)
+    _raise(_on(q.device, L.sparcml_attention, args, workspace.data_ptr(), workspace.numel()), "sparcml_attention")
+    return out, lse
+
+
+def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                       lse: torch.Tensor, causal: bool = False, window: Optional[int] = None,
+                       scale: Optional[float] = None, q_lengths: Optional[torch.Tensor] = None,
+                       k_lengths: Optional[torch.Tensor] = None, dq: Optional[torch.Tensor] = None,
+                       dk: Optional[torch.Tensor] = None, dv: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None):
+    """Gradients of attention, of whose results `out` and `lse` are needed: (dq, dk,
+    dv) like q, k and v; dk and dv are summed over the query heads that share a
+    head. They may be given, of any strides (the parts of a projection's gradient,
+    say). Behind a sequence's lengths, and for queries that see nothing, they are
+    0. Nothing of queries times keys is stored: the probabilities are computed
+    again, tile by tile."""
+    head = _attention_checks(q, k, v, causal, window, scale, q_lengths, k_lengths)
+    _head_tensor(dout, q.dtype, q.shape, q.device, "dout")
+    _head_tensor(out, q.dtype, q.shape, q.device, "out")
+    _check_dev(lse, torch.float32, "lse")
+    if lse.shape != (head[1], head[4], head[2]) or lse.device != q.device:
+        raise ValueError(f"lse must have shape {(head[1], head[4], head[2])} on {q.device}")
+    dq, dk, dv = _output_heads(dq, q, "dq"), _output_heads(dk, k, "dk"), _output_heads(dv, v, "dv")
+    args = _ATTENTION_ARGS.pack(*head, *_batch_heads(q), *_batch_heads(k), *_batch_heads(v), *_batch_heads(out),
+                                lse.data_ptr(), *_batch_heads(dout), *_batch_heads(dq), *_batch_heads(dk),
+                                *_batch_heads(dv))
+    L = _load()
+    workspace = _workspace(workspace, L.sparcml_attention_backward_workspace(args), q)
+    st = _on(q.device, L.sparcml_attention_backward, args, workspace.data_ptr(), workspace.numel())
+    _raise(st, "sparcml_attention_backward")
+    return dq, dk, dv
 
 
 # ---------------------------------------------------------------------------

@@ -17,7 +17,7 @@ BENCH_LIB = os.path.join(PKG, "libsparcml_bench.so")
 OBJDIR = os.path.join(PKG, "_build")
 
 SOURCES = ["api.hip", "topk_ef.hip", "topk_row.hip", "topk_bucketed.hip", "qsgd.hip", "sparse_reduce.hip",
-           "layer_norm.hip", "momentum.hip", "orthogonal.hip"]
+           "layer_norm.hip", "momentum.hip", "orthogonal.hip", "head_norm.hip", "attention.hip"]
 BENCH_SOURCES = ["reference_stream.hip"]
 
 ARCH = "gfx950"

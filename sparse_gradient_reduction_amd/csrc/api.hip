@@ -428,6 +428,98 @@ sparcml_status sparcml_layer_norm_backward(uint32_t type, uint32_t nodes, uint64
 }
 
 // --------------------------------------------------------------------------
+static bool heads_ok(const sparcml_heads& x, uint32_t type) {
+  return typed_ok(x.data, type) && x.batch < (1ull << 40) && x.token < (1ull << 40) && x.head < (1ull << 40);
+}
+
+static bool head_norm_sizes_ok(uint32_t nodes, uint64_t tokens, uint32_t dim) {
+  return nodes > 0 && nodes <= 65535u && dim > 0 && dim <= sparcml::kHeadNormDim && tokens < (1ull << 31) / nodes;
+}
+
+static bool head_norm_args_ok(const sparcml_head_norm_args& a) {
+  if (!type_ok(a.type) || !head_norm_sizes_ok(a.nodes, a.tokens, a.dim)) return false;
+  if (a.heads == 0 || a.heads > 65535u || a.groups == 0 || a.groups > 65535u) return false;
+  if (a.rotated > a.dim || a.rotated % 2 != 0 || !std::isfinite(a.eps) || a.eps < 0.0f) return false;
+  if ((a.q_weight && !f32_ok(a.q_weight)) || (a.k_weight && !f32_ok(a.k_weight))) return false;
+  if (a.tokens == 0) return true;
+  if (a.rotated > 0 && (!a.positions || (reinterpret_cast<uintptr_t>(a.positions) & 3u) || !a.frequencies ||
+                        (reinterpret_cast<uintptr_t>(a.frequencies) & 7u)))
+    return false;
+  return heads_ok(a.q, a.type) && heads_ok(a.k, a.type) && heads_ok(a.q_out, a.type) && heads_ok(a.k_out, a.type);
+}
+
+sparcml_status sparcml_head_norm_rotate(const sparcml_head_norm_args* args, hipStream_t stream) {
+  if (!args || !head_norm_args_ok(*args) || args->nodes != 1) return SPARCML_ERR_INVALID_ARG;
+  if (args->tokens == 0) return SPARCML_OK;
+  return from_hip(sparcml::head_norm_rotate_launch(*args, stream));
+}
+
+size_t sparcml_head_norm_rotate_backward_workspace(uint32_t nodes, uint64_t tokens, uint32_t dim) {
+  if (!head_norm_sizes_ok(nodes, tokens, dim)) return 0;
+  return sparcml::head_norm_rotate_backward_workspace_bytes(nodes, tokens, dim);
+}
+
+sparcml_status sparcml_head_norm_rotate_backward(const sparcml_head_norm_args* args, void* ws, size_t ws_bytes,
+                                                 hipStream_t stream) {
+  if (!args || !head_norm_args_ok(*args)) return SPARCML_ERR_INVALID_ARG;
+  const sparcml_head_norm_args& a = *args;
+  if (a.tokens > 0 && (!heads_ok(a.dq, a.type) || !heads_ok(a.dk, a.type))) return SPARCML_ERR_INVALID_ARG;
+  if ((a.dq_weight && (!f32_ok(a.dq_weight) || a.dq_stride < a.dim)) ||
+      (a.dk_weight && (!f32_ok(a.dk_weight) || a.dk_stride < a.dim)))
+    return SPARCML_ERR_INVALID_ARG;
+  if (!ws || !aligned256(ws) || ws_bytes < sparcml::head_norm_rotate_backward_workspace_bytes(a.nodes, a.tokens, a.dim))
+    return SPARCML_ERR_WORKSPACE;
+  return from_hip(sparcml::head_norm_rotate_backward_launch(a, ws, stream));
+}
+
+// --------------------------------------------------------------------------
+// what the workspaces are sized by; a launch has fewer than 2^31 workgroups,
+// which take 32 queries or keys at least
+static bool attention_sizes_ok(const sparcml_attention_args& a) {
+  if (!type_ok(a.type) || a.batch > 65535u || a.queries >= (1u << 29) || a.keys >= (1u << 29)) return false;
+  if (a.heads == 0 || a.heads > 65535u || a.groups == 0 || a.heads % a.groups != 0) return false;
+  const uint64_t bh = (uint64_t)a.batch * a.heads, most = std::max(a.queries, a.keys) / 32 + 1;
+  return a.dim > 0 && a.dim <= sparcml::kAttentionDim && (bh == 0 || most < (1ull << 31) / bh);
+}
+
+static bool attention_args_ok(const sparcml_attention_args& a, bool backward) {
+  if (!attention_sizes_ok(a) || !std::isfinite(a.scale) || !(a.scale > 0.0f)) return false;
+  if ((a.q_lengths && (reinterpret_cast<uintptr_t>(a.q_lengths) & 3u)) ||
+      (a.k_lengths && (reinterpret_cast<uintptr_t>(a.k_lengths) & 3u)))
+    return false;
+  if (a.batch == 0) return true;
+  if (a.queries > 0 && (!heads_ok(a.q, a.type) || !heads_ok(a.out, a.type) || !f32_ok(a.lse))) return false;
+  if (a.keys > 0 && (!heads_ok(a.k, a.type) || !heads_ok(a.v, a.type))) return false;
+  if (!backward) return true;
+  if (a.queries > 0 && (!heads_ok(a.dout, a.type) || !heads_ok(a.dq, a.type))) return false;
+  return a.keys == 0 || (heads_ok(a.dk, a.type) && heads_ok(a.dv, a.type));
+}
+
+size_t sparcml_attention_workspace(const sparcml_attention_args* args) {
+  return args && attention_sizes_ok(*args) ? sparcml::attention_workspace_bytes(*args) : 0;
+}
+
+sparcml_status sparcml_attention(const sparcml_attention_args* args, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (!args || !attention_args_ok(*args, false)) return SPARCML_ERR_INVALID_ARG;
+  if (!ws || !aligned256(ws) || ws_bytes < sparcml::attention_workspace_bytes(*args)) return SPARCML_ERR_WORKSPACE;
+  if (args->batch == 0 || args->queries == 0) return SPARCML_OK;
+  return from_hip(sparcml::attention_launch(*args, ws, stream));
+}
+
+size_t sparcml_attention_backward_workspace(const sparcml_attention_args* args) {
+  return args && attention_sizes_ok(*args) ? sparcml::attention_backward_workspace_bytes(*args) : 0;
+}
+
+sparcml_status sparcml_attention_backward(const sparcml_attention_args* args, void* ws, size_t ws_bytes,
+                                          hipStream_t stream) {
+  if (!args || !attention_args_ok(*args, true)) return SPARCML_ERR_INVALID_ARG;
+  if (!ws || !aligned256(ws) || ws_bytes < sparcml::attention_backward_workspace_bytes(*args))
+    return SPARCML_ERR_WORKSPACE;
+  if (args->batch == 0) return SPARCML_OK;
+  return from_hip(sparcml::attention_backward_launch(*args, ws, stream));
+}
+
+// --------------------------------------------------------------------------
 sparcml_status sparcml_momentum_step(uint64_t N, const sparcml_reduce_result* d_result, const uint32_t* idx,
                                      uint64_t idx_cap, const float* val, float* momentum, float mu, float scale,
                                      uint32_t nesterov, uint32_t update_type, void* update, hipStream_t stream) {

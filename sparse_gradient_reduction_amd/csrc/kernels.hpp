@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "sparcml.h"
+
 namespace sparcml {
 
 // Measurement only: events a sparcml_bench_* call attaches to kernel
@@ -134,6 +136,23 @@ hipError_t layer_norm_backward_launch(uint32_t type, uint32_t nodes, uint64_t ro
                                       uint64_t dres_stride, const float* weight, const float* mean, const float* rstd,
                                       void* dx, float* dweight, uint64_t dw_stride, float* dbias, uint64_t db_stride,
                                       void* ws, hipStream_t stream);
+
+// sums of part [nodes][chunks][2][cols] over the chunks, to row p of first and second (null: not wanted)
+hipError_t join_chunks_launch(uint32_t nodes, uint32_t cols, uint32_t chunks, const float* part, float* first,
+                              uint64_t first_stride, float* second, uint64_t second_stride, hipStream_t stream);
+
+// ---- norms of queries and keys with the rotation (strides in elements) --------
+constexpr uint32_t kHeadNormDim = 256;  // elements of the widest head
+hipError_t head_norm_rotate_launch(const sparcml_head_norm_args& g, hipStream_t stream);
+size_t head_norm_rotate_backward_workspace_bytes(uint32_t nodes, uint64_t tokens, uint32_t dim);
+hipError_t head_norm_rotate_backward_launch(const sparcml_head_norm_args& g, void* ws, hipStream_t stream);
+
+// ---- attention ------------------------------------------------------------------
+constexpr uint32_t kAttentionDim = 128;  // elements of the widest head
+size_t attention_workspace_bytes(const sparcml_attention_args& a);
+hipError_t attention_launch(const sparcml_attention_args& a, void* ws, hipStream_t stream);
+size_t attention_backward_workspace_bytes(const sparcml_attention_args& a);
+hipError_t attention_backward_launch(const sparcml_attention_args& a, void* ws, hipStream_t stream);
 
 // ---- momentum from a reduction's result (update: null if not wanted) --------
 hipError_t momentum_launch(uint64_t N, const ReduceResultDev* result, const uint32_t* idx, uint64_t idx_cap,

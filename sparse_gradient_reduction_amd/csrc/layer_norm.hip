@@ -443,11 +443,16 @@ hipError_t layer_norm_backward_launch(uint32_t type, uint32_t nodes, uint64_t ro
       e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
-    const uint64_t items = (uint64_t)((cols + 63) / 64) * nodes * 2;
-    hipLaunchKernelGGL(k_join_chunks, dim3((uint32_t)std::min<uint64_t>(items, 4 * kBlocks)), dim3(kSlices * 64), 0,
-                       stream, nodes, cols, chunks, part, dweight, dw_stride, dbias, db_stride);
-    return hipGetLastError();
+    return join_chunks_launch(nodes, cols, chunks, part, dweight, dw_stride, dbias, db_stride, stream);
   });
+}
+
+hipError_t join_chunks_launch(uint32_t nodes, uint32_t cols, uint32_t chunks, const float* part, float* first,
+                              uint64_t first_stride, float* second, uint64_t second_stride, hipStream_t stream) {
+  const uint64_t items = (uint64_t)((cols + 63) / 64) * nodes * 2;
+  hipLaunchKernelGGL(k_join_chunks, dim3((uint32_t)std::min<uint64_t>(items, 4 * kBlocks)), dim3(kSlices * 64), 0,
+                     stream, nodes, cols, chunks, part, first, first_stride, second, second_stride);
+  return hipGetLastError();
 }
 
 }  // namespace sparcml
