@@ -646,7 +646,9 @@ sparcml_status sparcml_head_norm_rotate_backward(const sparcml_head_norm_args* a
  *   dq, dk, dv  device, typed, like q, k, v (backward)
  *   ws          device workspace of sparcml_attention_workspace(args) or
  *               sparcml_attention_backward_workspace(args) bytes, which read
- *               the sizes only, 256-byte aligned; content does not matter
+ *               sizes, mask and type only (what is enough without a mask is
+ *               enough with any), 256-byte aligned; content does not matter;
+ *               NULL where that is 0
  * Nothing written may overlap anything else. With 16-bit types the products'
  * probabilities and ds are rounded to the type, their sums are fp32; with fp32
  * nothing is rounded further. Keys and values that some query of a sequence sees

@@ -836,11 +836,11 @@ _NO_HEADS = (0, 0, 0, 0)
 
 
 def _head_tensor(t: torch.Tensor, dtype, shape, device, name: str):
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or not t.is_cuda:
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda or t.device != device:
         raise TypeError(f"{name} must be a {dtype} tensor on {device if device.type == 'cuda' else 'a GPU'}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.stride(-1) != 1 and shape[-1] > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
 
 
@@ -863,9 +863,12 @@ def _output_heads(t: Optional[torch.Tensor], like: torch.Tensor, name: str) -> t
     return t if t.numel() == 0 else _apart(t, name)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _on(device, call, *args) -> int:
     """call(*args, the current stream of `device`) with that device the current one."""
-    if torch.cuda.current_device() == device.index:
+    if _current_device() == device.index:
         return call(*args, _stream(device))
     with torch.cuda.device(device):
         return call(*args, _stream(device))
@@ -975,13 +978,14 @@ def head_norm_rotate_backward(dq: torch.Tensor, dk: torch.Tensor, q: torch.Tenso
         dq_weight, qs = _node_rows(dq_weight, nodes, cols, q, "dq_weight")
         dk_weight, ks = _node_rows(dk_weight, nodes, cols, q, "dk_weight")
     L = _load()
-    workspace = _workspace(workspace, L.sparcml_head_norm_rotate_backward_workspace(nodes, tokens // nodes, cols), q)
+    ws, n, workspace = _call_workspace(
+        workspace, L.sparcml_head_norm_rotate_backward_workspace(nodes, tokens // nodes, cols), q)
     args = _HEAD_NORM_ARGS.pack(t, nodes, heads, groups, cols, rotated, interleaved, eps, tokens // nodes,
                                 *_token_heads(q, "q"), *_token_heads(k, "k"), *_token_heads(q_out, "q_out"),
                                 *_token_heads(k_out, "k_out"), _ptr(q_weight) or 0, _ptr(k_weight) or 0,
                                 _ptr(positions) or 0, _ptr(frequencies) or 0, *_token_heads(dq, "dq"),
                                 *_token_heads(dk, "dk"), dq_weight.data_ptr(), dk_weight.data_ptr(), qs, ks)
-    st = _on(q.device, L.sparcml_head_norm_rotate_backward, args, workspace.data_ptr(), workspace.numel())
+    st = _on(q.device, L.sparcml_head_norm_rotate_backward, args, ws, n)
     _raise(st, "sparcml_head_norm_rotate_backward")
     return q_out, k_out, dq_weight, dk_weight
 
@@ -991,12 +995,13 @@ def _attention_checks(q, k, v, causal, window, scale, q_lengths, k_lengths):
     """The first words of sparcml_attention_args: sizes, mask, scale and lengths."""
     if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or q.dim() != 4 or k.dim() != 4:
         raise TypeError("q, k and v must be tensors of [batch, tokens, heads, D]")
-    batch, queries, heads, cols = q.shape
-    keys, groups = k.shape[1], k.shape[2]
-    dev = q.device
-    _head_tensor(q, q.dtype, q.shape, dev, "q")
-    _head_tensor(k, q.dtype, (batch, keys, groups, cols), dev, "k")
-    _head_tensor(v, q.dtype, (batch, keys, groups, cols), dev, "v")
+    shape, dtype, dev = q.shape, q.dtype, q.device
+    batch, queries, heads, cols = shape
+    _, keys, groups, _ = k.shape
+    _head_tensor(q, dtype, shape, dev, "q")
+    shape = (batch, keys, groups, cols)
+    _head_tensor(k, dtype, shape, dev, "k")
+    _head_tensor(v, dtype, shape, dev, "v")
     if batch > 65535 or max(queries, keys) >= 1 << 29 or max(heads, groups) > 65535 or not 1 <= cols <= 128:
         raise ValueError("up to 65535 sequences and heads of 1 to 128 elements, fewer than 2^29 queries and keys")
     if groups < 1 or heads < 1 or heads % groups:
@@ -1013,7 +1018,7 @@ def _attention_checks(q, k, v, causal, window, scale, q_lengths, k_lengths):
             if t.device != dev or t.numel() != batch:
                 raise ValueError(f"{name} must have {batch} elements on {dev}")
     before = 0xFFFFFFFF if window is None else min(window - 1, 0xFFFFFFFF)
-    return (_type(q.dtype, "q"), batch, queries, keys, heads, groups, cols, before, 0 if causal else before, scale,
+    return (_type(dtype, "q"), batch, queries, keys, heads, groups, cols, before, 0 if causal else before, scale,
             _ptr(q_lengths) or 0, _ptr(k_lengths) or 0)
 
 
@@ -1022,9 +1027,19 @@ def _batch_heads(t: torch.Tensor):
     return t.data_ptr(), b, n, h
 
 
+def _call_workspace(t: Optional[torch.Tensor], need: int, like: torch.Tensor):
+    """(address, bytes) of the caller's workspace or a new one, and the tensor that keeps it."""
+    if t is None and need == 0:
+        return 0, 0, None
+    t = _workspace(t, need, like)
+    if t.device != like.device:
+        raise ValueError(f"workspace must be on {like.device}")
+    return t.data_ptr(), t.numel(), t
+
+
 def attention_workspace_bytes(q: torch.Tensor, k: torch.Tensor, backward: bool = False) -> int:
-    """Bytes of the workspace that attention or, `backward`, attention_backward
-    needs for queries and keys like these."""
+    """Bytes of the workspace that is enough for attention or, `backward`,
+    attention_backward of queries and keys like these, whatever the mask."""
     args = _ATTENTION_ARGS.pack(*_attention_checks(q, k, k, False, None, None, None, None), *([0] * 33))
     return int((_load().sparcml_attention_backward_workspace if backward else _load().sparcml_attention_workspace)(args))
 
@@ -1045,13 +1060,22 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
     1 / sqrt(D) if none is given."""
     head = _attention_checks(q, k, v, causal, window, scale, q_lengths, k_lengths)
     out = _output_heads(out, q, "out")
-    lse = _given(lse, q, "lse", (head[1], head[4], head[2]), torch.float32)
+    if lse is None:
+        lse = q.new_empty((head[1], head[4], head[2]), dtype=torch.float32)
+    else:
+        _check_lse(lse, head, q)
     args = _ATTENTION_ARGS.pack(*head, *_batch_heads(q), *_batch_heads(k), *_batch_heads(v), *_batch_heads(out),
                                 lse.data_ptr(), *_NO_HEADS, *_NO_HEADS, *_NO_HEADS, *_NO_HEADS)
     L = _load()
-    workspace = _workspace(workspace, L.sparcml_attention_workspace(args), q)
-    _raise(_on(q.device, L.sparcml_attention, args, workspace.data_ptr(), workspace.numel()), "sparcml_attention")
+    ws, n, workspace = _call_workspace(workspace, L.sparcml_attention_workspace(args), q)
+    _raise(_on(q.device, L.sparcml_attention, args, ws, n), "sparcml_attention")
     return out, lse
+
+
+def _check_lse(lse, head, q):
+    _check_dev(lse, torch.float32, "lse")
+    if lse.shape != (head[1], head[4], head[2]) or lse.device != q.device:
+        raise ValueError(f"lse must have shape {(head[1], head[4], head[2])} on {q.device}")
 
 
 def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
@@ -1069,16 +1093,14 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     head = _attention_checks(q, k, v, causal, window, scale, q_lengths, k_lengths)
     _head_tensor(dout, q.dtype, q.shape, q.device, "dout")
     _head_tensor(out, q.dtype, q.shape, q.device, "out")
-    _check_dev(lse, torch.float32, "lse")
-    if lse.shape != (head[1], head[4], head[2]) or lse.device != q.device:
-        raise ValueError(f"lse must have shape {(head[1], head[4], head[2])} on {q.device}")
+    _check_lse(lse, head, q)
     dq, dk, dv = _output_heads(dq, q, "dq"), _output_heads(dk, k, "dk"), _output_heads(dv, v, "dv")
     args = _ATTENTION_ARGS.pack(*head, *_batch_heads(q), *_batch_heads(k), *_batch_heads(v), *_batch_heads(out),
                                 lse.data_ptr(), *_batch_heads(dout), *_batch_heads(dq), *_batch_heads(dk),
                                 *_batch_heads(dv))
     L = _load()
-    workspace = _workspace(workspace, L.sparcml_attention_backward_workspace(args), q)
-    st = _on(q.device, L.sparcml_attention_backward, args, workspace.data_ptr(), workspace.numel())
+    ws, n, workspace = _call_workspace(workspace, L.sparcml_attention_backward_workspace(args), q)
+    st = _on(q.device, L.sparcml_attention_backward, args, ws, n)
     _raise(st, "sparcml_attention_backward")
     return dq, dk, dv
 

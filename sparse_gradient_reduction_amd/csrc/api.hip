@@ -501,7 +501,8 @@ size_t sparcml_attention_workspace(const sparcml_attention_args* args) {
 
 sparcml_status sparcml_attention(const sparcml_attention_args* args, void* ws, size_t ws_bytes, hipStream_t stream) {
   if (!args || !attention_args_ok(*args, false)) return SPARCML_ERR_INVALID_ARG;
-  if (!ws || !aligned256(ws) || ws_bytes < sparcml::attention_workspace_bytes(*args)) return SPARCML_ERR_WORKSPACE;
+  const size_t need = sparcml::attention_workspace_bytes(*args);
+  if (need > 0 && (!ws || !aligned256(ws) || ws_bytes < need)) return SPARCML_ERR_WORKSPACE;
   if (args->batch == 0 || args->queries == 0) return SPARCML_OK;
   return from_hip(sparcml::attention_launch(*args, ws, stream));
 }
@@ -513,8 +514,8 @@ size_t sparcml_attention_backward_workspace(const sparcml_attention_args* args) 
 sparcml_status sparcml_attention_backward(const sparcml_attention_args* args, void* ws, size_t ws_bytes,
                                           hipStream_t stream) {
   if (!args || !attention_args_ok(*args, true)) return SPARCML_ERR_INVALID_ARG;
-  if (!ws || !aligned256(ws) || ws_bytes < sparcml::attention_backward_workspace_bytes(*args))
-    return SPARCML_ERR_WORKSPACE;
+  const size_t need = sparcml::attention_backward_workspace_bytes(*args);
+  if (need > 0 && (!ws || !aligned256(ws) || ws_bytes < need)) return SPARCML_ERR_WORKSPACE;
   if (args->batch == 0) return SPARCML_OK;
   return from_hip(sparcml::attention_backward_launch(*args, ws, stream));
 }

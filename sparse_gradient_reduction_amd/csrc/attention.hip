@@ -64,7 +64,7 @@ __device__ __forceinline__ T* at(const sparcml_heads& x, uint64_t b, uint64_t t,
 // A result's lane has column lane % 32 and rows 8 (r / 4) + 4 h + r % 4.
 template <class T>
 struct Mma {
-  static constexpr int STEP = 16;
+  static constexpr int STEP = 16, MULS = 1;  // MULS: instructions to a mul
   typedef T Frag __attribute__((ext_vector_type(8)));
   typedef T Four __attribute__((ext_vector_type(4)));
   static __device__ __forceinline__ Acc mul(Frag a, Frag b, Acc c);
@@ -86,7 +86,7 @@ __device__ __forceinline__ Acc Mma<f16>::mul(Frag a, Frag b, Acc c) {
 }
 template <>
 struct Mma<float> {
-  static constexpr int STEP = 8;
+  static constexpr int STEP = 8, MULS = 4;
   typedef float Frag __attribute__((ext_vector_type(4)));
   static __device__ __forceinline__ Acc mul(Frag a, Frag b, Acc c) {
 #pragma unroll
@@ -98,11 +98,29 @@ struct Mma<float> {
   }
 };
 
+// Closes a stretch of code whose `muls` matrix instructions are to be issued
+// with `reads` LDS reads, early, and `others` vector instructions between them.
+template <int muls, int reads, int others>
+__device__ __forceinline__ void interleave() {
+  constexpr int R = (reads + muls - 1) / muls + 1, V = (others + muls - 1) / muls;
+#pragma unroll
+  for (int k = 0; k < muls; ++k) {
+    __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
+    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+    if constexpr (V > 0) __builtin_amdgcn_sched_group_barrier(0x2, V, 0);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // ---- tiles in LDS ---------------------------------------------------------------
-// ROWS heads of DP elements, 16-byte chunks, W elements a row; the chunks of a
-// row are exchanged in an order that differs between the rows that are read at
-// once: 8 rows' chunk c (a 16-byte read of 8 lanes) and 4 rows' 32 bytes (a
-// turned read of 16 lanes) are in different banks.
+// ROWS heads of DP elements, W elements a row, in 16-byte chunks; row r's chunk
+// c is at c ^ order(r). LDS serves 256 bytes at a time, from 64 banks: a chunk
+// of 16 rows (a 16-byte read's quarter), and 64 bytes of 4 rows (half of a read
+// that turns 16-bit values), have to be in different banks. With 16-bit values
+// order takes a row's lowest bits to the chunk's highest for the latter and the
+// next ones below for the former; with rows of 2 to the 256 bytes, the lowest
+// bit is in the place already. fp32's columns are 32 neighbours of 2 rows,
+// rows 4 apart; its rows are two to a bank, as its products take 8 times as long.
 template <class T, int DP, int ROWS_>
 struct Tile {
   typedef Mma<T> M;
@@ -110,31 +128,46 @@ struct Tile {
   static constexpr int ROWS = ROWS_, W = DP <= 64 ? 64 : 128, CH = W * (int)sizeof(T) / 16, SIZE = ROWS * CH;
   static constexpr int STEPS = DP / M::STEP, PACK = 16 / (int)sizeof(T);
 
-  static __device__ __forceinline__ int order(int row) { return CH == 8 ? (row >> 1 & 3) << 1 : (row & 7) << 1; }
+  static __device__ __forceinline__ int order(int row) {
+    if (sizeof(T) == 4) return (row & 7) << 1;
+    return CH == 8 ? (row >> 1 & 1) << 2 | (row >> 2 & 3) : (row & 3) << 2 | (row >> 2 & 3);
+  }
 
+  // A lane's byte offsets into a tile: of step 0 of its row, of its column 0.
+  // The others differ from them in single bits, which exclusive ors set. They
+  // are made new to the compiler where a tile's products begin, so that it does
+  // not keep a register for each place it can compute ahead.
+  struct Places {
+    int row, column;
+    __device__ __forceinline__ Places() {
+      const int lane = lane_id(), h = lane / 32, r = lane % 32;
+      row = (r * CH + (h ^ order(r))) * 16;
+      if constexpr (sizeof(T) == 2) {  // 4 rows of 16 columns turn to 16 lanes of 4 rows
+        const int i = lane % 16, v = 4 * h + i / 4;
+        column = (v * CH + ((lane / 16 % 2 * 2 + i % 4 / 2) ^ order(v))) * 16 + i % 2 * 8;
+      } else {
+        column = (4 * h * CH + (r / 4 ^ order(4 * h))) * 16 + r % 4 * 4;
+      }
+    }
+    __device__ __forceinline__ void make_new() { asm volatile("" : "+v"(row), "+v"(column)); }
+  };
   // step s of row `base` + lane % 32 (base a multiple of 32)
-  static __device__ __forceinline__ Frag row(const I4* lds, int base, int s) {
-    const int r = lane_id() % 32, h = lane_id() / 32;
-    return __builtin_bit_cast(Frag, lds[(base + r) * CH + ((2 * s + h) ^ order(r))]);
+  static __device__ __forceinline__ Frag row(const I4* lds, const Places& at, int base, int s) {
+    return *reinterpret_cast<const Frag*>(reinterpret_cast<const char*>(lds) + (at.row ^ s << 5) + base * CH * 16);
   }
   // column 32 t + lane % 32 of rows base + s * STEP .. (base a multiple of 32)
-  static __device__ __forceinline__ Frag column(const I4* lds, int base, int s, int t) {
-    const int lane = lane_id(), h = lane / 32;
+  static __device__ __forceinline__ Frag column(const I4* lds, const Places& at, int base, int s, int t) {
+    const char* p = reinterpret_cast<const char*>(lds) + (base + M::STEP * s) * CH * 16;
     if constexpr (sizeof(T) == 2) {
       typedef short S4 __attribute__((ext_vector_type(4)));
-      const int i = lane % 16, r = 4 * h + i / 4, c = 4 * t + lane / 16 % 2 * 2 + i % 4 / 2;
       typedef __attribute__((address_space(3))) S4 L;
-      const char* p = reinterpret_cast<const char*>(lds + (base + 16 * s + r) * CH + (c ^ order(r))) + i % 2 * 8;
-      const S4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L*)p);
-      const S4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L*)(p + 8 * CH * 16));
+      const S4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L*)(p + (at.column ^ t << 6)));
+      const S4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L*)(p + (at.column ^ t << 6 ^ 32) + 8 * CH * 16));
       return __builtin_bit_cast(Frag, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
       Frag f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = 4 * h + j, d = 32 * t + lane % 32;
-        f[j] = reinterpret_cast<const float*>(lds + (base + 8 * s + r) * CH + (d / 4 ^ order(r)))[d % 4];
-      }
+      for (int j = 0; j < 4; ++j) f[j] = *reinterpret_cast<const float*>(p + (at.column ^ t << 7 ^ j << 5) + j * CH * 16);
       return f;
     }
   }
@@ -157,50 +190,73 @@ __device__ __forceinline__ void wait_and_meet() {
   asm volatile("" ::: "memory");
 }
 
+// The same, but for the loads from memory.
+__device__ __forceinline__ void meet() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(15 | 3 << 14 | 7 << 4);  // lgkmcnt 0
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // Loads of a tile's rows by NT threads, 16 bytes a thread at a time. What is
 // not there (past a head's end, past the last query or key) becomes 0 and is
 // not read. DIRECT: memory to LDS, for heads on 16-byte borders whose rows are
-// within 2^31 bytes of the tile's first; otherwise through registers.
-template <class T, class TL, int NT, bool DIRECT>
+// within 2^31 bytes of the tile's first; otherwise through registers. PACKED:
+// rows as `pk` has them, else one a key.
+template <class T, class TL, int NT, bool DIRECT, bool PACKED>
 struct Loader {
-  static constexpr int N = TL::SIZE / NT;
-  static_assert(TL::SIZE % NT == 0, "whole chunks to a thread");
+  static constexpr int N = TL::SIZE / NT, STEP = NT / TL::CH, KEPT = PACKED ? N : 1;
+  static_assert(TL::SIZE % NT == 0 && NT % TL::CH == 0, "whole chunks to a thread, whole rows to a turn");
   static constexpr int kNothing = 0x7FFFFFF0;  // past the records
-  int offset[N], query[N];  // bytes from the tile's first row; its query, past all of them where it is never there
+  // of each turn (not PACKED: of the first, the others being STEP rows further
+  // each, at the same chunk): bytes from the tile's first row, and its query or
+  // key, past all of them where it is never there
+  int offset[KEPT], query[KEPT];
   uint64_t token, head;
-  uint32_t hp, dim;
+  uint32_t dim;
+  int all;  // queries or keys of a tile
 
   __device__ __forceinline__ Loader(const sparcml_heads& x, const Packing& pk, uint32_t dim_)
-      : token(x.token), head(x.head), hp(pk.hp), dim(dim_) {
+      : token(x.token), head(x.head), dim(dim_), all(PACKED ? pk.ip : TL::ROWS) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const uint32_t c = k * NT + threadIdx.x, row = c / TL::CH, i = row / pk.hp, h = row % pk.hp;
+    for (int k = 0; k < KEPT; ++k) {
+      const uint32_t c = k * NT + threadIdx.x, row = c / TL::CH;
+      const uint32_t i = PACKED ? row / pk.hp : row, h = PACKED ? row % pk.hp : 0;
       const uint32_t e = (c % TL::CH ^ TL::order(row)) * TL::PACK;
-      query[k] = i < pk.ip && e < dim ? (int)i : 1 << 30;
-      offset[k] = DIRECT ? (int)((i * token + h * head + e) * sizeof(T)) : (int)(h << 8 | e);
+      const bool never = i >= (uint32_t)all || e >= dim;
+      query[k] = never ? 1 << 30 : (int)i;
+      offset[k] = !DIRECT ? (int)(h << 8 | e) : never ? kNothing : (int)((i * token + h * head + e) * sizeof(T));
     }
   }
   // the queries or keys from .. to - 1, counted from the tile's first one
   __device__ __forceinline__ void load(const T* base, int from, int to, I4* lds) const {
     if constexpr (DIRECT) {
-#if __HIP_DEVICE_COMPILE__  // the host's pass has no such type, and would leave the kernel out
-      const auto memory = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base), 0, kNothing, 0x00027000);
-      const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-#pragma unroll
-      for (int k = 0; k < N; ++k)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            memory, (__attribute__((address_space(3))) void*)(lds + k * NT + wave * kWave), 16,
-            query[k] >= from && query[k] < to ? offset[k] : kNothing, 0, 0, 0);
-#endif
+      if (from <= 0 && to >= all) turns<true>(base, from, to, lds);
+      else turns<false>(base, from, to, lds);
     } else {
 #pragma unroll
       for (int k = 0; k < N; ++k) {
         typename Pack<T>::V v = {};
-        const int e = offset[k] & 255;
-        if (query[k] >= from && query[k] < to) v = load_pack(base + query[k] * token + (offset[k] >> 8) * head + e, (int64_t)dim - e);
+        const int q = PACKED ? query[k] : query[0] + k * STEP, x = offset[PACKED ? k : 0], e = x & 255;
+        if (q >= from && q < to) v = load_pack(base + q * token + (x >> 8) * head + e, (int64_t)dim - e);
         lds[k * NT + threadIdx.x] = __builtin_bit_cast(I4, v);
       }
     }
+  }
+  template <bool WHOLE>
+  __device__ __forceinline__ void turns(const T* base, int from, int to, I4* lds) const {
+#if __HIP_DEVICE_COMPILE__  // the host's pass has no such type, and would leave the kernel out
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const T* first = PACKED ? base : base + k * STEP * token;
+      const int q = PACKED ? query[k] : query[0] + k * STEP, x = offset[PACKED ? k : 0];
+      const auto memory = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(first), 0, kNothing, 0x00027000);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          memory, (__attribute__((address_space(3))) void*)(lds + k * NT + wave * kWave), 16,
+          WHOLE || (q >= from && q < to) ? x : kNothing, 0, 0, 0);
+    }
+#endif
   }
 };
 
@@ -226,10 +282,8 @@ struct Rows {
   int first, last;        // some row of the workgroup sees these; last < first: none does
   __device__ __forceinline__ Rows(const Args& a, const Sequence& s, const Packing& pk, uint32_t tile, uint32_t g) {
     const uint32_t wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const uint32_t r = wid * 32 + lane_id() % 32, q = r / pk.hp;
+    place(a, pk, tile, g, wid * 32 + lane_id() % 32);
     const int i0 = tile / pk.nh * pk.ip;
-    i = i0 + q, head = g * (a.heads / a.groups) + tile % pk.nh * pk.hp + r % pk.hp;
-    there = q < pk.ip && i < (int)a.queries;
     lo = s.first(i), span = s.last(i) - lo;
     live = there && i < s.n && (int)span >= 0;
     if (!live) lo = 1 << 30, span = 0;
@@ -239,15 +293,47 @@ struct Rows {
     wave_all_first = s.first(w1), wave_all_last = s.last(w0);
     first = s.first(i0), last = i0 <= i1 ? s.last(i1) : -1;
   }
+  // part `part` of `parts` of the keys, in whole tiles of BN
+  template <int BN>
+  __device__ __forceinline__ void take(uint32_t part, uint32_t parts) {
+    if (parts == 1 || last < first) return;
+    const int tiles = (last - first) / BN + 1, each = (tiles + parts - 1) / parts * BN;
+    const int64_t from = first + (int64_t)part * each;
+    last = min((int64_t)last, from + each - 1);
+    first = min(from, (int64_t)last + 1);
+  }
+  __device__ __forceinline__ Rows() {}
+  // row r of the tile
+  __device__ __forceinline__ void place(const Args& a, const Packing& pk, uint32_t tile, uint32_t g, uint32_t r) {
+    i = tile / pk.nh * pk.ip + r / pk.hp;
+    head = g * (a.heads / a.groups) + tile % pk.nh * pk.hp + r % pk.hp;
+    there = r / pk.hp < pk.ip && i < (int)a.queries;
+  }
 };
 
-// a row of a head, 16 bytes of it to a Frag; 0 past its end
-template <class T, class TL>
-__device__ __forceinline__ void load_row(typename TL::Frag (&f)[TL::STEPS], const T* p, bool there, uint32_t dim) {
+// A row of a head, 16 bytes of it to a Frag; 0 past its end, and where it is
+// not `there`. WHOLE: 16 bytes divide it; what is not there is then read from
+// the tensor's first head instead, which keeps the loads free of branches.
+template <class T, class TL, bool WHOLE>
+__device__ __forceinline__ void load_row(typename TL::Frag (&f)[TL::STEPS], const sparcml_heads& x, uint64_t b,
+                                         int i, uint32_t h, bool there, uint32_t dim) {
+  if constexpr (WHOLE) {
+    const T* p = there ? at<T>(x, b, i, h) : static_cast<const T*>(x.data);
 #pragma unroll
-  for (int s = 0; s < TL::STEPS; ++s) {
-    const int e = (2 * s + lane_id() / 32) * TL::PACK;
-    f[s] = __builtin_bit_cast(typename TL::Frag, load_pack(p + e, there ? (int64_t)dim - e : 0));
+    for (int s = 0; s < TL::STEPS; ++s) {
+      const uint32_t e = (2 * s + lane_id() / 32) * TL::PACK;
+      f[s] = __builtin_bit_cast(typename TL::Frag, *reinterpret_cast<const typename Pack<T>::U*>(p + (e < dim ? e : 0)));
+    }
+#pragma unroll
+    for (int s = 0; s < TL::STEPS; ++s)
+      if (!there || (2 * s + lane_id() / 32) * TL::PACK >= dim) f[s] = typename TL::Frag{};
+  } else {
+    const T* p = at<T>(x, b, i, h);
+#pragma unroll
+    for (int s = 0; s < TL::STEPS; ++s) {
+      const int e = (2 * s + lane_id() / 32) * TL::PACK;
+      f[s] = __builtin_bit_cast(typename TL::Frag, load_pack(p + e, there ? (int64_t)dim - e : 0));
+    }
   }
 }
 
@@ -274,45 +360,60 @@ __device__ __forceinline__ void store_row(const Acc (&acc)[DP / 32], float by, T
     }
 }
 
-constexpr int kKeys = 64;  // keys of a tile, 16-bit; 32 with fp32
+// The same in fp32, DP elements a row, for a later kernel to join.
+template <int DP>
+__device__ __forceinline__ void store_part(const Acc (&acc)[DP / 32], float by, float* p) {
+#pragma unroll
+  for (int t = 0; t < DP / 32; ++t)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<f32x4*>(p + 32 * t + 8 * q + 4 * (lane_id() / 32)) =
+          f32x4{acc[t][4 * q], acc[t][4 * q + 1], acc[t][4 * q + 2], acc[t][4 * q + 3]} * by;
+}
+
+constexpr int kWalked = 32;  // rows of a tile of queries that is walked over
+constexpr int kKeys = 64;    // keys of a tile, 16-bit; 32 with fp32
 template <class T>
 constexpr int keys_of() { return sizeof(T) == 2 ? kKeys : kKeys / 2; }
 
+constexpr int kJoinThreads = 256;
+
 // ---- forward --------------------------------------------------------------------
 template <class T, int DP, int NW, bool DIRECT>
-__global__ __launch_bounds__(NW * kWave, (sizeof(T) == 4 && DP > 64 ? 1 : 2)) void k_attention(Args a, Packing pk, uint32_t tiles) {
+__global__ __launch_bounds__(NW * kWave, (sizeof(T) == 4 && DP > 64 ? 1 : 2)) void k_attention(Args a, Packing pk, uint32_t tiles,
+                                                                         uint32_t parts, float* part) {
   constexpr int BN = keys_of<T>(), NT = NW * kWave;
   typedef Tile<T, DP, BN> TL;
   typedef Mma<T> M;
   __shared__ I4 k0[TL::SIZE], v0[TL::SIZE], k1[TL::SIZE], v1[TL::SIZE];
-  const uint32_t id = xcd_contiguous(blockIdx.x, gridDim.x), bg = id / tiles, tile = tiles - 1 - id % tiles;
+  const uint32_t id = xcd_contiguous(blockIdx.x, gridDim.x), bg = id / parts / tiles, tile = tiles - 1 - id / parts % tiles;
   const uint32_t b = bg / a.groups, g = bg % a.groups;
   const Sequence s(a, b);
-  const Rows<NW> rows(a, s, pk, tile, g);
+  Rows<NW> rows(a, s, pk, tile, g);
+  rows.template take<BN>(id % parts, parts);
   const float c = a.scale * kLog2e;
 
   typename TL::Frag q[TL::STEPS];
-  load_row<T, TL>(q, at<T>(a.q, b, rows.i, rows.head), rows.live, a.dim);
+  load_row<T, TL, DIRECT>(q, a.q, b, rows.i, rows.head, rows.live, a.dim);
   Acc o[DP / 32] = {};
   float top = -INFINITY, sum = 0.0f;
 
   const Packing one{1, BN, 1};
-  const Loader<T, TL, NT, DIRECT> lk(a.k, one, a.dim), lv(a.v, one, a.dim);
+  const Loader<T, TL, NT, DIRECT, false> lk(a.k, one, a.dim), lv(a.v, one, a.dim);
   const T *ks = at<T>(a.k, b, 0, g), *vs = at<T>(a.v, b, 0, g);
   const auto load = [&](int j, I4* kt, I4* vt) {
     lk.load(ks + j * a.k.token, 0, rows.last + 1 - j, kt);
     lv.load(vs + j * a.v.token, 0, rows.last + 1 - j, vt);
   };
-  const auto pass = [&](int j, const I4* kt, const I4* vt, I4* kn, I4* vn) {
-    wait_and_meet();
-    if (j + BN <= rows.last) load(j + BN, kn, vn);
-    if (j > rows.wave_last || j + BN - 1 < rows.wave_first) return;
+  typename TL::Places places;
+  const auto products = [&](auto masked, int j, const I4* kt, const I4* vt) {
+    places.make_new();
     Acc p[BN / 32] = {};
 #pragma unroll
     for (int t = 0; t < BN / 32; ++t)
 #pragma unroll
-      for (int x = 0; x < TL::STEPS; ++x) p[t] = M::mul(TL::row(kt, 32 * t, x), q[x], p[t]);
-    if (j < rows.wave_all_first || j + BN - 1 > rows.wave_all_last) {
+      for (int x = 0; x < TL::STEPS; ++x) p[t] = M::mul(TL::row(kt, places, 32 * t, x), q[x], p[t]);
+    if constexpr (masked) {
       const uint32_t from = j + 4 * (lane_id() / 32) - rows.lo;
 #pragma unroll
       for (int t = 0; t < BN / 32; ++t)
@@ -348,8 +449,15 @@ __global__ __launch_bounds__(NW * kWave, (sizeof(T) == 4 && DP > 64 ? 1 : 2)) vo
       for (int x = 0; x < 32 / M::STEP; ++x) {
         const typename TL::Frag f = M::frag(p[t], x);
 #pragma unroll
-        for (int y = 0; y < DP / 32; ++y) o[y] = M::mul(TL::column(vt, 32 * t, x, y), f, o[y]);
+        for (int y = 0; y < DP / 32; ++y) o[y] = M::mul(TL::column(vt, places, 32 * t, x, y), f, o[y]);
       }
+  };
+  const auto pass = [&](int j, const I4* kt, const I4* vt, I4* kn, I4* vn) {
+    wait_and_meet();
+    if (j + BN <= rows.last) load(j + BN, kn, vn);
+    if (j > rows.wave_last || j + BN - 1 < rows.wave_first) return;
+    if (j < rows.wave_all_first || j + BN - 1 > rows.wave_all_last) products(std::true_type{}, j, kt, vt);
+    else products(std::false_type{}, j, kt, vt);
   };
   if (rows.first <= rows.last) load(rows.first, k0, v0);
   for (int j = rows.first; j <= rows.last; j += 2 * BN) {
@@ -358,8 +466,80 @@ __global__ __launch_bounds__(NW * kWave, (sizeof(T) == 4 && DP > 64 ? 1 : 2)) vo
   }
   sum = rows.live ? both_halves_sum(sum) : 0.0f;
   if (!rows.there) return;
+  if (parts > 1) {
+    const uint64_t row = (uint64_t)id * (NW * 32) + threadIdx.x / kWave * 32 + lane_id() % 32;
+    if (lane_id() < 32) reinterpret_cast<float2*>(part)[row] = make_float2(top, sum);
+    store_part<DP>(o, 1.0f, part + (uint64_t)gridDim.x * (NW * 32) * 2 + row * DP);
+    return;
+  }
   store_row<T, DP>(o, sum == 0.0f ? 0.0f : 1.0f / sum, at<T>(a.out, b, rows.i, rows.head), a.dim);
   if (lane_id() < 32) a.lse[((uint64_t)b * a.heads + rows.head) * a.queries + rows.i] = sum == 0.0f ? -INFINITY : top * kLn2 + logf(sum);
+}
+
+// Where a thread of a joining kernel is: a wave joins row r of the ROWS of a
+// tile, L lanes of 4 elements, from e on, taking every SLICES-th part.
+template <int DP, int ROWS>
+struct Joined {
+  static constexpr int L = DP <= 32 ? 8 : DP <= 64 ? 16 : 32, SLICES = kWave / L;
+  uint64_t row;
+  uint32_t id, r, e, slice;
+  __device__ __forceinline__ Joined() {
+    row = (uint64_t)blockIdx.x * (kJoinThreads / kWave) + threadIdx.x / kWave;
+    id = row / ROWS, r = row % ROWS, e = lane_id() % L * 4, slice = lane_id() / L;
+  }
+  static uint32_t blocks(uint64_t rows) { return (uint32_t)(rows / (kJoinThreads / kWave)); }
+  static __device__ __forceinline__ float sum(float v) {
+#pragma unroll
+    for (int d = L; d < kWave; d <<= 1) v += __shfl_xor(v, d, kWave);
+    return v;
+  }
+  static __device__ __forceinline__ f32x4 sum(f32x4 v) { return f32x4{sum(v[0]), sum(v[1]), sum(v[2]), sum(v[3])}; }
+  template <class T>
+  __device__ __forceinline__ void store(f32x4 o, T* p, uint32_t dim) const {
+    typedef T Four __attribute__((ext_vector_type(4)));
+    typedef Four Any __attribute__((aligned(sizeof(T))));
+    if (e + 4 <= dim) {
+      Four v;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = from_f32<T>(o[j]);
+      *reinterpret_cast<Any*>(p + e) = v;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 3; ++j)
+        if (e + j < dim) p[e + j] = from_f32<T>(o[j]);
+    }
+  }
+};
+
+// Joins the parts of a row: out = sum of 2^(top - most) o, over the sum of 2^(top
+// - most) sum.
+template <class T, int DP, int NW>
+__global__ __launch_bounds__(kJoinThreads) void k_attention_join(Args a, Packing pk, uint32_t tiles, uint32_t parts,
+                                                                 const float* part) {
+  constexpr int ROWS = NW * 32;
+  const Joined<DP, ROWS> in;
+  const uint64_t all = (uint64_t)tiles * a.batch * a.groups * ROWS;
+  const uint32_t bg = in.id / tiles, b = bg / a.groups;
+  Rows<NW> rows;
+  rows.place(a, pk, tiles - 1 - in.id % tiles, bg % a.groups, in.r);
+  if (!rows.there) return;
+  const float2* tops = reinterpret_cast<const float2*>(part) + (uint64_t)in.id * parts * ROWS + in.r;
+  const float* os = part + all * parts * 2 + ((uint64_t)in.id * parts * ROWS + in.r) * DP + in.e;
+  float most = -INFINITY, sum = 0.0f;
+  for (uint32_t k = lane_id(); k < parts; k += kWave) most = fmaxf(most, tops[k * ROWS].x);
+  most = wave_max(most);
+  f32x4 o = {};
+#pragma unroll 4
+  for (uint32_t k = in.slice; k < parts; k += in.SLICES) {
+    const float2 t = tops[k * ROWS];
+    const float by = t.x == most ? 1.0f : __builtin_amdgcn_exp2f(t.x - most);
+    sum = fmaf(t.y, by, sum);
+    if (in.e < DP) o += *reinterpret_cast<const f32x4*>(os + (uint64_t)k * ROWS * DP) * by;
+  }
+  sum = in.sum(sum), o = in.sum(o);
+  if (in.slice != 0) return;
+  in.store(o * (sum == 0.0f ? 0.0f : 1.0f / sum), at<T>(a.out, b, rows.i, rows.head), a.dim);
+  if (in.e == 0) a.lse[((uint64_t)b * a.heads + rows.head) * a.queries + rows.i] = sum == 0.0f ? -INFINITY : most * kLn2 + logf(sum);
 }
 
 // ---- backward -------------------------------------------------------------------
@@ -421,28 +601,31 @@ __device__ __forceinline__ float factor_of(const float* norms, uint32_t bg) {
 }
 
 // ---- backward: dq ---------------------------------------------------------------
-// Each row's lse in base 2 less the probabilities' exponent (or +inf, where they
-// are 0) and sum of dout * out go to `stats` ([batch][heads][queries] each) for
-// dk and dv.
+// For dk and dv, what their products take off goes to `stats` ([batch][heads]
+// [queries] each): each row's lse in base 2 less the probabilities' exponent, or
+// +inf where they are 0, with 16-bit types as a score, before its scaling; and
+// its sum of dout * out.
 template <class T, int DP, int NW, bool DIRECT>
-__global__ __launch_bounds__(NW * kWave, ((sizeof(T) == 4 ? DP > 64 : DP > 96) ? 1 : 2)) void k_attention_dq(Args a, Packing pk, uint32_t tiles, float* stats, const float* norms) {
+__global__ __launch_bounds__(NW * kWave, (sizeof(T) == 4 && DP > 64 ? 1 : 2)) void k_attention_dq(Args a, Packing pk, uint32_t tiles, float* stats,
+                                                                            const float* norms, uint32_t parts, float* part) {
   constexpr int BN = keys_of<T>(), NT = NW * kWave;
   typedef Tile<T, DP, BN> TL;
   typedef Mma<T> M;
   __shared__ I4 k0[TL::SIZE], v0[TL::SIZE], k1[TL::SIZE], v1[TL::SIZE];
-  const uint32_t id = xcd_contiguous(blockIdx.x, gridDim.x), bg = id / tiles, tile = tiles - 1 - id % tiles;
+  const uint32_t id = xcd_contiguous(blockIdx.x, gridDim.x), bg = id / parts / tiles, tile = tiles - 1 - id / parts % tiles;
   const uint32_t b = bg / a.groups, g = bg % a.groups;
   const Sequence s(a, b);
-  const Rows<NW> rows(a, s, pk, tile, g);
+  Rows<NW> rows(a, s, pk, tile, g);
+  rows.template take<BN>(id % parts, parts);
   const float c = a.scale * kLog2e;
 
   typename TL::Frag q[TL::STEPS], d[TL::STEPS];
-  load_row<T, TL>(q, at<T>(a.q, b, rows.i, rows.head), rows.live, a.dim);
-  load_row<T, TL>(d, at<T>(a.dout, b, rows.i, rows.head), rows.live, a.dim);
+  load_row<T, TL, DIRECT>(q, a.q, b, rows.i, rows.head, rows.live, a.dim);
+  load_row<T, TL, DIRECT>(d, a.dout, b, rows.i, rows.head, rows.live, a.dim);
   float lse = INFINITY, delta = 0.0f;
   {
     typename TL::Frag f[TL::STEPS];
-    load_row<T, TL>(f, at<T>(a.out, b, rows.i, rows.head), rows.live, a.dim);
+    load_row<T, TL, DIRECT>(f, a.out, b, rows.i, rows.head, rows.live, a.dim);
 #pragma unroll
     for (int x = 0; x < TL::STEPS; ++x)
 #pragma unroll
@@ -450,9 +633,9 @@ __global__ __launch_bounds__(NW * kWave, ((sizeof(T) == 4 ? DP > 64 : DP > 96) ?
     delta = both_halves_sum(delta);
     const uint64_t where = ((uint64_t)b * a.heads + rows.head) * a.queries + rows.i;
     if (rows.live) lse = a.lse[where] * kLog2e - kBoost<T>;
-    if (rows.there && lane_id() < 32) {
-      stats[where] = lse;
-      stats[where + (uint64_t)a.batch * a.heads * a.queries] = delta;
+    if (rows.there && lane_id() < 32 && id % parts == 0) {
+      stats[where] = sizeof(T) == 2 ? -lse / c : -lse;
+      stats[where + (uint64_t)a.batch * a.heads * a.queries] = -delta;
     }
   }
   const float f = factor_of<T>(norms, bg);
@@ -460,156 +643,259 @@ __global__ __launch_bounds__(NW * kWave, ((sizeof(T) == 4 ? DP > 64 : DP > 96) ?
   Acc o[DP / 32] = {};
 
   const Packing one{1, BN, 1};
-  const Loader<T, TL, NT, DIRECT> lk(a.k, one, a.dim), lv(a.v, one, a.dim);
+  const Loader<T, TL, NT, DIRECT, false> lk(a.k, one, a.dim), lv(a.v, one, a.dim);
   const T *ks = at<T>(a.k, b, 0, g), *vs = at<T>(a.v, b, 0, g);
   const auto load = [&](int j, I4* kt, I4* vt) {
     lk.load(ks + j * a.k.token, 0, rows.last + 1 - j, kt);
     lv.load(vs + j * a.v.token, 0, rows.last + 1 - j, vt);
   };
+  typename TL::Places places;
+  const auto products = [&](auto masked, int j, const I4* kt, const I4* vt) {
+    places.make_new();
+    const uint32_t from = j + 4 * (lane_id() / 32) - rows.lo;
+#pragma unroll
+    for (int t = 0; t < BN / 32; ++t) {
+      __builtin_amdgcn_sched_barrier(0);
+      Acc p = {}, e = {};
+#pragma unroll
+      for (int x = 0; x < TL::STEPS; ++x) {
+        p = M::mul(TL::row(kt, places, 32 * t, x), q[x], p);
+        e = M::mul(TL::row(vt, places, 32 * t, x), d[x], e);
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        p[r] = __builtin_amdgcn_exp2f(fmaf(p[r], c, -lse));
+        if constexpr (masked) p[r] = from + (32 * t + 8 * (r / 4) + r % 4) > rows.span ? 0.0f : p[r];
+        p[r] *= kBoost<T> == 0.0f ? e[r] - delta : fmaf(e[r], f, -delta);
+      }
+#pragma unroll
+      for (int x = 0; x < 32 / M::STEP; ++x) {
+        const typename TL::Frag b = M::frag(p, x);
+#pragma unroll
+        for (int y = 0; y < DP / 32; ++y) o[y] = M::mul(TL::column(kt, places, 32 * t, x, y), b, o[y]);
+      }
+    }
+  };
   const auto pass = [&](int j, const I4* kt, const I4* vt, I4* kn, I4* vn) {
     wait_and_meet();
     if (j + BN <= rows.last) load(j + BN, kn, vn);
     if (j > rows.wave_last || j + BN - 1 < rows.wave_first) return;
-    const bool masked = j < rows.wave_all_first || j + BN - 1 > rows.wave_all_last;
-#pragma unroll
-    for (int t = 0; t < BN / 32; ++t) {
-      Acc p = {}, e = {};
-#pragma unroll
-      for (int x = 0; x < TL::STEPS; ++x) {
-        p = M::mul(TL::row(kt, 32 * t, x), q[x], p);
-        e = M::mul(TL::row(vt, 32 * t, x), d[x], e);
-      }
-#pragma unroll
-      for (int r = 0; r < 16; ++r) p[r] = __builtin_amdgcn_exp2f(fmaf(p[r], c, -lse));
-      if (masked) {
-        const uint32_t from = j + 4 * (lane_id() / 32) - rows.lo;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) p[r] = from + (32 * t + 8 * (r / 4) + r % 4) > rows.span ? 0.0f : p[r];
-      }
-#pragma unroll
-      for (int r = 0; r < 16; ++r) p[r] *= kBoost<T> == 0.0f ? e[r] - delta : fmaf(e[r], f, -delta);
-#pragma unroll
-      for (int x = 0; x < 32 / M::STEP; ++x) {
-        const typename TL::Frag f = M::frag(p, x);
-#pragma unroll
-        for (int y = 0; y < DP / 32; ++y) o[y] = M::mul(TL::column(kt, 32 * t, x, y), f, o[y]);
-      }
-    }
+    if (j < rows.wave_all_first || j + BN - 1 > rows.wave_all_last) products(std::true_type{}, j, kt, vt);
+    else products(std::false_type{}, j, kt, vt);
   };
   if (rows.first <= rows.last) load(rows.first, k0, v0);
   for (int j = rows.first; j <= rows.last; j += 2 * BN) {
     pass(j, k0, v0, k1, v1);
     if (j + BN <= rows.last) pass(j + BN, k1, v1, k0, v0);
   }
-  if (rows.there) store_row<T, DP>(o, a.scale / f * exp2f(-kBoost<T>), at<T>(a.dq, b, rows.i, rows.head), a.dim);
+  if (!rows.there) return;
+  const float by = a.scale / f * exp2f(-kBoost<T>);
+  if (parts == 1) store_row<T, DP>(o, by, at<T>(a.dq, b, rows.i, rows.head), a.dim);
+  else store_part<DP>(o, by, part + ((uint64_t)id * (NW * 32) + threadIdx.x / kWave * 32 + lane_id() % 32) * DP);
 }
 
+// The sum of the parts of a row of dq.
+template <class T, int DP, int NW>
+__global__ __launch_bounds__(kJoinThreads) void k_attention_join_dq(Args a, Packing pk, uint32_t tiles, uint32_t parts,
+                                                                    const float* part) {
+  constexpr int ROWS = NW * 32;
+  const Joined<DP, ROWS> in;
+  const uint32_t bg = in.id / tiles;
+  Rows<NW> rows;
+  rows.place(a, pk, tiles - 1 - in.id % tiles, bg % a.groups, in.r);
+  if (!rows.there) return;
+  f32x4 o = {};
+  if (in.e < DP) {
+#pragma unroll 4
+    for (uint32_t k = in.slice; k < parts; k += in.SLICES)
+      o += *reinterpret_cast<const f32x4*>(part + (((uint64_t)in.id * parts + k) * ROWS + in.r) * DP + in.e);
+  }
+  o = in.sum(o);
+  if (in.slice == 0) in.store(o, at<T>(a.dq, bg / a.groups, rows.i, rows.head), a.dim);
+}
+
+
 // ---- backward: dk and dv --------------------------------------------------------
-// A wave has 32 keys and walks over the tiles of queries that see one of the
-// workgroup's.
+// Two waves have 32 keys and walk over the tiles of queries that see one of the
+// workgroup's. One computes the scores, the probabilities and dv, the other dout
+// v^T, ds (from the probabilities that it gets through LDS) and dk: four
+// products shared evenly, and each wave holds one operand and one sum instead of
+// two, so that three waves of 128-element heads fit a SIMD where one would.
 template <class T, int DP, int NW, bool DIRECT>
-__global__ __launch_bounds__(NW * kWave, (DP > 64 ? 1 : 2)) void k_attention_dkv(Args a, Packing pk, uint32_t tiles,
-                                                                 const float* stats, const float* norms) {
-  constexpr int BM = keys_of<T>(), NT = NW * kWave;
+__global__ __launch_bounds__(NW * kWave, (DP > 64 ? 2 : 3)) void k_attention_dkv(
+    Args a, Packing pk, uint32_t tiles, const float* stats, const float* norms, uint32_t parts, float* part) {
+  constexpr int BM = kWalked, NT = NW * kWave, KEYS = NW / 2 * 32;
   typedef Tile<T, DP, BM> TL;
   typedef Mma<T> M;
   __shared__ I4 q0[TL::SIZE], d0[TL::SIZE], q1[TL::SIZE], d1[TL::SIZE];
-  __shared__ float stat[2][2][BM];
-  __shared__ int query[BM];
-  const uint32_t id = xcd_contiguous(blockIdx.x, gridDim.x), bg = id / tiles, tile = id % tiles;
+  __shared__ f32x4 shared[NW / 2][4][kWave];  // a pair's probabilities, as a result's lanes have them
+  __shared__ __align__(16) float stat[2][2][BM];
+  __shared__ uint32_t query[BM];
+  const uint32_t id = xcd_contiguous(blockIdx.x, gridDim.x), bg = id / parts / tiles, tile = id / parts % tiles;
   const uint32_t b = bg / a.groups, g = bg % a.groups, each = a.heads / a.groups;
   const Sequence s(a, b);
   const float c = a.scale * kLog2e;
   const uint32_t wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id();
-  const int j0 = tile * NW * 32, w0 = j0 + wid * 32, j = w0 + lane % 32, end = min(j0 + NW * 32, s.m);
+  const uint32_t pair = wid / 2;
+  const bool second = ((wid ^ blockIdx.x) & 1) != 0;  // waves of a place share a SIMD: both kinds on each
+  const int j0 = tile * KEYS, w0 = j0 + pair * 32, j = w0 + lane % 32, end = min(j0 + KEYS, s.m);
   const bool there = j < (int)a.keys;
 
-  typename TL::Frag k[TL::STEPS], v[TL::STEPS];
-  load_row<T, TL>(k, at<T>(a.k, b, j, g), j < s.m, a.dim);
-  load_row<T, TL>(v, at<T>(a.v, b, j, g), j < s.m, a.dim);
+  typename TL::Frag held[TL::STEPS];  // of k, or of v
+  load_row<T, TL, DIRECT>(held, second ? a.v : a.k, b, j, g, j < s.m, a.dim);
   const float f = factor_of<T>(norms, bg);
-  Acc dk[DP / 32] = {}, dv[DP / 32] = {};
+  Acc sum[DP / 32] = {};  // dv, or dk
 
   // queries first .. last see one of the workgroup's keys
   const int first = max(0, j0 - s.after - s.m + s.n), last = j0 < end ? min(s.n - 1, end - 1 + s.before - s.m + s.n) : -1;
-  const int t0 = first / (int)pk.ip * (int)pk.nh, t1 = last < first ? t0 : (last / (int)pk.ip + 1) * (int)pk.nh;
+  int t0 = first / (int)pk.ip * (int)pk.nh, t1 = last < first ? t0 : (last / (int)pk.ip + 1) * (int)pk.nh;
+  if (parts > 1) {
+    const int64_t each = (t1 - t0 + parts - 1) / parts, from = t0 + id % parts * each;
+    t1 = min((int64_t)t1, from + each);
+    t0 = min(from, (int64_t)t1);
+  }
 
-  const Loader<T, TL, NT, DIRECT> lq(a.q, pk, a.dim), ld(a.dout, pk, a.dim);
+  const Loader<T, TL, NT, DIRECT, true> lq(a.q, pk, a.dim), ld(a.dout, pk, a.dim);
   const int seeing = max(0, s.n - s.m - s.after);  // the first query that sees a key
   const uint32_t my_i = threadIdx.x / pk.hp, my_h = threadIdx.x % pk.hp;
   if (threadIdx.x < BM) query[threadIdx.x] = my_i;
-  const auto load = [&](int t, I4* qt, I4* dt, int turn) {
+  // the rows' lse and delta pass through registers: they are stored when the
+  // tiles' loads, which were asked for after them, have had time
+  const auto stats_of = [&](int t) {
+    const uint32_t h = g * each + t % pk.nh * pk.hp;
+    const int i = t / pk.nh * pk.ip + my_i;
+    float2 v = make_float2(-INFINITY, 0.0f);
+    if (threadIdx.x < BM && my_i < pk.ip && i >= seeing && i < s.n) {
+      const uint64_t where = ((uint64_t)b * a.heads + h + my_h) * a.queries + i;
+      v = make_float2(stats[where], stats[where + (uint64_t)a.batch * a.heads * a.queries]);
+    }
+    return v;
+  };
+  const auto keep = [&](float2 v, int turn) {
+    if (threadIdx.x < BM) {
+      stat[turn][0][threadIdx.x] = v.x;
+      stat[turn][1][threadIdx.x] = v.y;
+    }
+  };
+  const auto load = [&](int t, I4* qt, I4* dt) {
     const uint32_t h = g * each + t % pk.nh * pk.hp;
     const int i0 = t / pk.nh * pk.ip;
     lq.load(at<T>(a.q, b, i0, h), seeing - i0, s.n - i0, qt);
     ld.load(at<T>(a.dout, b, i0, h), seeing - i0, s.n - i0, dt);
-    if (threadIdx.x < BM) {
-      const uint32_t r = threadIdx.x;
-      const int i = i0 + my_i;
-      float lse = INFINITY, delta = 0.0f;
-      if (my_i < pk.ip && i >= seeing && i < s.n) {
-        const uint64_t where = ((uint64_t)b * a.heads + h + my_h) * a.queries + i;
-        lse = stats[where];
-        delta = stats[where + (uint64_t)a.batch * a.heads * a.queries];
+  };
+  typename TL::Places places;
+  // `tile` times the held rows. 16-bit: the sums start from -lse or -delta.
+  const auto rows_product = [&](const I4* tile, const float* from) {
+    places.make_new();
+    Acc p = {};
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(from + 4 * (lane / 32) + 8 * r);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) p[4 * r + x] = v[x];
       }
-      stat[turn][0][r] = lse;
-      stat[turn][1][r] = delta * f;
+    }
+#pragma unroll
+    for (int x = 0; x < TL::STEPS; ++x) p = M::mul(TL::row(tile, places, 0, x), held[x], p);
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const float off = from[4 * (lane / 32) + 8 * (r / 4) + r % 4];
+        p[r] = second ? p[r] + off : fmaf(p[r], c, off);
+      }
+    }
+    return p;
+  };
+  const auto columns_product = [&](const I4* tile, const Acc& p) {
+#pragma unroll
+    for (int x = 0; x < 32 / M::STEP; ++x) {
+      const typename TL::Frag b = M::frag(p, x);
+#pragma unroll
+      for (int y = 0; y < DP / 32; ++y) sum[y] = M::mul(TL::column(tile, places, 0, x, y), b, sum[y]);
     }
   };
   const auto pass = [&](int t, const I4* qt, const I4* dt, I4* qn, I4* dn, int turn) {
     wait_and_meet();
-    if (t + 1 < t1) load(t + 1, qn, dn, turn ^ 1);
+    float2 next = {};
+    if (t > t0) {
+      next = stats_of(t - 1);
+      load(t - 1, qn, dn);
+    }
     const int i0 = t / pk.nh * pk.ip, i1 = min(i0 + (int)pk.ip, s.n) - 1;
-    // keys that the tile's first and last queries see
-    if (w0 > s.last(i1) || min(w0 + 31, end - 1) < s.first(i0) || w0 >= end) return;
-    const bool masked = w0 < s.first(i1) || w0 + 31 > s.last(i0);
+    // some query of the tile sees some key of the pair
+    const bool some = w0 < end && w0 <= s.last(i1) && min(w0 + 31, end - 1) >= s.first(i0);
+    if (!second) {
+      Acc p;
+      if (some) {
+        p = rows_product(qt, stat[turn][0]);
 #pragma unroll
-    for (int u = 0; u < BM / 32; ++u) {
-      Acc p = {}, e = {};
+        for (int r = 0; r < 16; ++r) p[r] = __builtin_amdgcn_exp2f(sizeof(T) == 2 ? p[r] * c : p[r]);
+        if (w0 < s.first(i1) || w0 + 31 > s.last(i0)) {  // not all see all
+          // the key's way from the first one that the tile's first query may see; past all of them where there is no key
+          const uint32_t far = j < s.m ? (uint32_t)(j - i0 - s.m + s.n + s.before) : 0xFFFFFF00u;
+          const uint32_t span = (uint32_t)s.before + (uint32_t)s.after;
 #pragma unroll
-      for (int x = 0; x < TL::STEPS; ++x) {
-        p = M::mul(TL::row(qt, 32 * u, x), k[x], p);
-        e = M::mul(TL::row(dt, 32 * u, x), v[x], e);
+          for (int r = 0; r < 16; ++r) p[r] = far - query[4 * (lane / 32) + 8 * (r / 4) + r % 4] > span ? 0.0f : p[r];
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) shared[pair][r][lane] = f32x4{p[4 * r], p[4 * r + 1], p[4 * r + 2], p[4 * r + 3]};
       }
-      const int h4 = 32 * u + 4 * (lane / 32);
-#pragma unroll
-      for (int r = 0; r < 16; ++r)
-        p[r] = __builtin_amdgcn_exp2f(fmaf(p[r], c, -stat[turn][0][h4 + 8 * (r / 4) + r % 4]));
-      if (masked) {
-        const int far = j - i0 - s.m + s.n;  // from the place of the tile's first query
+      meet();
+      if (some) columns_product(dt, p);
+    } else {
+      Acc e;
+      if (some) e = rows_product(dt, stat[turn][1]);
+      meet();
+      if (some) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          const int ahead = far - query[h4 + 8 * (r / 4) + r % 4];
-          p[r] = ahead > s.after || ahead < -s.before || j >= s.m ? 0.0f : p[r];
+          const float p = shared[pair][r / 4][lane][r % 4];
+          e[r] *= kBoost<T> == 0.0f ? p : p * f;
         }
-      }
-#pragma unroll
-      for (int x = 0; x < 32 / M::STEP; ++x) {
-        const typename TL::Frag f = M::frag(p, x);
-#pragma unroll
-        for (int y = 0; y < DP / 32; ++y) dv[y] = M::mul(TL::column(dt, 32 * u, x, y), f, dv[y]);
-      }
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const float delta = stat[turn][1][h4 + 8 * (r / 4) + r % 4];
-        p[r] *= kBoost<T> == 0.0f ? e[r] - delta : fmaf(e[r], f, -delta);
-      }
-#pragma unroll
-      for (int x = 0; x < 32 / M::STEP; ++x) {
-        const typename TL::Frag f = M::frag(p, x);
-#pragma unroll
-        for (int y = 0; y < DP / 32; ++y) dk[y] = M::mul(TL::column(qt, 32 * u, x, y), f, dk[y]);
+        columns_product(qt, e);
       }
     }
+    keep(next, turn ^ 1);
   };
-  if (t0 < t1) load(t0, q0, d0, 0);
-  for (int t = t0; t < t1; t += 2) {
+  // From the last queries to the first: under a causal mask all workgroups of a
+  // head see the last ones, so that those that run together find what they read
+  // in L2, where from the first on each is at another place (16384 tokens'
+  // gradients: 1639 us that way).
+  if (t0 < t1) {
+    keep(stats_of(t1 - 1), 0);
+    load(t1 - 1, q0, d0);
+  }
+  for (int t = t1 - 1; t >= t0; t -= 2) {
     pass(t, q0, d0, q1, d1, 0);
-    if (t + 1 < t1) pass(t + 1, q1, d1, q0, d0, 1);
+    if (t > t0) pass(t - 1, q1, d1, q0, d0, 1);
   }
   if (!there) return;
-  store_row<T, DP>(dk, a.scale / f * exp2f(-kBoost<T>), at<T>(a.dk, b, j, g), a.dim);
-  store_row<T, DP>(dv, exp2f(-kBoost<T>), at<T>(a.dv, b, j, g), a.dim);
+  const float by = second ? a.scale / f * exp2f(-kBoost<T>) : exp2f(-kBoost<T>);
+  if (parts == 1) store_row<T, DP>(sum, by, at<T>(second ? a.dk : a.dv, b, j, g), a.dim);
+  else store_part<DP>(sum, by, part + (((uint64_t)id * 2 + !second) * KEYS + pair * 32 + lane % 32) * DP);
+}
+
+// The sums of the parts of a row of dk and of dv.
+template <class T, int DP, int ROWS>
+__global__ __launch_bounds__(kJoinThreads) void k_attention_join_dkv(Args a, uint32_t tiles, uint32_t parts,
+                                                                     const float* part) {
+  const Joined<DP, ROWS> in;
+  const uint32_t bg = in.id / tiles, j = in.id % tiles * ROWS + in.r;
+  if (j >= a.keys) return;
+  f32x4 k = {}, v = {};
+  if (in.e < DP) {
+#pragma unroll 4
+    for (uint32_t n = in.slice; n < parts; n += in.SLICES) {
+      const float* from = part + (((uint64_t)in.id * parts + n) * 2 * ROWS + in.r) * DP + in.e;
+      k += *reinterpret_cast<const f32x4*>(from);
+      v += *reinterpret_cast<const f32x4*>(from + ROWS * DP);
+    }
+  }
+  k = in.sum(k), v = in.sum(v);
+  if (in.slice != 0) return;
+  in.store(k, at<T>(a.dk, bg / a.groups, j, bg % a.groups), a.dim);
+  in.store(v, at<T>(a.dv, bg / a.groups, j, bg % a.groups), a.dim);
 }
 
 // ---- launches -------------------------------------------------------------------
@@ -651,53 +937,104 @@ hipError_t with_dim(const Args& a, bool direct, F&& f) {
   });
 }
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 4, kRows = kWaves * 32, kKeyRows = kWaves / 2 * 32;  // of a workgroup; its queries and heads; its keys
+
+// How a call is cut up: the tiles of queries of a sequence's key and value
+// head (forward, dq) and of its keys (dk, dv), and the parts that the keys or
+// queries that a tile walks over are split into.
+struct Plan {
+  Packing rows, walked;  // of the tiles of queries that stay, and of those that are walked over for dk and dv
+  uint64_t tiles, key_tiles;
+  uint32_t parts, key_parts;
+  bool direct, key_direct;
+  size_t dp;
+
+  // Few workgroups with long ways are split so that all compute units have two
+  // of them. A part has at least kShortest tiles, and is not worth the kernel
+  // that joins it where the whole way has fewer than 4 times as many.
+  static constexpr uint64_t kShortest = 4, kFull = 512;
+  static uint32_t parts_of(uint64_t workgroups, uint64_t way) {
+    if (workgroups == 0 || workgroups * 2 > kFull || way < 4 * kShortest) return 1;
+    return (uint32_t)std::min(kFull / workgroups, way / kShortest);
+  }
+
+  explicit Plan(const Args& a) {
+    const uint32_t bn = a.type == SPARCML_F32 ? kKeys / 2 : kKeys;
+    const uint64_t bg = (uint64_t)a.batch * a.groups, reach = (uint64_t)a.before + a.after;
+    uint64_t walked_tiles;
+    rows = packing_of(a, kRows, tiles);
+    walked = packing_of(a, kWalked, walked_tiles);
+    key_tiles = (a.keys + kKeyRows - 1) / kKeyRows;
+    parts = parts_of(tiles * bg, std::min<uint64_t>(a.keys, reach + rows.ip) / bn);
+    key_parts = parts_of(key_tiles * bg, std::min<uint64_t>(a.queries, reach + kKeyRows) / walked.ip * walked.nh);
+    direct = a.dim * (a.type == SPARCML_F32 ? 4 : 2) % 16 == 0 && (a.keys == 0 || (direct_ok(a, a.k, bn, 1) && direct_ok(a, a.v, bn, 1)));
+    key_direct = a.dim * (a.type == SPARCML_F32 ? 4 : 2) % 16 == 0 && (a.queries == 0 || (direct_ok(a, a.q, walked.ip, walked.hp) && direct_ok(a, a.dout, walked.ip, walked.hp)));
+    dp = (a.dim + 31) / 32 * 32;
+  }
+  size_t part_floats(const Args& a) const {
+    return parts > 1 ? tiles * a.batch * a.groups * parts * kRows * (dp + 2) : 0;
+  }
+  size_t key_part_floats(const Args& a) const {
+    return key_parts > 1 ? key_tiles * a.batch * a.groups * key_parts * kKeyRows * 2 * dp : 0;
+  }
+};
 
 }  // namespace
 
-size_t attention_workspace_bytes(const Args&) { return 256; }
+size_t attention_workspace_bytes(const Args& a) { return Plan(a).part_floats(a) * sizeof(float); }
 
-hipError_t attention_launch(const Args& a, void*, hipStream_t stream) {
-  uint64_t tiles;
-  const Packing pk = packing_of(a, kWaves * 32, tiles);
-  const bool direct = a.keys == 0 || (direct_ok(a, a.k, kKeys, 1) && direct_ok(a, a.v, kKeys, 1));
-  return with_dim(a, direct, [&](auto t, auto dp, auto d) {
-    hipLaunchKernelGGL((k_attention<decltype(t), dp, kWaves, d>), dim3((uint32_t)(tiles * a.batch * a.groups)),
-                       dim3(kWaves * kWave), 0, stream, a, pk, (uint32_t)tiles);
+hipError_t attention_launch(const Args& a, void* ws, hipStream_t stream) {
+  const Plan plan(a);
+  float* part = static_cast<float*>(ws);
+  const uint32_t tiles = (uint32_t)plan.tiles, all = tiles * a.batch * a.groups;
+  return with_dim(a, plan.direct, [&](auto t, auto dp, auto d) {
+    typedef decltype(t) T;
+    hipLaunchKernelGGL((k_attention<T, dp, kWaves, d>), dim3(all * plan.parts), dim3(kWaves * kWave), 0, stream, a,
+                       plan.rows, tiles, plan.parts, part);
+    if (plan.parts > 1)
+      hipLaunchKernelGGL((k_attention_join<T, dp, kWaves>), dim3(Joined<dp, kRows>::blocks((uint64_t)all * kRows)),
+                         dim3(kJoinThreads), 0, stream, a, plan.rows, tiles, plan.parts, part);
   });
 }
 
-size_t attention_backward_workspace_bytes(const Args& a) {
+// the rows' sums, fp16's norms, the parts: dq's are done with when dk's and dv's come
+static size_t stats_floats(const Args& a) {
   const size_t norms = a.type == SPARCML_F16 ? (size_t)a.batch * a.groups * 2 * kNormParts : 0;
-  return ((size_t)a.batch * a.heads * a.queries * 2 + norms) * sizeof(float) + 256;
+  return ((size_t)a.batch * a.heads * a.queries * 2 + norms + 63) / 64 * 64;
+}
+
+size_t attention_backward_workspace_bytes(const Args& a) {
+  const Plan plan(a);
+  return (stats_floats(a) + std::max(plan.part_floats(a), plan.key_part_floats(a))) * sizeof(float);
 }
 
 hipError_t attention_backward_launch(const Args& a, void* ws, hipStream_t stream) {
-  float* stats = static_cast<float*>(ws);
-  float* norms = stats + (size_t)a.batch * a.heads * a.queries * 2;
-  if (a.type == SPARCML_F16) {
+  const Plan plan(a);
+  float *stats = static_cast<float*>(ws), *norms = stats + (size_t)a.batch * a.heads * a.queries * 2;
+  float* part = stats + stats_floats(a);
+  if (a.type == SPARCML_F16)
     hipLaunchKernelGGL(k_attention_norms<f16>, dim3(a.batch * a.groups * kNormParts), dim3(4 * kWave), 0, stream, a, norms);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
   if (a.queries > 0) {
-    uint64_t tiles;
-    const Packing pk = packing_of(a, kWaves * 32, tiles);
-    const bool direct = a.keys == 0 || (direct_ok(a, a.k, kKeys, 1) && direct_ok(a, a.v, kKeys, 1));
-    const hipError_t e = with_dim(a, direct, [&](auto t, auto dp, auto d) {
-      hipLaunchKernelGGL((k_attention_dq<decltype(t), dp, kWaves, d>), dim3((uint32_t)(tiles * a.batch * a.groups)),
-                         dim3(kWaves * kWave), 0, stream, a, pk, (uint32_t)tiles, stats, norms);
+    const uint32_t tiles = (uint32_t)plan.tiles, all = tiles * a.batch * a.groups;
+    const hipError_t e = with_dim(a, plan.direct, [&](auto t, auto dp, auto d) {
+      typedef decltype(t) T;
+      hipLaunchKernelGGL((k_attention_dq<T, dp, kWaves, d>), dim3(all * plan.parts), dim3(kWaves * kWave), 0, stream, a,
+                         plan.rows, tiles, stats, norms, plan.parts, part);
+      if (plan.parts > 1)
+        hipLaunchKernelGGL((k_attention_join_dq<T, dp, kWaves>), dim3(Joined<dp, kRows>::blocks((uint64_t)all * kRows)),
+                           dim3(kJoinThreads), 0, stream, a, plan.rows, tiles, plan.parts, part);
     });
     if (e != hipSuccess) return e;
   }
-  if (a.keys == 0) return hipSuccess;
-  uint64_t none;
-  const uint32_t tiles = (a.keys + kWaves * 32 - 1) / (kWaves * 32);
-  const Packing pk = packing_of(a, a.type == SPARCML_F32 ? kKeys / 2 : kKeys, none);
-  const bool direct = a.queries == 0 || (direct_ok(a, a.q, pk.ip, pk.hp) && direct_ok(a, a.dout, pk.ip, pk.hp));
-  return with_dim(a, direct, [&](auto t, auto dp, auto d) {
-    hipLaunchKernelGGL((k_attention_dkv<decltype(t), dp, kWaves, d>), dim3(tiles * a.batch * a.groups),
-                       dim3(kWaves * kWave), 0, stream, a, pk, tiles, stats, norms);
+  if (a.keys == 0) return hipGetLastError();
+  const uint32_t tiles = (uint32_t)plan.key_tiles, all = tiles * a.batch * a.groups;
+  return with_dim(a, plan.key_direct, [&](auto t, auto dp, auto d) {
+    typedef decltype(t) T;
+    hipLaunchKernelGGL((k_attention_dkv<T, dp, kWaves, d>), dim3(all * plan.key_parts), dim3(kWaves * kWave), 0, stream,
+                       a, plan.walked, tiles, stats, norms, plan.key_parts, part);
+    if (plan.key_parts > 1)
+      hipLaunchKernelGGL((k_attention_join_dkv<T, dp, kKeyRows>), dim3(Joined<dp, kKeyRows>::blocks((uint64_t)all * kKeyRows)),
+                         dim3(kJoinThreads), 0, stream, a, tiles, plan.key_parts, part);
   });
 }
 

@@ -28,6 +28,10 @@ CASES = [
     (3, 70, 70, 8, 1, 96, True, 30, [(70, 10), (10, 70), (64, 64)]),
     (1, 17, 1500, 2, 1, 64, False, None, None),
     (1, 1200, 33, 1, 1, 128, False, None, None),
+    (1, 3, 4000, 6, 2, 48, True, None, None),        # few queries, few keys: the way is split
+    (2, 60, 5000, 2, 1, 128, True, 1500, [(60, 5000), (60, 100)]),
+    (2, 4000, 70, 4, 2, 80, False, None, [(4000, 70), (5, 1)]),
+    (3, 2500, 2500, 1, 1, 32, True, 700, [(2500, 2500), (0, 0), (2000, 2000)]),
     (1, 515, 515, 2, 2, 127, True, None, None),
 ]
 
@@ -208,7 +212,7 @@ def test_no_queries_no_keys_no_sequences(t):
 
 
 @pytest.mark.parametrize("t", TYPES)
-@pytest.mark.parametrize("case", [(2, 300, 300, 4, 2, 128, True), (1, 40, 5000, 2, 2, 64, False)])
+@pytest.mark.parametrize("case", [(2, 300, 300, 4, 2, 128, True), (1, 40, 5000, 2, 2, 64, False), (1, 5000, 40, 2, 2, 64, False)])
 def test_repeated_calls_give_the_same_bits(t, case):
     b, n, m, h, g, d, causal = case
     q, k, v, dout = (x.cuda() for x in make(t, b, n, m, h, g, d, seed=12))
