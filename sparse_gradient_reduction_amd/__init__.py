@@ -851,7 +851,7 @@ def _apart(t: torch.Tensor, name: str):
         if n > 1:
             if step < end:
                 raise ValueError(f"{name}'s elements must not share a place")
-            end = step * n
+            end = step * (n - 1) + end
     return t
 
 
@@ -861,6 +861,18 @@ def _output_heads(t: Optional[torch.Tensor], like: torch.Tensor, name: str) -> t
         return torch.empty_like(like, memory_format=torch.contiguous_format)
     _head_tensor(t, like.dtype, like.shape, like.device, name)
     return t if t.numel() == 0 else _apart(t, name)
+
+
+def _alike(like: torch.Tensor, strides, *tensors) -> bool:
+    """Whether `tensors` and `like`, of these strides, are of one type, shape and
+    GPU, with contiguous heads: the quick look, before the one that says what is wrong."""
+    dtype, shape, dev = like.dtype, like.shape, like.device
+    if not like.is_cuda or strides[-1] != 1:
+        return False
+    for t in tensors:
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.device != dev or t.stride(-1) != 1:
+            return False
+    return True
 
 
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -895,17 +907,19 @@ def _head_norm_checks(q, k, q_weight, k_weight, positions, frequencies):
     """(type, tokens, heads, groups, D, rotated) of head_norm_rotate's arguments."""
     if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or q.dim() < 2 or k.dim() < 2:
         raise TypeError("q and k must be tensors of [..., heads, D]")
-    heads, cols, groups = q.shape[-2], q.shape[-1], k.shape[-2]
-    _head_tensor(q, q.dtype, q.shape, q.device, "q")
-    _head_tensor(k, q.dtype, q.shape[:-2] + (groups, cols), q.device, "k")
-    tokens = q.shape[:-2].numel()
+    shape, dev = q.shape, q.device
+    heads, cols, groups = shape[-2], shape[-1], k.shape[-2]
+    if not (_alike(q, q.stride()) and _alike(k, k.stride()) and k.dtype == q.dtype and k.device == dev
+            and k.shape[:-2] == shape[:-2] and k.shape[-1] == cols):
+        _head_tensor(q, q.dtype, shape, dev, "q")
+        _head_tensor(k, q.dtype, shape[:-2] + (groups, cols), dev, "k")
+    tokens = shape[:-2].numel()
     if tokens >= 1 << 31 or max(heads, groups) >= 1 << 16 or min(heads, groups, cols) < 1 or cols > 256:
         raise ValueError("q and k must have 1 to 65535 heads of 1 to 256 elements and fewer than 2^31 tokens")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _check_dev(w, torch.float32, name)
-            if w.device != q.device or w.numel() != cols:
-                raise ValueError(f"{name} must have {cols} elements on {q.device}")
+    if q_weight is not None:
+        _dim_vector(q_weight, cols, dev, "q_weight")
+    if k_weight is not None:
+        _dim_vector(k_weight, cols, dev, "k_weight")
     rotated = 0
     if frequencies is not None:
         rotated = 2 * frequencies.numel()
@@ -913,9 +927,15 @@ def _head_norm_checks(q, k, q_weight, k_weight, positions, frequencies):
         _check_dev(positions, torch.int32, "positions")
         if rotated > cols or positions.numel() != tokens:
             raise ValueError(f"frequencies must have at most {cols // 2} elements, positions {tokens}")
-        if frequencies.device != q.device or positions.device != q.device:
-            raise ValueError(f"positions and frequencies must be on {q.device}")
+        if frequencies.device != dev or positions.device != dev:
+            raise ValueError(f"positions and frequencies must be on {dev}")
     return _type(q.dtype, "q"), tokens, heads, groups, cols, rotated
+
+
+def _dim_vector(t, cols, device, name):
+    _check_dev(t, torch.float32, name)
+    if t.device != device or t.numel() != cols:
+        raise ValueError(f"{name} must have {cols} elements on {device}")
 
 
 def rotation_frequencies(rotated: int, base: float = 10000.0, device=None) -> torch.Tensor:
@@ -942,7 +962,9 @@ def head_norm_rotate(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.
                                 *_token_heads(k, "k"), *_token_heads(q_out, "q_out"), *_token_heads(k_out, "k_out"),
                                 _ptr(q_weight) or 0, _ptr(k_weight) or 0, _ptr(positions) or 0, _ptr(frequencies) or 0,
                                 *_NO_HEADS, *_NO_HEADS, 0, 0, 0, 0)
-    _raise(_on(q.device, _load().sparcml_head_norm_rotate, args), "sparcml_head_norm_rotate")
+    st = _on(q.device, _load().sparcml_head_norm_rotate, args)
+    if st:
+        _raise(st, "sparcml_head_norm_rotate")
     return q_out, k_out
 
 
@@ -966,8 +988,9 @@ def head_norm_rotate_backward(dq: torch.Tensor, dk: torch.Tensor, q: torch.Tenso
     after the other. q_out and k_out may be dq and dk (or q and k); dq_weight and
     dk_weight may be columns of the [P, N] gradients."""
     t, tokens, heads, groups, cols, rotated = _head_norm_checks(q, k, q_weight, k_weight, positions, frequencies)
-    _head_tensor(dq, q.dtype, q.shape, q.device, "dq")
-    _head_tensor(dk, k.dtype, k.shape, q.device, "dk")
+    if not (_alike(q, q.stride(), dq) and _alike(k, k.stride(), dk)):
+        _head_tensor(dq, q.dtype, q.shape, q.device, "dq")
+        _head_tensor(dk, k.dtype, k.shape, q.device, "dk")
     if not 1 <= nodes <= 65535 or tokens % nodes:
         raise ValueError(f"{tokens} tokens do not belong to {nodes} nodes (up to 65535) in equal parts")
     q_out, k_out = _output_heads(q_out, q, "q_out"), _output_heads(k_out, k, "k_out")
@@ -992,34 +1015,48 @@ def head_norm_rotate_backward(dq: torch.Tensor, dk: torch.Tensor, q: torch.Tenso
 
 # ---------------------------------------------------------------------------
 def _attention_checks(q, k, v, causal, window, scale, q_lengths, k_lengths):
-    """The first words of sparcml_attention_args: sizes, mask, scale and lengths."""
+    """The first words of sparcml_attention_args: sizes, mask, scale, lengths, q, k and v."""
     if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or q.dim() != 4 or k.dim() != 4:
         raise TypeError("q, k and v must be tensors of [batch, tokens, heads, D]")
     shape, dtype, dev = q.shape, q.dtype, q.device
     batch, queries, heads, cols = shape
-    _, keys, groups, _ = k.shape
-    _head_tensor(q, dtype, shape, dev, "q")
-    shape = (batch, keys, groups, cols)
-    _head_tensor(k, dtype, shape, dev, "k")
-    _head_tensor(v, dtype, shape, dev, "v")
-    if batch > 65535 or max(queries, keys) >= 1 << 29 or max(heads, groups) > 65535 or not 1 <= cols <= 128:
+    k_batch, keys, groups, k_cols = k.shape
+    qs, ks = q.stride(), k.stride()
+    if not (_alike(q, qs) and _alike(k, ks, v) and k.dtype == dtype and k.device == dev and k_batch == batch and k_cols == cols):
+        _head_tensor(q, dtype, shape, dev, "q")
+        shape = (batch, keys, groups, cols)
+        _head_tensor(k, dtype, shape, dev, "k")
+        _head_tensor(v, dtype, shape, dev, "v")
+    if batch > 65535 or queries >= 1 << 29 or keys >= 1 << 29 or heads > 65535 or not 1 <= cols <= 128:
         raise ValueError("up to 65535 sequences and heads of 1 to 128 elements, fewer than 2^29 queries and keys")
     if groups < 1 or heads < 1 or heads % groups:
         raise ValueError(f"{heads} heads do not share {groups} groups of keys and values in equal parts")
-    if window is not None and window < 1:
-        raise ValueError("window must be at least 1")
     if scale is None:
         scale = cols ** -0.5
-    if not 0.0 < scale < math.inf:
-        raise ValueError("scale must be finite and positive")
-    for t, name in ((q_lengths, "q_lengths"), (k_lengths, "k_lengths")):
-        if t is not None:
-            _check_dev(t, torch.int32, name)
-            if t.device != dev or t.numel() != batch:
-                raise ValueError(f"{name} must have {batch} elements on {dev}")
-    before = 0xFFFFFFFF if window is None else min(window - 1, 0xFFFFFFFF)
-    return (_type(dtype, "q"), batch, queries, keys, heads, groups, cols, before, 0 if causal else before, scale,
-            _ptr(q_lengths) or 0, _ptr(k_lengths) or 0)
+    elif not 1e-30 <= scale < math.inf:
+        raise ValueError("scale must be finite and at least 1e-30")
+    n = m = 0
+    if q_lengths is not None:
+        n = _lengths(q_lengths, batch, dev, "q_lengths")
+    if k_lengths is not None:
+        m = _lengths(k_lengths, batch, dev, "k_lengths")
+    before = 0xFFFFFFFF
+    if window is not None:
+        if window < 1:
+            raise ValueError("window must be at least 1")
+        before = min(window - 1, before)
+    t = _TYPES.get(dtype)
+    vs = v.stride()
+    return (_type(dtype, "q") if t is None else t, batch, queries, keys, heads, groups, cols, before,
+            0 if causal else before, scale, n, m, q.data_ptr(), qs[0], qs[1], qs[2], k.data_ptr(), ks[0], ks[1], ks[2],
+            v.data_ptr(), vs[0], vs[1], vs[2])
+
+
+def _lengths(t, batch, device, name):
+    _check_dev(t, torch.int32, name)
+    if t.device != device or t.numel() != batch:
+        raise ValueError(f"{name} must have {batch} elements on {device}")
+    return t.data_ptr()
 
 
 def _batch_heads(t: torch.Tensor):
@@ -1040,7 +1077,7 @@ def _call_workspace(t: Optional[torch.Tensor], need: int, like: torch.Tensor):
 def attention_workspace_bytes(q: torch.Tensor, k: torch.Tensor, backward: bool = False) -> int:
     """Bytes of the workspace that is enough for attention or, `backward`,
     attention_backward of queries and keys like these, whatever the mask."""
-    args = _ATTENTION_ARGS.pack(*_attention_checks(q, k, k, False, None, None, None, None), *([0] * 33))
+    args = _ATTENTION_ARGS.pack(*_attention_checks(q, k, k, False, None, None, None, None), *([0] * 21))
     return int((_load().sparcml_attention_backward_workspace if backward else _load().sparcml_attention_workspace)(args))
 
 
@@ -1064,11 +1101,12 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
         lse = q.new_empty((head[1], head[4], head[2]), dtype=torch.float32)
     else:
         _check_lse(lse, head, q)
-    args = _ATTENTION_ARGS.pack(*head, *_batch_heads(q), *_batch_heads(k), *_batch_heads(v), *_batch_heads(out),
-                                lse.data_ptr(), *_NO_HEADS, *_NO_HEADS, *_NO_HEADS, *_NO_HEADS)
+    args = _ATTENTION_ARGS.pack(*head, *_batch_heads(out), lse.data_ptr(), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
     L = _load()
     ws, n, workspace = _call_workspace(workspace, L.sparcml_attention_workspace(args), q)
-    _raise(_on(q.device, L.sparcml_attention, args, ws, n), "sparcml_attention")
+    st = _on(q.device, L.sparcml_attention, args, ws, n)
+    if st:
+        _raise(st, "sparcml_attention")
     return out, lse
 
 
@@ -1091,13 +1129,13 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     0. Nothing of queries times keys is stored: the probabilities are computed
     again, tile by tile."""
     head = _attention_checks(q, k, v, causal, window, scale, q_lengths, k_lengths)
-    _head_tensor(dout, q.dtype, q.shape, q.device, "dout")
-    _head_tensor(out, q.dtype, q.shape, q.device, "out")
+    if not _alike(q, q.stride(), dout, out):
+        _head_tensor(dout, q.dtype, q.shape, q.device, "dout")
+        _head_tensor(out, q.dtype, q.shape, q.device, "out")
     _check_lse(lse, head, q)
     dq, dk, dv = _output_heads(dq, q, "dq"), _output_heads(dk, k, "dk"), _output_heads(dv, v, "dv")
-    args = _ATTENTION_ARGS.pack(*head, *_batch_heads(q), *_batch_heads(k), *_batch_heads(v), *_batch_heads(out),
-                                lse.data_ptr(), *_batch_heads(dout), *_batch_heads(dq), *_batch_heads(dk),
-                                *_batch_heads(dv))
+    args = _ATTENTION_ARGS.pack(*head, *_batch_heads(out), lse.data_ptr(), *_batch_heads(dout), *_batch_heads(dq),
+                                *_batch_heads(dk), *_batch_heads(dv))
     L = _load()
     ws, n, workspace = _call_workspace(workspace, L.sparcml_attention_backward_workspace(args), q)
     st = _on(q.device, L.sparcml_attention_backward, args, ws, n)

@@ -483,7 +483,7 @@ static bool attention_sizes_ok(const sparcml_attention_args& a) {
 }
 
 static bool attention_args_ok(const sparcml_attention_args& a, bool backward) {
-  if (!attention_sizes_ok(a) || !std::isfinite(a.scale) || !(a.scale > 0.0f)) return false;
+  if (!attention_sizes_ok(a) || !std::isfinite(a.scale) || !(a.scale >= 1e-30f)) return false;
   if ((a.q_lengths && (reinterpret_cast<uintptr_t>(a.q_lengths) & 3u)) ||
       (a.k_lengths && (reinterpret_cast<uintptr_t>(a.k_lengths) & 3u)))
     return false;

@@ -190,14 +190,6 @@ __device__ __forceinline__ void wait_and_meet() {
   asm volatile("" ::: "memory");
 }
 
-// The same, but for the loads from memory.
-__device__ __forceinline__ void meet() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(15 | 3 << 14 | 7 << 4);  // lgkmcnt 0
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
 // Loads of a tile's rows by NT threads, 16 bytes a thread at a time. What is
 // not there (past a head's end, past the last query or key) becomes 0 and is
 // not read. DIRECT: memory to LDS, for heads on 16-byte borders whose rows are
@@ -371,7 +363,6 @@ __device__ __forceinline__ void store_part(const Acc (&acc)[DP / 32], float by, 
           f32x4{acc[t][4 * q], acc[t][4 * q + 1], acc[t][4 * q + 2], acc[t][4 * q + 3]} * by;
 }
 
-constexpr int kWalked = 32;  // rows of a tile of queries that is walked over
 constexpr int kKeys = 64;    // keys of a tile, 16-bit; 32 with fp32
 template <class T>
 constexpr int keys_of() { return sizeof(T) == 2 ? kKeys : kKeys / 2; }
@@ -400,10 +391,12 @@ __global__ __launch_bounds__(NW * kWave, (sizeof(T) == 4 && DP > 64 ? 1 : 2)) vo
 
   const Packing one{1, BN, 1};
   const Loader<T, TL, NT, DIRECT, false> lk(a.k, one, a.dim), lv(a.v, one, a.dim);
-  const T *ks = at<T>(a.k, b, 0, g), *vs = at<T>(a.v, b, 0, g);
+  const T *ks = at<T>(a.k, b, rows.first, g), *vs = at<T>(a.v, b, rows.first, g);  // of the next tile
+  const uint64_t k_step = BN * a.k.token, v_step = BN * a.v.token;
   const auto load = [&](int j, I4* kt, I4* vt) {
-    lk.load(ks + j * a.k.token, 0, rows.last + 1 - j, kt);
-    lv.load(vs + j * a.v.token, 0, rows.last + 1 - j, vt);
+    lk.load(ks, 0, rows.last + 1 - j, kt);
+    lv.load(vs, 0, rows.last + 1 - j, vt);
+    ks += k_step, vs += v_step;
   };
   typename TL::Places places;
   const auto products = [&](auto masked, int j, const I4* kt, const I4* vt) {
@@ -476,24 +469,36 @@ __global__ __launch_bounds__(NW * kWave, (sizeof(T) == 4 && DP > 64 ? 1 : 2)) vo
   if (lane_id() < 32) a.lse[((uint64_t)b * a.heads + rows.head) * a.queries + rows.i] = sum == 0.0f ? -INFINITY : top * kLn2 + logf(sum);
 }
 
-// Where a thread of a joining kernel is: a wave joins row r of the ROWS of a
-// tile, L lanes of 4 elements, from e on, taking every SLICES-th part.
-template <int DP, int ROWS>
+// Where a thread of a joining kernel is: L lanes join row r of the ROWS of a
+// tile, 4 elements each from e on. MANY parts: a wave joins a row, its L lanes
+// each taking every SLICES-th part, since a few rows' parts one after the other
+// would take as long as they are many.
+constexpr uint32_t kManyParts = 8;
+template <int DP, int ROWS, bool MANY>
 struct Joined {
-  static constexpr int L = DP <= 32 ? 8 : DP <= 64 ? 16 : 32, SLICES = kWave / L;
+  static constexpr int L = DP <= 32 ? 8 : DP <= 64 ? 16 : 32, SLICES = MANY ? kWave / L : 1, LANES = L * SLICES;
   uint64_t row;
   uint32_t id, r, e, slice;
   __device__ __forceinline__ Joined() {
-    row = (uint64_t)blockIdx.x * (kJoinThreads / kWave) + threadIdx.x / kWave;
-    id = row / ROWS, r = row % ROWS, e = lane_id() % L * 4, slice = lane_id() / L;
+    row = (uint64_t)blockIdx.x * (kJoinThreads / LANES) + threadIdx.x / LANES;
+    id = row / ROWS, r = row % ROWS, e = lane_id() % L * 4, slice = lane_id() % LANES / L;
   }
-  static uint32_t blocks(uint64_t rows) { return (uint32_t)(rows / (kJoinThreads / kWave)); }
+  static uint32_t blocks(uint64_t rows) { return (uint32_t)(rows / (kJoinThreads / LANES)); }  // ROWS is a multiple of it
   static __device__ __forceinline__ float sum(float v) {
 #pragma unroll
-    for (int d = L; d < kWave; d <<= 1) v += __shfl_xor(v, d, kWave);
+    for (int d = L; d < LANES; d <<= 1) v += __shfl_xor(v, d, kWave);
     return v;
   }
   static __device__ __forceinline__ f32x4 sum(f32x4 v) { return f32x4{sum(v[0]), sum(v[1]), sum(v[2]), sum(v[3])}; }
+  // the largest of f(k), k < parts, for the row
+  template <class F>
+  __device__ __forceinline__ float most(uint32_t parts, F&& f) const {
+    float v = -INFINITY;
+    for (uint32_t k = lane_id() % LANES; k < parts; k += LANES) v = fmaxf(v, f(k));
+#pragma unroll
+    for (int d = 1; d < LANES; d <<= 1) v = fmaxf(v, __shfl_xor(v, d, kWave));
+    return v;
+  }
   template <class T>
   __device__ __forceinline__ void store(f32x4 o, T* p, uint32_t dim) const {
     typedef T Four __attribute__((ext_vector_type(4)));
@@ -513,11 +518,11 @@ struct Joined {
 
 // Joins the parts of a row: out = sum of 2^(top - most) o, over the sum of 2^(top
 // - most) sum.
-template <class T, int DP, int NW>
+template <class T, int DP, int NW, bool MANY>
 __global__ __launch_bounds__(kJoinThreads) void k_attention_join(Args a, Packing pk, uint32_t tiles, uint32_t parts,
                                                                  const float* part) {
   constexpr int ROWS = NW * 32;
-  const Joined<DP, ROWS> in;
+  const Joined<DP, ROWS, MANY> in;
   const uint64_t all = (uint64_t)tiles * a.batch * a.groups * ROWS;
   const uint32_t bg = in.id / tiles, b = bg / a.groups;
   Rows<NW> rows;
@@ -525,9 +530,8 @@ __global__ __launch_bounds__(kJoinThreads) void k_attention_join(Args a, Packing
   if (!rows.there) return;
   const float2* tops = reinterpret_cast<const float2*>(part) + (uint64_t)in.id * parts * ROWS + in.r;
   const float* os = part + all * parts * 2 + ((uint64_t)in.id * parts * ROWS + in.r) * DP + in.e;
-  float most = -INFINITY, sum = 0.0f;
-  for (uint32_t k = lane_id(); k < parts; k += kWave) most = fmaxf(most, tops[k * ROWS].x);
-  most = wave_max(most);
+  const float most = in.most(parts, [&](uint32_t k) { return tops[k * ROWS].x; });
+  float sum = 0.0f;
   f32x4 o = {};
 #pragma unroll 4
   for (uint32_t k = in.slice; k < parts; k += in.SLICES) {
@@ -644,10 +648,12 @@ __global__ __launch_bounds__(NW * kWave, (sizeof(T) == 4 && DP > 64 ? 1 : 2)) vo
 
   const Packing one{1, BN, 1};
   const Loader<T, TL, NT, DIRECT, false> lk(a.k, one, a.dim), lv(a.v, one, a.dim);
-  const T *ks = at<T>(a.k, b, 0, g), *vs = at<T>(a.v, b, 0, g);
+  const T *ks = at<T>(a.k, b, rows.first, g), *vs = at<T>(a.v, b, rows.first, g);  // of the next tile
+  const uint64_t k_step = BN * a.k.token, v_step = BN * a.v.token;
   const auto load = [&](int j, I4* kt, I4* vt) {
-    lk.load(ks + j * a.k.token, 0, rows.last + 1 - j, kt);
-    lv.load(vs + j * a.v.token, 0, rows.last + 1 - j, vt);
+    lk.load(ks, 0, rows.last + 1 - j, kt);
+    lv.load(vs, 0, rows.last + 1 - j, vt);
+    ks += k_step, vs += v_step;
   };
   typename TL::Places places;
   const auto products = [&](auto masked, int j, const I4* kt, const I4* vt) {
@@ -695,11 +701,11 @@ __global__ __launch_bounds__(NW * kWave, (sizeof(T) == 4 && DP > 64 ? 1 : 2)) vo
 }
 
 // The sum of the parts of a row of dq.
-template <class T, int DP, int NW>
+template <class T, int DP, int NW, bool MANY>
 __global__ __launch_bounds__(kJoinThreads) void k_attention_join_dq(Args a, Packing pk, uint32_t tiles, uint32_t parts,
                                                                     const float* part) {
   constexpr int ROWS = NW * 32;
-  const Joined<DP, ROWS> in;
+  const Joined<DP, ROWS, MANY> in;
   const uint32_t bg = in.id / tiles;
   Rows<NW> rows;
   rows.place(a, pk, tiles - 1 - in.id % tiles, bg % a.groups, in.r);
@@ -716,19 +722,16 @@ __global__ __launch_bounds__(kJoinThreads) void k_attention_join_dq(Args a, Pack
 
 
 // ---- backward: dk and dv --------------------------------------------------------
-// Two waves have 32 keys and walk over the tiles of queries that see one of the
-// workgroup's. One computes the scores, the probabilities and dv, the other dout
-// v^T, ds (from the probabilities that it gets through LDS) and dk: four
-// products shared evenly, and each wave holds one operand and one sum instead of
-// two, so that three waves of 128-element heads fit a SIMD where one would.
+// A wave has 32 keys and walks over the tiles of queries that see one of the
+// workgroup's.
 template <class T, int DP, int NW, bool DIRECT>
-__global__ __launch_bounds__(NW * kWave, (DP > 64 ? 2 : 3)) void k_attention_dkv(
+__global__ __launch_bounds__(NW * kWave, (DP > 64 ? 1 : 2)) void k_attention_dkv(
     Args a, Packing pk, uint32_t tiles, const float* stats, const float* norms, uint32_t parts, float* part) {
-  constexpr int BM = kWalked, NT = NW * kWave, KEYS = NW / 2 * 32;
+  constexpr int BM = keys_of<T>(), NT = NW * kWave, KEYS = NW * 32;
   typedef Tile<T, DP, BM> TL;
   typedef Mma<T> M;
+  typedef typename TL::Frag Frag;
   __shared__ I4 q0[TL::SIZE], d0[TL::SIZE], q1[TL::SIZE], d1[TL::SIZE];
-  __shared__ f32x4 shared[NW / 2][4][kWave];  // a pair's probabilities, as a result's lanes have them
   __shared__ __align__(16) float stat[2][2][BM];
   __shared__ uint32_t query[BM];
   const uint32_t id = xcd_contiguous(blockIdx.x, gridDim.x), bg = id / parts / tiles, tile = id / parts % tiles;
@@ -736,15 +739,14 @@ __global__ __launch_bounds__(NW * kWave, (DP > 64 ? 2 : 3)) void k_attention_dkv
   const Sequence s(a, b);
   const float c = a.scale * kLog2e;
   const uint32_t wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id();
-  const uint32_t pair = wid / 2;
-  const bool second = ((wid ^ blockIdx.x) & 1) != 0;  // waves of a place share a SIMD: both kinds on each
-  const int j0 = tile * KEYS, w0 = j0 + pair * 32, j = w0 + lane % 32, end = min(j0 + KEYS, s.m);
+  const int j0 = tile * KEYS, w0 = j0 + wid * 32, j = w0 + lane % 32, end = min(j0 + KEYS, s.m);
   const bool there = j < (int)a.keys;
 
-  typename TL::Frag held[TL::STEPS];  // of k, or of v
-  load_row<T, TL, DIRECT>(held, second ? a.v : a.k, b, j, g, j < s.m, a.dim);
+  Frag k[TL::STEPS], v[TL::STEPS];
+  load_row<T, TL, DIRECT>(k, a.k, b, j, g, j < s.m, a.dim);
+  load_row<T, TL, DIRECT>(v, a.v, b, j, g, j < s.m, a.dim);
   const float f = factor_of<T>(norms, bg);
-  Acc sum[DP / 32] = {};  // dv, or dk
+  Acc dk[DP / 32] = {}, dv[DP / 32] = {};
 
   // queries first .. last see one of the workgroup's keys
   const int first = max(0, j0 - s.after - s.m + s.n), last = j0 < end ? min(s.n - 1, end - 1 + s.before - s.m + s.n) : -1;
@@ -755,20 +757,44 @@ __global__ __launch_bounds__(NW * kWave, (DP > 64 ? 2 : 3)) void k_attention_dkv
     t0 = min(from, (int64_t)t1);
   }
 
+  const int count = t1 - t0;
+
   const Loader<T, TL, NT, DIRECT, true> lq(a.q, pk, a.dim), ld(a.dout, pk, a.dim);
   const int seeing = max(0, s.n - s.m - s.after);  // the first query that sees a key
   const uint32_t my_i = threadIdx.x / pk.hp, my_h = threadIdx.x % pk.hp;
   if (threadIdx.x < BM) query[threadIdx.x] = my_i;
+  // Where the next tile is: its first query, its heads, and what follows from
+  // them. Moved on instead of computed again, since divisions and products of
+  // 64 bits between two tiles would take longer than the tile (8 scalar
+  // instructions to a matrix one, 1558 us for 16384 tokens' gradients).
+  struct {
+    int i0;
+    uint32_t chunk;
+    const T *q, *d;
+    const float* stat;
+  } at_tile;
+  const uint64_t all_stats = (uint64_t)a.batch * a.heads * a.queries;
+  const auto go_to = [&](int i0, uint32_t chunk) {
+    const uint32_t h = g * each + chunk * pk.hp;
+    at_tile = {i0, chunk, at<T>(a.q, b, i0, h), at<T>(a.dout, b, i0, h), stats + ((uint64_t)b * a.heads + h) * a.queries + i0};
+  };
+  const uint64_t q_step = pk.ip * a.q.token, d_step = pk.ip * a.dout.token;
+  const auto step_back = [&]() {
+    if (pk.nh > 1) {
+      const bool wrap = at_tile.chunk == 0;
+      go_to(at_tile.i0 - (wrap ? (int)pk.ip : 0), wrap ? pk.nh - 1 : at_tile.chunk - 1);
+    } else {
+      at_tile.i0 -= pk.ip, at_tile.q -= q_step, at_tile.d -= d_step, at_tile.stat -= pk.ip;
+    }
+  };
   // the rows' lse and delta pass through registers: they are stored when the
   // tiles' loads, which were asked for after them, have had time
-  const auto stats_of = [&](int t) {
-    const uint32_t h = g * each + t % pk.nh * pk.hp;
-    const int i = t / pk.nh * pk.ip + my_i;
+  const uint64_t my_stat = (uint64_t)my_h * a.queries + my_i;
+  const bool mine = threadIdx.x < BM && my_i < pk.ip;
+  const auto stats_of = [&]() {
     float2 v = make_float2(-INFINITY, 0.0f);
-    if (threadIdx.x < BM && my_i < pk.ip && i >= seeing && i < s.n) {
-      const uint64_t where = ((uint64_t)b * a.heads + h + my_h) * a.queries + i;
-      v = make_float2(stats[where], stats[where + (uint64_t)a.batch * a.heads * a.queries]);
-    }
+    const int i = at_tile.i0 + my_i;
+    if (mine && i >= seeing && i < s.n) v = make_float2(at_tile.stat[my_stat], at_tile.stat[my_stat + all_stats]);
     return v;
   };
   const auto keep = [&](float2 v, int turn) {
@@ -777,110 +803,108 @@ __global__ __launch_bounds__(NW * kWave, (DP > 64 ? 2 : 3)) void k_attention_dkv
       stat[turn][1][threadIdx.x] = v.y;
     }
   };
-  const auto load = [&](int t, I4* qt, I4* dt) {
-    const uint32_t h = g * each + t % pk.nh * pk.hp;
-    const int i0 = t / pk.nh * pk.ip;
-    lq.load(at<T>(a.q, b, i0, h), seeing - i0, s.n - i0, qt);
-    ld.load(at<T>(a.dout, b, i0, h), seeing - i0, s.n - i0, dt);
+  const auto load = [&](I4* qt, I4* dt) {
+    lq.load(at_tile.q, seeing - at_tile.i0, s.n - at_tile.i0, qt);
+    ld.load(at_tile.d, seeing - at_tile.i0, s.n - at_tile.i0, dt);
   };
   typename TL::Places places;
-  // `tile` times the held rows. 16-bit: the sums start from -lse or -delta.
-  const auto rows_product = [&](const I4* tile, const float* from) {
+  const auto products = [&](auto masked, int i0, const I4* qt, const I4* dt, const float (&row)[2][BM]) {
     places.make_new();
-    Acc p = {};
-    if constexpr (sizeof(T) == 2) {
+    // the key's way from the first one that the tile's first query may see; past all of them where there is no key
+    const uint32_t far = j < s.m ? (uint32_t)(j - i0 - s.m + s.n + s.before) : 0xFFFFFF00u;
+    const uint32_t span = (uint32_t)s.before + (uint32_t)s.after;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const f32x4 v = *reinterpret_cast<const f32x4*>(from + 4 * (lane / 32) + 8 * r);
+    for (int u = 0; u < BM / 32; ++u) {
+      const int h4 = 32 * u + 4 * (lane / 32);
+      // 16-bit: the products start from -lse and -delta
+      const auto start = [&](int which) {
+        Acc a = {};
+        if constexpr (sizeof(T) == 2) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) p[4 * r + x] = v[x];
+          for (int r = 0; r < 4; ++r) {
+            const f32x4 v = *reinterpret_cast<const f32x4*>(row[which] + h4 + 8 * r);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) a[4 * r + x] = v[x];
+          }
+        }
+        return a;
+      };
+      Acc p = start(0), e = start(1);
+#pragma unroll
+      for (int x = 0; x < TL::STEPS; ++x) {
+        p = M::mul(TL::row(qt, places, 32 * u, x), k[x], p);
+        e = M::mul(TL::row(dt, places, 32 * u, x), v[x], e);
       }
-    }
-#pragma unroll
-    for (int x = 0; x < TL::STEPS; ++x) p = M::mul(TL::row(tile, places, 0, x), held[x], p);
-    if constexpr (sizeof(T) == 4) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const float off = from[4 * (lane / 32) + 8 * (r / 4) + r % 4];
-        p[r] = second ? p[r] + off : fmaf(p[r], c, off);
+        p[r] = __builtin_amdgcn_exp2f(sizeof(T) == 2 ? p[r] * c : fmaf(p[r], c, row[0][h4 + 8 * (r / 4) + r % 4]));
+        if constexpr (masked) p[r] = far - query[h4 + 8 * (r / 4) + r % 4] > span ? 0.0f : p[r];
+      }
+#pragma unroll
+      for (int x = 0; x < 32 / M::STEP; ++x) {
+        const Frag b = M::frag(p, x);
+#pragma unroll
+        for (int y = 0; y < DP / 32; ++y) dv[y] = M::mul(TL::column(dt, places, 32 * u, x, y), b, dv[y]);
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        if constexpr (kBoost<T> != 0.0f) p[r] *= f;
+        p[r] *= sizeof(T) == 2 ? e[r] : e[r] + row[1][h4 + 8 * (r / 4) + r % 4];
+      }
+#pragma unroll
+      for (int x = 0; x < 32 / M::STEP; ++x) {
+        const Frag b = M::frag(p, x);
+#pragma unroll
+        for (int y = 0; y < DP / 32; ++y) dk[y] = M::mul(TL::column(qt, places, 32 * u, x, y), b, dk[y]);
       }
     }
-    return p;
   };
-  const auto columns_product = [&](const I4* tile, const Acc& p) {
-#pragma unroll
-    for (int x = 0; x < 32 / M::STEP; ++x) {
-      const typename TL::Frag b = M::frag(p, x);
-#pragma unroll
-      for (int y = 0; y < DP / 32; ++y) sum[y] = M::mul(TL::column(tile, places, 0, x, y), b, sum[y]);
-    }
-  };
-  const auto pass = [&](int t, const I4* qt, const I4* dt, I4* qn, I4* dn, int turn) {
+  const auto pass = [&](int n, const I4* qt, const I4* dt, I4* qn, I4* dn, int turn) {
     wait_and_meet();
+    const int i0 = at_tile.i0, i1 = min(i0 + (int)pk.ip, s.n) - 1;
     float2 next = {};
-    if (t > t0) {
-      next = stats_of(t - 1);
-      load(t - 1, qn, dn);
+    if (n + 1 < count) {
+      step_back();
+      next = stats_of();
+      load(qn, dn);
     }
-    const int i0 = t / pk.nh * pk.ip, i1 = min(i0 + (int)pk.ip, s.n) - 1;
-    // some query of the tile sees some key of the pair
-    const bool some = w0 < end && w0 <= s.last(i1) && min(w0 + 31, end - 1) >= s.first(i0);
-    if (!second) {
-      Acc p;
-      if (some) {
-        p = rows_product(qt, stat[turn][0]);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) p[r] = __builtin_amdgcn_exp2f(sizeof(T) == 2 ? p[r] * c : p[r]);
-        if (w0 < s.first(i1) || w0 + 31 > s.last(i0)) {  // not all see all
-          // the key's way from the first one that the tile's first query may see; past all of them where there is no key
-          const uint32_t far = j < s.m ? (uint32_t)(j - i0 - s.m + s.n + s.before) : 0xFFFFFF00u;
-          const uint32_t span = (uint32_t)s.before + (uint32_t)s.after;
-#pragma unroll
-          for (int r = 0; r < 16; ++r) p[r] = far - query[4 * (lane / 32) + 8 * (r / 4) + r % 4] > span ? 0.0f : p[r];
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) shared[pair][r][lane] = f32x4{p[4 * r], p[4 * r + 1], p[4 * r + 2], p[4 * r + 3]};
-      }
-      meet();
-      if (some) columns_product(dt, p);
-    } else {
-      Acc e;
-      if (some) e = rows_product(dt, stat[turn][1]);
-      meet();
-      if (some) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const float p = shared[pair][r / 4][lane][r % 4];
-          e[r] *= kBoost<T> == 0.0f ? p : p * f;
-        }
-        columns_product(qt, e);
-      }
+    // some query of the tile sees some key of the wave, or all see all
+    if (w0 < end && w0 <= s.last(i1) && min(w0 + 31, end - 1) >= s.first(i0)) {
+      if (w0 < s.first(i1) || w0 + 31 > s.last(i0)) products(std::true_type{}, i0, qt, dt, stat[turn]);
+      else products(std::false_type{}, i0, qt, dt, stat[turn]);
     }
     keep(next, turn ^ 1);
   };
   // From the last queries to the first: under a causal mask all workgroups of a
   // head see the last ones, so that those that run together find what they read
   // in L2, where from the first on each is at another place (16384 tokens'
-  // gradients: 1639 us that way).
-  if (t0 < t1) {
-    keep(stats_of(t1 - 1), 0);
-    load(t1 - 1, q0, d0);
-  }
-  for (int t = t1 - 1; t >= t0; t -= 2) {
-    pass(t, q0, d0, q1, d1, 0);
-    if (t > t0) pass(t - 1, q1, d1, q0, d0, 1);
+  // gradients are a twentieth slower that way).
+  if (count > 0) {
+    go_to((t1 - 1) / (int)pk.nh * (int)pk.ip, (t1 - 1) % pk.nh);
+    keep(stats_of(), 0);
+    load(q0, d0);
+    for (int n = 0; n < count; n += 2) {
+      pass(n, q0, d0, q1, d1, 0);
+      if (n + 1 < count) pass(n + 1, q1, d1, q0, d0, 1);
+    }
   }
   if (!there) return;
-  const float by = second ? a.scale / f * exp2f(-kBoost<T>) : exp2f(-kBoost<T>);
-  if (parts == 1) store_row<T, DP>(sum, by, at<T>(second ? a.dk : a.dv, b, j, g), a.dim);
-  else store_part<DP>(sum, by, part + (((uint64_t)id * 2 + !second) * KEYS + pair * 32 + lane % 32) * DP);
+  const float byk = a.scale / f * exp2f(-kBoost<T>), byv = exp2f(-kBoost<T>);
+  if (parts == 1) {
+    store_row<T, DP>(dk, byk, at<T>(a.dk, b, j, g), a.dim);
+    store_row<T, DP>(dv, byv, at<T>(a.dv, b, j, g), a.dim);
+  } else {
+    float* to = part + ((uint64_t)id * 2 * KEYS + wid * 32 + lane % 32) * DP;
+    store_part<DP>(dk, byk, to);
+    store_part<DP>(dv, byv, to + KEYS * DP);
+  }
 }
 
 // The sums of the parts of a row of dk and of dv.
-template <class T, int DP, int ROWS>
+template <class T, int DP, int ROWS, bool MANY>
 __global__ __launch_bounds__(kJoinThreads) void k_attention_join_dkv(Args a, uint32_t tiles, uint32_t parts,
                                                                      const float* part) {
-  const Joined<DP, ROWS> in;
+  const Joined<DP, ROWS, MANY> in;
   const uint32_t bg = in.id / tiles, j = in.id % tiles * ROWS + in.r;
   if (j >= a.keys) return;
   f32x4 k = {}, v = {};
@@ -937,7 +961,14 @@ hipError_t with_dim(const Args& a, bool direct, F&& f) {
   });
 }
 
-constexpr int kWaves = 4, kRows = kWaves * 32, kKeyRows = kWaves / 2 * 32;  // of a workgroup; its queries and heads; its keys
+// f(whether there are many), where there are parts to join
+template <class F>
+void join(uint32_t parts, F&& f) {
+  if (parts >= kManyParts) f(std::true_type{});
+  else if (parts > 1) f(std::false_type{});
+}
+
+constexpr int kWaves = 4, kRows = kWaves * 32;  // of a workgroup; its queries and heads, or keys
 
 // How a call is cut up: the tiles of queries of a sequence's key and value
 // head (forward, dq) and of its keys (dk, dv), and the parts that the keys or
@@ -963,10 +994,10 @@ struct Plan {
     const uint64_t bg = (uint64_t)a.batch * a.groups, reach = (uint64_t)a.before + a.after;
     uint64_t walked_tiles;
     rows = packing_of(a, kRows, tiles);
-    walked = packing_of(a, kWalked, walked_tiles);
-    key_tiles = (a.keys + kKeyRows - 1) / kKeyRows;
+    walked = packing_of(a, bn, walked_tiles);
+    key_tiles = (a.keys + kRows - 1) / kRows;
     parts = parts_of(tiles * bg, std::min<uint64_t>(a.keys, reach + rows.ip) / bn);
-    key_parts = parts_of(key_tiles * bg, std::min<uint64_t>(a.queries, reach + kKeyRows) / walked.ip * walked.nh);
+    key_parts = parts_of(key_tiles * bg, std::min<uint64_t>(a.queries, reach + kRows) / walked.ip * walked.nh);
     direct = a.dim * (a.type == SPARCML_F32 ? 4 : 2) % 16 == 0 && (a.keys == 0 || (direct_ok(a, a.k, bn, 1) && direct_ok(a, a.v, bn, 1)));
     key_direct = a.dim * (a.type == SPARCML_F32 ? 4 : 2) % 16 == 0 && (a.queries == 0 || (direct_ok(a, a.q, walked.ip, walked.hp) && direct_ok(a, a.dout, walked.ip, walked.hp)));
     dp = (a.dim + 31) / 32 * 32;
@@ -975,7 +1006,7 @@ struct Plan {
     return parts > 1 ? tiles * a.batch * a.groups * parts * kRows * (dp + 2) : 0;
   }
   size_t key_part_floats(const Args& a) const {
-    return key_parts > 1 ? key_tiles * a.batch * a.groups * key_parts * kKeyRows * 2 * dp : 0;
+    return key_parts > 1 ? key_tiles * a.batch * a.groups * key_parts * kRows * 2 * dp : 0;
   }
 };
 
@@ -991,9 +1022,10 @@ hipError_t attention_launch(const Args& a, void* ws, hipStream_t stream) {
     typedef decltype(t) T;
     hipLaunchKernelGGL((k_attention<T, dp, kWaves, d>), dim3(all * plan.parts), dim3(kWaves * kWave), 0, stream, a,
                        plan.rows, tiles, plan.parts, part);
-    if (plan.parts > 1)
-      hipLaunchKernelGGL((k_attention_join<T, dp, kWaves>), dim3(Joined<dp, kRows>::blocks((uint64_t)all * kRows)),
+    join(plan.parts, [&](auto many) {
+      hipLaunchKernelGGL((k_attention_join<T, dp, kWaves, many>), dim3(Joined<dp, kRows, many>::blocks((uint64_t)all * kRows)),
                          dim3(kJoinThreads), 0, stream, a, plan.rows, tiles, plan.parts, part);
+    });
   });
 }
 
@@ -1020,9 +1052,11 @@ hipError_t attention_backward_launch(const Args& a, void* ws, hipStream_t stream
       typedef decltype(t) T;
       hipLaunchKernelGGL((k_attention_dq<T, dp, kWaves, d>), dim3(all * plan.parts), dim3(kWaves * kWave), 0, stream, a,
                          plan.rows, tiles, stats, norms, plan.parts, part);
-      if (plan.parts > 1)
-        hipLaunchKernelGGL((k_attention_join_dq<T, dp, kWaves>), dim3(Joined<dp, kRows>::blocks((uint64_t)all * kRows)),
-                           dim3(kJoinThreads), 0, stream, a, plan.rows, tiles, plan.parts, part);
+      join(plan.parts, [&](auto many) {
+        hipLaunchKernelGGL((k_attention_join_dq<T, dp, kWaves, many>),
+                           dim3(Joined<dp, kRows, many>::blocks((uint64_t)all * kRows)), dim3(kJoinThreads), 0, stream, a,
+                           plan.rows, tiles, plan.parts, part);
+      });
     });
     if (e != hipSuccess) return e;
   }
@@ -1032,9 +1066,10 @@ hipError_t attention_backward_launch(const Args& a, void* ws, hipStream_t stream
     typedef decltype(t) T;
     hipLaunchKernelGGL((k_attention_dkv<T, dp, kWaves, d>), dim3(all * plan.key_parts), dim3(kWaves * kWave), 0, stream,
                        a, plan.walked, tiles, stats, norms, plan.key_parts, part);
-    if (plan.key_parts > 1)
-      hipLaunchKernelGGL((k_attention_join_dkv<T, dp, kKeyRows>), dim3(Joined<dp, kKeyRows>::blocks((uint64_t)all * kKeyRows)),
+    join(plan.key_parts, [&](auto many) {
+      hipLaunchKernelGGL((k_attention_join_dkv<T, dp, kRows, many>), dim3(Joined<dp, kRows, many>::blocks((uint64_t)all * kRows)),
                          dim3(kJoinThreads), 0, stream, a, tiles, plan.key_parts, part);
+    });
   });
 }
 
