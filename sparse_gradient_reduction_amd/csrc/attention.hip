@@ -980,13 +980,17 @@ struct Plan {
   bool direct, key_direct;
   size_t dp;
 
-  // Few workgroups with long ways are split so that all compute units have two
-  // of them. A part has at least kShortest tiles, and is not worth the kernel
-  // that joins it where the whole way has fewer than 4 times as many.
-  static constexpr uint64_t kShortest = 4, kFull = 512;
-  static uint32_t parts_of(uint64_t workgroups, uint64_t way) {
-    if (workgroups == 0 || workgroups * 2 > kFull || way < 4 * kShortest) return 1;
-    return (uint32_t)std::min(kFull / workgroups, way / kShortest);
+  // Few workgroups with long ways are split so that all compute units are
+  // full: two workgroups each, one of those that hold 128-element heads' dk and
+  // dv (5 sequences of 1001, 80-element heads, in 3 parts: gradients 82 us, in
+  // one 77). Parts have `shortest` tiles at least, and a way that has fewer than
+  // `least` is not worth the kernel that joins it: 512 tokens of 16 heads of 64
+  // take 12 us, in parts of 4 tiles 20; an fp32 tile takes about 6 times as long,
+  // and 128 queries of 512 keys 14 us in parts of 2, else 18.
+  static uint32_t parts_of(const Args& a, uint64_t workgroups, uint64_t way, uint64_t full) {
+    const uint64_t shortest = a.type == SPARCML_F32 ? 2 : 4, least = a.type == SPARCML_F32 ? 4 : 16;
+    if (workgroups == 0 || workgroups * 2 > full || way < least) return 1;
+    return (uint32_t)std::min(full / workgroups, way / shortest);
   }
 
   explicit Plan(const Args& a) {
@@ -996,8 +1000,8 @@ struct Plan {
     rows = packing_of(a, kRows, tiles);
     walked = packing_of(a, bn, walked_tiles);
     key_tiles = (a.keys + kRows - 1) / kRows;
-    parts = parts_of(tiles * bg, std::min<uint64_t>(a.keys, reach + rows.ip) / bn);
-    key_parts = parts_of(key_tiles * bg, std::min<uint64_t>(a.queries, reach + kRows) / walked.ip * walked.nh);
+    parts = parts_of(a, tiles * bg, std::min<uint64_t>(a.keys, reach + rows.ip) / bn, 512);
+    key_parts = parts_of(a, key_tiles * bg, std::min<uint64_t>(a.queries, reach + kRows) / walked.ip * walked.nh, a.dim > 64 ? 256 : 512);
     direct = a.dim * (a.type == SPARCML_F32 ? 4 : 2) % 16 == 0 && (a.keys == 0 || (direct_ok(a, a.k, bn, 1) && direct_ok(a, a.v, bn, 1)));
     key_direct = a.dim * (a.type == SPARCML_F32 ? 4 : 2) % 16 == 0 && (a.queries == 0 || (direct_ok(a, a.q, walked.ip, walked.hp) && direct_ok(a, a.dout, walked.ip, walked.hp)));
     dp = (a.dim + 31) / 32 * 32;

@@ -58,8 +58,8 @@ struct Slots {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       typename Part<T, V>::W wa = {}, wb = {};
-      if (there(k, 0)) wa = *reinterpret_cast<const typename Part<T, V>::U*>(p + a(k));
-      if (there(k, 1)) wb = *reinterpret_cast<const typename Part<T, V>::U*>(p + b(k));
+      if (there(k, 0)) wa = __builtin_nontemporal_load(reinterpret_cast<const typename Part<T, V>::U*>(p + a(k)));
+      if (there(k, 1)) wb = __builtin_nontemporal_load(reinterpret_cast<const typename Part<T, V>::U*>(p + b(k)));
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         x[2 * V * k + e] = to_f32((T)wa[e]);
@@ -76,8 +76,8 @@ struct Slots {
         wa[e] = from_f32<T>(x[2 * V * k + e]);
         wb[e] = from_f32<T>(x[2 * V * k + V + e]);
       }
-      if (there(k, 0)) *reinterpret_cast<typename Part<T, V>::U*>(p + a(k)) = wa;
-      if (there(k, 1)) *reinterpret_cast<typename Part<T, V>::U*>(p + b(k)) = wb;
+      if (there(k, 0)) __builtin_nontemporal_store(wa, reinterpret_cast<typename Part<T, V>::U*>(p + a(k)));
+      if (there(k, 1)) __builtin_nontemporal_store(wb, reinterpret_cast<typename Part<T, V>::U*>(p + b(k)));
     }
   }
   __device__ __forceinline__ void weight(float (&w)[E], const float* p) const {
