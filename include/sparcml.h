@@ -630,7 +630,8 @@ sparcml_status sparcml_head_norm_rotate_backward(const sparcml_head_norm_args* a
  * is not read, so it may hold anything. A call repeated gives the same bits.
  *
  *   batch       0 .. 65535 (0: nothing is done)
- *   queries, keys  0 .. 2^29 - 1
+ *   queries, keys  0 .. 2^29 - 1; batch * heads * (the larger of them / 128 + 1)
+ *               < 2^24
  *   heads       1 .. 65535, a multiple of groups
  *   dim         1 .. 128
  *   before, after  UINT32_MAX (or any that reach past the keys): all of them;
@@ -651,9 +652,10 @@ sparcml_status sparcml_head_norm_rotate_backward(const sparcml_head_norm_args* a
  *               NULL where that is 0
  * Nothing written may overlap anything else. With 16-bit types the products'
  * probabilities and ds are rounded to the type, their sums are fp32; with fp32
- * nothing is rounded further. Keys and values that some query of a sequence sees
- * have to be finite: a NaN or an infinity in one of them may reach all its
- * sequence's rows, also those that do not see it. It touches no other sequence.
+ * nothing is rounded further. What some query of a sequence sees, and the queries
+ * that see something and their dout, have to be finite: a NaN or an infinity in
+ * one of them may reach all its sequence's results, also those it has no part
+ * in. It touches no other sequence.
  * ---------------------------------------------------------------------- */
 typedef struct {
   uint32_t type, batch, queries, keys, heads, groups, dim, before, after;

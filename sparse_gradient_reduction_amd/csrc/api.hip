@@ -473,13 +473,13 @@ sparcml_status sparcml_head_norm_rotate_backward(const sparcml_head_norm_args* a
 }
 
 // --------------------------------------------------------------------------
-// what the workspaces are sized by; a launch has fewer than 2^31 workgroups,
-// which take 32 queries or keys at least
+// what the workspaces are sized by; a launch has fewer than 2^24 workgroups of
+// 256 threads, which take 128 queries of a head, or keys
 static bool attention_sizes_ok(const sparcml_attention_args& a) {
   if (!type_ok(a.type) || a.batch > 65535u || a.queries >= (1u << 29) || a.keys >= (1u << 29)) return false;
   if (a.heads == 0 || a.heads > 65535u || a.groups == 0 || a.heads % a.groups != 0) return false;
-  const uint64_t bh = (uint64_t)a.batch * a.heads, most = std::max(a.queries, a.keys) / 32 + 1;
-  return a.dim > 0 && a.dim <= sparcml::kAttentionDim && bh < (1ull << 24) && (bh == 0 || most < (1ull << 31) / bh);
+  const uint64_t bh = (uint64_t)a.batch * a.heads, most = std::max(a.queries, a.keys) / 128 + 1;
+  return a.dim > 0 && a.dim <= sparcml::kAttentionDim && (bh == 0 || most < (1ull << 24) / bh);
 }
 
 static bool attention_args_ok(const sparcml_attention_args& a, bool backward) {

@@ -562,31 +562,35 @@ constexpr int kNormParts = 64;
 template <class T>
 __global__ __launch_bounds__(4 * kWave) void k_attention_norms(Args a, float* norms) {
   __shared__ float most[2][4];
-  const uint32_t bg = blockIdx.x / kNormParts, part = blockIdx.x % kNormParts;
-  const uint32_t b = bg / a.groups, g = bg % a.groups, each = a.heads / a.groups;
-  const Sequence s(a, b);
-  const uint32_t seeing = max(0, s.n - s.m - s.after), in = threadIdx.x % 16 * Pack<T>::N;
-  const uint64_t rows[2] = {(uint64_t)max(0, s.n - (int)seeing) * each, (uint64_t)s.m};
-  float top[2] = {0.0f, 0.0f};
+  const uint32_t items = a.batch * a.groups * kNormParts;
+  for (uint32_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const uint32_t bg = it / kNormParts, part = it % kNormParts;
+    const uint32_t b = bg / a.groups, g = bg % a.groups, each = a.heads / a.groups;
+    const Sequence s(a, b);
+    const uint32_t seeing = max(0, s.n - s.m - s.after), in = threadIdx.x % 16 * Pack<T>::N;
+    const uint64_t rows[2] = {(uint64_t)max(0, s.n - (int)seeing) * each, (uint64_t)s.m};
+    float top[2] = {0.0f, 0.0f};
 #pragma unroll
-  for (int which = 0; which < 2; ++which)
-    for (uint64_t r = part * 16 + threadIdx.x / 16; r < rows[which]; r += 16 * kNormParts) {
-      const T* p = which ? at<T>(a.v, b, r, g) : at<T>(a.dout, b, seeing + r / each, g * each + r % each);
-      const typename Pack<T>::V v = load_pack(p + in, (int64_t)a.dim - in);
-      float sum = 0.0f;
+    for (int which = 0; which < 2; ++which)
+      for (uint64_t r = part * 16 + threadIdx.x / 16; r < rows[which]; r += 16 * kNormParts) {
+        const T* p = which ? at<T>(a.v, b, r, g) : at<T>(a.dout, b, seeing + r / each, g * each + r % each);
+        const typename Pack<T>::V v = load_pack(p + in, (int64_t)a.dim - in);
+        float sum = 0.0f;
 #pragma unroll
-      for (int e = 0; e < Pack<T>::N; ++e) sum = fmaf(to_f32((T)v[e]), to_f32((T)v[e]), sum);
-      top[which] = fmaxf(top[which], lanes_sum<16>(sum));
+        for (int e = 0; e < Pack<T>::N; ++e) sum = fmaf(to_f32((T)v[e]), to_f32((T)v[e]), sum);
+        top[which] = fmaxf(top[which], lanes_sum<16>(sum));
+      }
+    __syncthreads();  // the last item's have been read
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const float v = wave_max(top[which]);
+      if (lane_id() == 0) most[which][threadIdx.x / kWave] = v;
     }
-#pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    const float v = wave_max(top[which]);
-    if (lane_id() == 0) most[which][threadIdx.x / kWave] = v;
-  }
-  __syncthreads();
-  if (threadIdx.x < 2) {
-    const float* v = most[threadIdx.x];
-    norms[(bg * 2 + threadIdx.x) * kNormParts + part] = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+    __syncthreads();
+    if (threadIdx.x < 2) {
+      const float* v = most[threadIdx.x];
+      norms[(bg * 2 + threadIdx.x) * kNormParts + part] = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+    }
   }
 }
 // f of a sequence's key and value head
@@ -1049,7 +1053,8 @@ hipError_t attention_backward_launch(const Args& a, void* ws, hipStream_t stream
   float *stats = static_cast<float*>(ws), *norms = stats + (size_t)a.batch * a.heads * a.queries * 2;
   float* part = stats + stats_floats(a);
   if (a.type == SPARCML_F16)
-    hipLaunchKernelGGL(k_attention_norms<f16>, dim3(a.batch * a.groups * kNormParts), dim3(4 * kWave), 0, stream, a, norms);
+    hipLaunchKernelGGL(k_attention_norms<f16>, dim3(std::min(a.batch * a.groups * kNormParts, 1u << 16)), dim3(4 * kWave), 0,
+                       stream, a, norms);
   if (a.queries > 0) {
     const uint32_t tiles = (uint32_t)plan.tiles, all = tiles * a.batch * a.groups;
     const hipError_t e = with_dim(a, plan.direct, [&](auto t, auto dp, auto d) {

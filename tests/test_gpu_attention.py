@@ -31,6 +31,9 @@ CASES = [
     (1, 3, 4000, 6, 2, 48, True, None, None),        # few queries, few keys: the way is split
     (2, 60, 5000, 2, 1, 128, True, 1500, [(60, 5000), (60, 100)]),
     (2, 4000, 70, 4, 2, 80, False, None, [(4000, 70), (5, 1)]),
+    (1, 9, 40, 130, 1, 16, True, None, None),        # a head's queries in more than one tile
+    (2, 5, 70, 131, 1, 8, False, None, [(5, 70), (3, 66)]),
+    (2, 200, 180, 15, 3, 64, True, None, None),
     (3, 2500, 2500, 1, 1, 32, True, 700, [(2500, 2500), (0, 0), (2000, 2000)]),
     (1, 515, 515, 2, 2, 127, True, None, None),
 ]
@@ -302,3 +305,59 @@ def test_on_another_stream():
         got = sg.attention_backward(dout, q, k, v, o, l)
     side.synchronize()
     assert all(torch.equal(x, y) for x, y in zip((out, lse, *want), (o, l, *got)))
+
+
+def test_places_past_32_bits():
+    """Heads of a wide buffer: sequence 16 starts past element 2^32, tokens are 2^22 elements apart."""
+    b, n, d = 16, 70, 64
+    wide = torch.empty(b, n, 1 << 22, dtype=torch.bfloat16, device="cuda")
+    q, k, v, dout = make(torch.bfloat16, b, n, n, 2, 1, d, seed=16)
+    parts = []
+    for x, at in ((q, 0), (k, 1000), (v, 1 << 21), (dout, 3 << 20)):
+        part = wide[..., at:at + x.shape[2] * d].unflatten(-1, (-1, d))
+        part.copy_(x)
+        parts.append(part)
+    out, lse = sg.attention(*parts[:3], causal=True)
+    got = sg.attention_backward(parts[3], *parts[:3], out, lse, causal=True)
+    plain = [x.cuda() for x in (q, k, v, dout)]
+    want = sg.attention(*plain[:3], causal=True)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    for x, y in zip(got, sg.attention_backward(plain[3], *plain[:3], *want, causal=True)):
+        assert torch.equal(x, y)
+    last = [x[-1:] for x in (q, k, v, dout)]
+    check_forward((out[-1:], lse[-1:]), *last[:3], causal=True)
+
+
+def test_tokens_too_far_apart_for_one_tile():
+    """64 tokens that lie 2^25 elements apart are past what a tile's loads reach without registers."""
+    n, d = 66, 64
+    wide = torch.empty(n, 1 << 25, dtype=torch.bfloat16, device="cuda")
+    q, k, v, dout = make(torch.bfloat16, 1, n, n, 1, 1, d, seed=17)
+    parts = []
+    for x, at in ((q, 0), (k, 1024), (v, 1 << 24), (dout, 3 << 20)):
+        part = wide[:, at:at + d].view(1, n, 1, d)
+        part.copy_(x)
+        parts.append(part)
+    out, lse = sg.attention(*parts[:3])
+    check_forward((out, lse), q, k, v)
+    check_backward(sg.attention_backward(parts[3], *parts[:3], out, lse), dout, q, k, v, out, lse)
+
+
+def test_two_calls_side_by_side():
+    """Calls on two streams, each with a workspace, that split their ways."""
+    a, b = (make(torch.bfloat16, 1, 20, 6000, 4, 4, 64, seed=s) for s in (18, 19))
+    a, b = [x.cuda() for x in a], [x.cuda() for x in b]
+    want = []
+    for q, k, v, dout in (a, b):
+        out, lse = sg.attention(q, k, v)
+        want.append((out, lse, *sg.attention_backward(dout, q, k, v, out, lse)))
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [None, None]
+    for turn in range(3):
+        for i, (q, k, v, dout) in enumerate((a, b)):
+            with torch.cuda.stream(streams[i]):
+                out, lse = sg.attention(q, k, v)
+                got[i] = (out, lse, *sg.attention_backward(dout, q, k, v, out, lse))
+        torch.cuda.synchronize()
+        for x, y in zip(want, got):
+            assert all(torch.equal(u, w) for u, w in zip(x, y))
