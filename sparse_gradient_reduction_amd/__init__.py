@@ -1103,8 +1103,12 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
         _check_lse(lse, head, q)
     args = _ATTENTION_ARGS.pack(*head, *_batch_heads(out), lse.data_ptr(), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
     L = _load()
-    ws, n, workspace = _call_workspace(workspace, L.sparcml_attention_workspace(args), q)
-    st = _on(q.device, L.sparcml_attention, args, ws, n)
+    st = ERR_WORKSPACE
+    if workspace is None:  # most calls need none; those that do say so
+        st = _on(q.device, L.sparcml_attention, args, 0, 0)
+    if st == ERR_WORKSPACE:
+        ws, n, workspace = _call_workspace(workspace, L.sparcml_attention_workspace(args), q)
+        st = _on(q.device, L.sparcml_attention, args, ws, n)
     if st:
         _raise(st, "sparcml_attention")
     return out, lse
