@@ -12,12 +12,17 @@
 // Sums are fp32; an angle is 64 bits up to its place in the turn; 16-bit
 // results are rounded once, at the store.
 //
-// Both are bound by memory. A head's D elements are held by L lanes, two packs
+// Both are bound by memory, large calls by its rate (65536 tokens of 32 + 8 heads
+// of 128, bf16: forward 255 us, 5.3 TB/s, backward 390 us, 5.2 TB/s; a large copy
+// reaches 4.95), small ones by the launch (8 tokens: 4 us of a call's 12). What is
+// read and written is touched once and goes past the caches, which takes 4 of 100
+// off. A head's D elements are held by L lanes, two packs
 // of V elements each, chosen so that a pair is in one lane (halves: the packs
 // are as far apart as the pair's elements; interleaved: the packs are next to
-// each other). A wave takes a token with all its heads: its lanes compute each
-// cosine and sine once, exchange them through LDS and keep their own for all
-// heads of the token, so that no table is read.
+// each other). A wave takes a token with all its heads, or several tokens where
+// they have few: its lanes compute each cosine and sine once, exchange them
+// through LDS and keep their own for all heads of the token, so that no table is
+// read.
 #include <algorithm>
 
 #include "kernels.hpp"
@@ -28,7 +33,6 @@ namespace {
 
 constexpr int kWaves = 4;  // of a workgroup; forward they share nothing, backward the last sums
 constexpr int kThreads = kWaves * kWave;
-constexpr uint32_t kMostPairs = kHeadNormDim / 2;
 
 // V elements at any element's border.
 template <class T, int V>
@@ -96,16 +100,22 @@ template <class S>
 struct Turn {
   float c[S::V * S::K], s[S::V * S::K];
 
-  // Each lane computes those of some pairs of the wave's token into `shared`,
-  // which is the wave's own, and reads those of its pairs.
-  __device__ __forceinline__ void at(const S& slots, int32_t position, const double* frequency, float2* shared) {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");  // the last token's have been read
+  // The lanes compute those of the pairs of the wave's tokens t .. t + count - 1
+  // into `shared`, which is the wave's own, and read those of their pairs of
+  // token t + mine.
+  __device__ __forceinline__ void at(const S& slots, const int32_t* positions, uint64_t t, uint32_t count, uint32_t mine,
+                                     const double* frequency, float2* shared) {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");  // the last tokens' have been read
     __builtin_amdgcn_wave_barrier();
-    for (uint32_t i = lane_id(); i < slots.pairs; i += kWave) {
-      const double turns = (double)position * frequency[i] * 0.15915494309189533577;  // 1 / (2 pi)
+    uint32_t i = lane_id(), n = 0;  // pair i of token t + n
+    while (i >= slots.pairs && n < count) i -= slots.pairs, ++n;
+    while (n < count) {
+      const double turns = (double)positions[t + n] * frequency[i] * 0.15915494309189533577;  // 1 / (2 pi)
       float sine, cosine;
       sincospif((float)(2.0 * (turns - rint(turns))), &sine, &cosine);
-      shared[i] = make_float2(cosine, sine);
+      shared[n * slots.pairs + i] = make_float2(cosine, sine);
+      i += kWave;
+      while (i >= slots.pairs && n < count) i -= slots.pairs, ++n;
     }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -114,7 +124,7 @@ struct Turn {
     for (int k = 0; k < S::K; ++k)
 #pragma unroll
       for (int e = 0; e < S::V; ++e) {
-        const float2 v = slots.turns(k) ? shared[S::slot(k) * S::V + e] : make_float2(1.0f, 0.0f);
+        const float2 v = slots.turns(k) ? shared[mine * slots.pairs + S::slot(k) * S::V + e] : make_float2(1.0f, 0.0f);
         c[S::V * k + e] = v.x;
         s[S::V * k + e] = v.y;
       }
@@ -137,30 +147,53 @@ struct Turn {
   }
 };
 
+// How a wave's S::H groups of lanes are dealt: to `tokens` tokens, `heads` groups
+// each, a power of two that takes a token's heads at once where there are as
+// many (a call of 58454 tokens of 2 query and 2 key heads of 64 takes 26 us so,
+// with all groups to one token's heads 55).
+template <class S>
+struct Dealt {
+  uint32_t heads, tokens, token, head;  // token, head: the lane's first
+  __device__ __forceinline__ explicit Dealt(const sparcml_head_norm_args& g) {
+    const uint32_t most = max(g.heads, g.groups);
+    heads = 1;
+    while (heads < (uint32_t)S::H && heads < most) heads <<= 1;
+    tokens = S::H / heads;
+    token = lane_id() / S::L / heads, head = lane_id() / S::L % heads;
+  }
+  // float2 of LDS for a wave: tokens * pairs, each of the S::H groups' lanes having V * K pairs
+  static constexpr int SHARED = kWave * S::V * S::K;
+};
+
 template <int L>
 __device__ __forceinline__ float head_sum(float v) {
   if (L == 4) return dpp_add<0x4E>(dpp_add<0xB1>(v));  // quad_perm [1,0,3,2], [2,3,0,1]
   return lanes_sum<(L < 8 ? 8 : L)>(v);
 }
 
-// One wave a token: its query heads, then its key heads, S::H of them at once.
+// A wave's tokens: their query heads, then their key heads.
 template <class S>
 __global__ __launch_bounds__(kThreads) void k_head_norm_rotate(sparcml_head_norm_args g) {
   typedef typename S::Type T;
-  __shared__ float2 shared[kWaves][kMostPairs];
+  __shared__ float2 shared[kWaves][Dealt<S>::SHARED];
   const S slots{g.dim, g.rotated / 2};
   float wq[S::E], wk[S::E];
   slots.weight(wq, g.q_weight);
   slots.weight(wk, g.k_weight);
   const float over = 1.0f / (float)g.dim;
-  const uint32_t wid = threadIdx.x / kWave, first = lane_id() / S::L;
-  for (uint64_t t = (uint64_t)blockIdx.x * kWaves + wid; t < g.tokens; t += (uint64_t)gridDim.x * kWaves) {
+  const uint32_t wid = threadIdx.x / kWave;
+  const Dealt<S> dealt(g);
+  for (uint64_t t0 = ((uint64_t)blockIdx.x * kWaves + wid) * dealt.tokens; t0 < g.tokens;
+       t0 += (uint64_t)gridDim.x * kWaves * dealt.tokens) {
+    const uint64_t t = t0 + dealt.token;
     Turn<S> turn;
-    turn.at(slots, g.rotated ? g.positions[t] : 0, g.frequencies, shared[wid]);
+    turn.at(slots, g.positions, t0, g.rotated ? min((uint64_t)dealt.tokens, g.tokens - t0) : 0, dealt.token, g.frequencies,
+            shared[wid]);
+    if (t >= g.tokens) continue;
     const auto heads = [&](uint32_t count, const sparcml_heads& in, const sparcml_heads& out, const float (&w)[S::E]) {
       const T* src = static_cast<const T*>(in.data) + t * in.token;
       T* dst = static_cast<T*>(out.data) + t * out.token;
-      for (uint32_t i = first; i < count; i += S::H) {
+      for (uint32_t i = dealt.head; i < count; i += dealt.heads) {
         float x[S::E], s = 0.0f;
         slots.load(x, src + i * in.head);
 #pragma unroll
@@ -185,25 +218,28 @@ template <class S>
 __global__ __launch_bounds__(kThreads) void k_head_norm_rotate_backward(sparcml_head_norm_args g, uint32_t chunks,
                                                                         uint64_t each, float* part) {
   typedef typename S::Type T;
-  __shared__ float2 shared[kWaves][kMostPairs];
+  __shared__ float2 shared[kWaves][Dealt<S>::SHARED];
   const S slots{g.dim, g.rotated / 2};
   float wq[S::E], wk[S::E], sq[S::E] = {}, sk[S::E] = {};
   slots.weight(wq, g.q_weight);
   slots.weight(wk, g.k_weight);
   const float over = 1.0f / (float)g.dim;
-  const uint32_t wid = threadIdx.x / kWave, first = lane_id() / S::L;
+  const uint32_t wid = threadIdx.x / kWave;
+  const Dealt<S> dealt(g);
   const uint32_t p = blockIdx.x / chunks, c = blockIdx.x % chunks;
   const uint64_t begin = min(c * each, g.tokens), end = min(begin + each, g.tokens);
-  for (uint64_t n = begin + wid; n < end; n += kWaves) {
-    const uint64_t t = p * g.tokens + n;
+  for (uint64_t n = begin + wid * dealt.tokens; n < end; n += kWaves * dealt.tokens) {
+    const uint64_t t = p * g.tokens + n + dealt.token;
     Turn<S> turn;
-    turn.at(slots, g.rotated ? g.positions[t] : 0, g.frequencies, shared[wid]);
+    turn.at(slots, g.positions, p * g.tokens + n, g.rotated ? min((uint64_t)dealt.tokens, end - n) : 0, dealt.token,
+            g.frequencies, shared[wid]);
+    if (n + dealt.token >= end) continue;
     const auto heads = [&](uint32_t count, const sparcml_heads& in, const sparcml_heads& grad, const sparcml_heads& out,
                            const float (&w)[S::E], float (&sw)[S::E]) {
       const T* src = static_cast<const T*>(in.data) + t * in.token;
       const T* dy = static_cast<const T*>(grad.data) + t * grad.token;
       T* dst = static_cast<T*>(out.data) + t * out.token;
-      for (uint32_t i = first; i < count; i += S::H) {
+      for (uint32_t i = dealt.head; i < count; i += dealt.heads) {
         float x[S::E], u[S::E], s = 0.0f, gh = 0.0f;
         slots.load(x, src + i * in.head);
         slots.load(u, dy + i * grad.head);
@@ -286,10 +322,18 @@ hipError_t with_slots(const sparcml_head_norm_args& g, F&& f) {
   });
 }
 
-// Workgroups of a node: 8 to a CU in all, a token at least to each wave.
-uint32_t chunks_of(uint32_t nodes, uint64_t tokens) {
-  const uint64_t most = (2048 + nodes - 1) / nodes, wanted = (tokens + kWaves - 1) / kWaves;
+// Workgroups of a node, 8 to a CU in all, each of whose waves has `least` tokens
+// at least: backward 4, since a workgroup's sums of its weights' gradients take
+// as long as a token's heads do (a call of 64 nodes of 98 tokens, 32 + 4 heads of
+// 32, takes 33 us so, with 1 token 42, with 2 38, with 8 42).
+constexpr uint32_t kLeastTokens = 4;
+uint32_t chunks_of(uint32_t nodes, uint64_t tokens, uint32_t least) {
+  const uint64_t most = (2048 + nodes - 1) / nodes, wanted = (tokens + kWaves * least - 1) / (kWaves * least);
   return (uint32_t)std::max<uint64_t>(1, std::min(most, wanted));
+}
+// tokens of a chunk, as many for each wave
+uint64_t each_of(uint64_t tokens, uint32_t chunks) {
+  return ((tokens + chunks - 1) / chunks + kWaves - 1) / kWaves * kWaves;
 }
 
 }  // namespace
@@ -297,21 +341,21 @@ uint32_t chunks_of(uint32_t nodes, uint64_t tokens) {
 hipError_t head_norm_rotate_launch(const sparcml_head_norm_args& g, hipStream_t stream) {
   return with_slots(g, [&](auto s) {
     using S = decltype(s);
-    hipLaunchKernelGGL(k_head_norm_rotate<S>, dim3(chunks_of(1, g.tokens)), dim3(kThreads), 0, stream, g);
+    hipLaunchKernelGGL(k_head_norm_rotate<S>, dim3(chunks_of(1, g.tokens, 1)), dim3(kThreads), 0, stream, g);
   });
 }
 
 size_t head_norm_rotate_backward_workspace_bytes(uint32_t nodes, uint64_t tokens, uint32_t dim) {
-  return (size_t)nodes * chunks_of(nodes, tokens) * 2 * dim * sizeof(float) + 256;
+  return (size_t)nodes * chunks_of(nodes, tokens, kLeastTokens) * 2 * dim * sizeof(float) + 256;
 }
 
 hipError_t head_norm_rotate_backward_launch(const sparcml_head_norm_args& g, void* ws, hipStream_t stream) {
   float* part = static_cast<float*>(ws);
-  const uint32_t chunks = chunks_of(g.nodes, g.tokens);
+  const uint32_t chunks = chunks_of(g.nodes, g.tokens, kLeastTokens);
   const hipError_t e = with_slots(g, [&](auto s) {
     using S = decltype(s);
     hipLaunchKernelGGL(k_head_norm_rotate_backward<S>, dim3(g.nodes * chunks), dim3(kThreads), 0, stream, g, chunks,
-                       (g.tokens + chunks - 1) / chunks, part);
+                       each_of(g.tokens, chunks), part);
   });
   if (e != hipSuccess || chunks == 1) return e;
   return join_chunks_launch(g.nodes, g.dim, chunks, part, g.dq_weight, g.dq_stride, g.dk_weight, g.dk_stride, stream);
