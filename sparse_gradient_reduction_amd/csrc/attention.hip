@@ -64,9 +64,8 @@ __device__ __forceinline__ T* at(const sparcml_heads& x, uint64_t b, uint64_t t,
 // A result's lane has column lane % 32 and rows 8 (r / 4) + 4 h + r % 4.
 template <class T>
 struct Mma {
-  static constexpr int STEP = 16, MULS = 1;  // MULS: instructions to a mul
+  static constexpr int STEP = 16;
   typedef T Frag __attribute__((ext_vector_type(8)));
-  typedef T Four __attribute__((ext_vector_type(4)));
   static __device__ __forceinline__ Acc mul(Frag a, Frag b, Acc c);
   // rows s * STEP .. of a result, as a right operand
   static __device__ __forceinline__ Frag frag(const Acc& p, int s) {
@@ -86,7 +85,7 @@ __device__ __forceinline__ Acc Mma<f16>::mul(Frag a, Frag b, Acc c) {
 }
 template <>
 struct Mma<float> {
-  static constexpr int STEP = 8, MULS = 4;
+  static constexpr int STEP = 8;
   typedef float Frag __attribute__((ext_vector_type(4)));
   static __device__ __forceinline__ Acc mul(Frag a, Frag b, Acc c) {
 #pragma unroll
@@ -97,20 +96,6 @@ struct Mma<float> {
     return Frag{p[4 * s], p[4 * s + 1], p[4 * s + 2], p[4 * s + 3]};
   }
 };
-
-// Closes a stretch of code whose `muls` matrix instructions are to be issued
-// with `reads` LDS reads, early, and `others` vector instructions between them.
-template <int muls, int reads, int others>
-__device__ __forceinline__ void interleave() {
-  constexpr int R = (reads + muls - 1) / muls + 1, V = (others + muls - 1) / muls;
-#pragma unroll
-  for (int k = 0; k < muls; ++k) {
-    __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
-    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-    if constexpr (V > 0) __builtin_amdgcn_sched_group_barrier(0x2, V, 0);
-  }
-  __builtin_amdgcn_sched_barrier(0);
-}
 
 // ---- tiles in LDS ---------------------------------------------------------------
 // ROWS heads of DP elements, W elements a row, in 16-byte chunks; row r's chunk
@@ -179,7 +164,6 @@ struct Tile {
 struct Packing {
   uint32_t hp, ip, nh;
 };
-
 
 // Waits for this wave's loads and LDS accesses, then for the workgroup's other
 // waves to be there too.
@@ -292,6 +276,7 @@ struct Rows {
     const int tiles = (last - first) / BN + 1, each = (tiles + parts - 1) / parts * BN;
     const int64_t from = first + (int64_t)part * each;
     last = min((int64_t)last, from + each - 1);
+    wave_last = min(wave_last, last);
     first = min(from, (int64_t)last + 1);
   }
   __device__ __forceinline__ Rows() {}
@@ -363,13 +348,20 @@ __device__ __forceinline__ void store_part(const Acc (&acc)[DP / 32], float by, 
           f32x4{acc[t][4 * q], acc[t][4 * q + 1], acc[t][4 * q + 2], acc[t][4 * q + 3]} * by;
 }
 
-constexpr int kKeys = 64;    // keys of a tile, 16-bit; 32 with fp32
+constexpr int kKeys = 64;  // keys of a tile, 16-bit; 32 with fp32
 template <class T>
 constexpr int keys_of() { return sizeof(T) == 2 ? kKeys : kKeys / 2; }
 
 constexpr int kJoinThreads = 256;
 
 // ---- forward --------------------------------------------------------------------
+// Two tiles to a turn, since each is at another place in LDS; the second of the
+// last turn may be past the end, where a wave passes it over like any tile it
+// does not see. (Leaving the loop between the two cost 36 register moves a tile,
+// 4 x 4096 tokens of 32 heads of 128, bf16, 629 us instead of 590.) Of the time
+// there, 930 TFLOP/s, the matrix instructions take half; the rest is the
+// softmax's, 7 vector instructions to each of them, which two waves to a SIMD
+// hide in part.
 template <class T, int DP, int NW, bool DIRECT>
 __global__ __launch_bounds__(NW * kWave, (sizeof(T) == 4 && DP > 64 ? 1 : 2)) void k_attention(Args a, Packing pk, uint32_t tiles,
                                                                          uint32_t parts, float* part) {
@@ -455,7 +447,7 @@ __global__ __launch_bounds__(NW * kWave, (sizeof(T) == 4 && DP > 64 ? 1 : 2)) vo
   if (rows.first <= rows.last) load(rows.first, k0, v0);
   for (int j = rows.first; j <= rows.last; j += 2 * BN) {
     pass(j, k0, v0, k1, v1);
-    if (j + BN <= rows.last) pass(j + BN, k1, v1, k0, v0);
+    pass(j + BN, k1, v1, k0, v0);
   }
   sum = rows.live ? both_halves_sum(sum) : 0.0f;
   if (!rows.there) return;
@@ -612,7 +604,8 @@ __device__ __forceinline__ float factor_of(const float* norms, uint32_t bg) {
 // For dk and dv, what their products take off goes to `stats` ([batch][heads]
 // [queries] each): each row's lse in base 2 less the probabilities' exponent, or
 // +inf where they are 0, with 16-bit types as a score, before its scaling; and
-// its sum of dout * out.
+// its sum of dout * out. 4 x 4096 tokens of 32 heads of 128: 790 us, 1040
+// TFLOP/s, more than half of it matrix instructions.
 template <class T, int DP, int NW, bool DIRECT>
 __global__ __launch_bounds__(NW * kWave, (sizeof(T) == 4 && DP > 64 ? 1 : 2)) void k_attention_dq(Args a, Packing pk, uint32_t tiles, float* stats,
                                                                             const float* norms, uint32_t parts, float* part) {
@@ -696,7 +689,7 @@ __global__ __launch_bounds__(NW * kWave, (sizeof(T) == 4 && DP > 64 ? 1 : 2)) vo
   if (rows.first <= rows.last) load(rows.first, k0, v0);
   for (int j = rows.first; j <= rows.last; j += 2 * BN) {
     pass(j, k0, v0, k1, v1);
-    if (j + BN <= rows.last) pass(j + BN, k1, v1, k0, v0);
+    pass(j + BN, k1, v1, k0, v0);
   }
   if (!rows.there) return;
   const float by = a.scale / f * exp2f(-kBoost<T>);
@@ -724,10 +717,15 @@ __global__ __launch_bounds__(kJoinThreads) void k_attention_join_dq(Args a, Pack
   if (in.slice == 0) in.store(o, at<T>(a.dq, bg / a.groups, rows.i, rows.head), a.dim);
 }
 
-
 // ---- backward: dk and dv --------------------------------------------------------
 // A wave has 32 keys and walks over the tiles of queries that see one of the
-// workgroup's.
+// workgroup's. It holds k, v, dk and dv, with 128-element heads 192 registers, so
+// that there is one wave to a SIMD (the second one's spills took 2800 us instead
+// of 1960 for the gradients of 4 x 4096 tokens of 32 heads of 128) and nothing
+// hides the vector instructions between the products, nor the reads from LDS.
+// The mask is applied in the middle of the one way through a tile's products:
+// a way of its own for masked tiles had the results moved to other registers at
+// its end, 2150 us instead of 1960.
 template <class T, int DP, int NW, bool DIRECT>
 __global__ __launch_bounds__(NW * kWave, (DP > 64 ? 1 : 2)) void k_attention_dkv(
     Args a, Packing pk, uint32_t tiles, const float* stats, const float* norms, uint32_t parts, float* part) {
@@ -769,8 +767,7 @@ __global__ __launch_bounds__(NW * kWave, (DP > 64 ? 1 : 2)) void k_attention_dkv
   if (threadIdx.x < BM) query[threadIdx.x] = my_i;
   // Where the next tile is: its first query, its heads, and what follows from
   // them. Moved on instead of computed again, since divisions and products of
-  // 64 bits between two tiles would take longer than the tile (8 scalar
-  // instructions to a matrix one, 1558 us for 16384 tokens' gradients).
+  // 64 bits between two tiles would take longer than the tile.
   struct {
     int i0;
     uint32_t chunk;
@@ -812,7 +809,7 @@ __global__ __launch_bounds__(NW * kWave, (DP > 64 ? 1 : 2)) void k_attention_dkv
     ld.load(at_tile.d, seeing - at_tile.i0, s.n - at_tile.i0, dt);
   };
   typename TL::Places places;
-  const auto products = [&](auto masked, int i0, const I4* qt, const I4* dt, const float (&row)[2][BM]) {
+  const auto products = [&](bool masked, int i0, const I4* qt, const I4* dt, const float (&row)[2][BM]) {
     places.make_new();
     // the key's way from the first one that the tile's first query may see; past all of them where there is no key
     const uint32_t far = j < s.m ? (uint32_t)(j - i0 - s.m + s.n + s.before) : 0xFFFFFF00u;
@@ -842,7 +839,10 @@ __global__ __launch_bounds__(NW * kWave, (DP > 64 ? 1 : 2)) void k_attention_dkv
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         p[r] = __builtin_amdgcn_exp2f(sizeof(T) == 2 ? p[r] * c : fmaf(p[r], c, row[0][h4 + 8 * (r / 4) + r % 4]));
-        if constexpr (masked) p[r] = far - query[h4 + 8 * (r / 4) + r % 4] > span ? 0.0f : p[r];
+      }
+      if (masked) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) p[r] = far - query[h4 + 8 * (r / 4) + r % 4] > span ? 0.0f : p[r];
       }
 #pragma unroll
       for (int x = 0; x < 32 / M::STEP; ++x) {
@@ -873,9 +873,8 @@ __global__ __launch_bounds__(NW * kWave, (DP > 64 ? 1 : 2)) void k_attention_dkv
       load(qn, dn);
     }
     // some query of the tile sees some key of the wave, or all see all
-    if (w0 < end && w0 <= s.last(i1) && min(w0 + 31, end - 1) >= s.first(i0)) {
-      if (w0 < s.first(i1) || w0 + 31 > s.last(i0)) products(std::true_type{}, i0, qt, dt, stat[turn]);
-      else products(std::false_type{}, i0, qt, dt, stat[turn]);
+    if (n < count && w0 < end && w0 <= s.last(i1) && min(w0 + 31, end - 1) >= s.first(i0)) {
+      products(w0 < s.first(i1) || w0 + 31 > s.last(i0), i0, qt, dt, stat[turn]);
     }
     keep(next, turn ^ 1);
   };
@@ -889,7 +888,7 @@ __global__ __launch_bounds__(NW * kWave, (DP > 64 ? 1 : 2)) void k_attention_dkv
     load(q0, d0);
     for (int n = 0; n < count; n += 2) {
       pass(n, q0, d0, q1, d1, 0);
-      if (n + 1 < count) pass(n + 1, q1, d1, q0, d0, 1);
+      pass(n + 1, q1, d1, q0, d0, 1);
     }
   }
   if (!there) return;
