@@ -47,6 +47,10 @@ struct Sequence {
   }
   __device__ __forceinline__ int first(int i) const { return max(0, i + m - n - before); }
   __device__ __forceinline__ int last(int i) const { return min(m - 1, i + m - n + after); }
+  // Keys from here on, up to m, are seen by some query, those before it by none:
+  // they may hold anything, and a probability of 0 times what is not finite is
+  // no 0.
+  __device__ __forceinline__ int first_seen() const { return n > 0 ? first(0) : m; }
 };
 
 template <class T>
@@ -745,8 +749,9 @@ __global__ __launch_bounds__(NW * kWave, (DP > 64 ? 1 : 2)) void k_attention_dkv
   const bool there = j < (int)a.keys;
 
   Frag k[TL::STEPS], v[TL::STEPS];
-  load_row<T, TL, DIRECT>(k, a.k, b, j, g, j < s.m, a.dim);
-  load_row<T, TL, DIRECT>(v, a.v, b, j, g, j < s.m, a.dim);
+  const bool seen = j >= s.first_seen() && j < s.m;
+  load_row<T, TL, DIRECT>(k, a.k, b, j, g, seen, a.dim);
+  load_row<T, TL, DIRECT>(v, a.v, b, j, g, seen, a.dim);
   const float f = factor_of<T>(norms, bg);
   Acc dk[DP / 32] = {}, dv[DP / 32] = {};
 
