@@ -553,7 +553,9 @@ template <class T>
 constexpr float kBoost = sizeof(T) == 2 && std::is_same<T, f16>::value ? 14.0f : 0.0f;  // as an exponent
 
 // The largest sum of squares of a row of dout and of v, of one of kNormParts
-// parts of the rows of each sequence's key and value head.
+// parts of the rows of each sequence's key and value head that take part: the
+// queries that see something and the keys that are seen. The others may hold
+// anything.
 constexpr int kNormParts = 64;
 template <class T>
 __global__ __launch_bounds__(4 * kWave) void k_attention_norms(Args a, float* norms) {
@@ -563,13 +565,13 @@ __global__ __launch_bounds__(4 * kWave) void k_attention_norms(Args a, float* no
     const uint32_t bg = it / kNormParts, part = it % kNormParts;
     const uint32_t b = bg / a.groups, g = bg % a.groups, each = a.heads / a.groups;
     const Sequence s(a, b);
-    const uint32_t seeing = max(0, s.n - s.m - s.after), in = threadIdx.x % 16 * Pack<T>::N;
-    const uint64_t rows[2] = {(uint64_t)max(0, s.n - (int)seeing) * each, (uint64_t)s.m};
+    const uint32_t seeing = max(0, s.n - s.m - s.after), seen = s.first_seen(), in = threadIdx.x % 16 * Pack<T>::N;
+    const uint64_t rows[2] = {(uint64_t)max(0, s.n - (int)seeing) * each, (uint64_t)max(0, s.m - (int)seen)};
     float top[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int which = 0; which < 2; ++which)
       for (uint64_t r = part * 16 + threadIdx.x / 16; r < rows[which]; r += 16 * kNormParts) {
-        const T* p = which ? at<T>(a.v, b, r, g) : at<T>(a.dout, b, seeing + r / each, g * each + r % each);
+        const T* p = which ? at<T>(a.v, b, seen + r, g) : at<T>(a.dout, b, seeing + r / each, g * each + r % each);
         const typename Pack<T>::V v = load_pack(p + in, (int64_t)a.dim - in);
         float sum = 0.0f;
 #pragma unroll

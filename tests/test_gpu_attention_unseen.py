@@ -21,7 +21,7 @@ CASES = [
     (3, 40, 260, 4, 2, 96, True, 20, [(40, 140), (0, 77), (7, 227)]),
     (1, 1, 48, 1, 1, 33, True, 31, None),
 ]
-ODD = {"nan": [math.nan], "infinite": [math.inf, -math.inf]}
+ODD = {"nan": [math.nan], "infinite": [math.inf, -math.inf], "huge": [3e4, -6e4]}
 
 
 def unseen_keys(batch, queries, keys, causal, window, lengths):
@@ -37,7 +37,7 @@ def both(q, k, v, dout, lengths, mask):
 
 
 @pytest.mark.parametrize("t,odd,which", [(t, odd, which) for t in TYPES for odd in ("nan", "infinite") for which in "kv"
-                                         if (t, odd, which) != (torch.float16, "infinite", "v")])
+                                         if (t, odd, which) != (torch.float16, "infinite", "v")])  # that one: below
 @pytest.mark.parametrize("case", CASES)
 def test_gradients_of_unseen_keys_are_zero(t, odd, which, case):
     batch, queries, keys, heads, groups, dim, causal, window, lengths = case
@@ -55,3 +55,22 @@ def test_gradients_of_unseen_keys_are_zero(t, odd, which, case):
     for x, y, name in zip(got, want, ("out", "lse", "dq", "dk", "dv")):
         assert torch.equal(x, y), name
     assert bool((got[3].cpu()[unseen] == 0).all()) and bool((got[4].cpu()[unseen] == 0).all())
+
+
+@pytest.mark.parametrize("odd", ["infinite", "huge"])
+@pytest.mark.parametrize("case", CASES)
+def test_unseen_values_do_not_size_fp16_gradients(odd, case):
+    """fp16 holds ds by the largest values that some query sees."""
+    batch, queries, keys, heads, groups, dim, causal, window, lengths = case
+    mask = {"causal": causal, "window": window}
+    q, k, v, dout = make(torch.float16, batch, queries, keys, heads, groups, dim, seed=22)
+    dout = (dout.float() * 100).half()
+    unseen = unseen_keys(batch, queries, keys, causal, window, lengths)
+    v[unseen] = 0
+    want = both(q, k, v, dout, lengths, mask)
+    check_backward(want[2:], dout, q, k, v, *want[:2], lengths, **mask)
+    dirty = v.clone()
+    dirty[unseen] = torch.tensor(ODD[odd]).half()[torch.arange(dim) % len(ODD[odd])]
+    got = both(q, k, dirty, dout, lengths, mask)
+    for x, y, name in zip(got, want, ("out", "lse", "dq", "dk", "dv")):
+        assert torch.equal(x, y), name
