@@ -359,6 +359,22 @@ constexpr int keys_of() { return sizeof(T) == 2 ? kKeys : kKeys / 2; }
 constexpr int kJoinThreads = 256;
 
 // ---- forward --------------------------------------------------------------------
+// The probabilities go to the second product in the type, 2^kHeld times as
+// large as they are below the running maximum, which is moved on where a score
+// passes it by a factor of 2^kPast. fp16 has 40 binary digits from its smallest
+// to its largest value: held at 2^13 and 2^2 past that, at most 2^15, those of
+// 2^-27 of the maximum have all their digits and those of 2^-38 are lost (held
+// at 1, 2^-14 and 2^-25: a row whose result is made of many such keys beside a
+// large one of value 0 lost its result). The larger kPast, the fewer rescalings:
+// 2^2 instead of 2^8 takes nothing that shows at 4 x 4096 tokens (585 and 592
+// us, where bf16's unchanged code gave 555 and 563) and up to 4 of 100 where ways
+// are short (5 x 1001 padded tokens, a window of 300: 16.6 and 17.2 us). bf16 has
+// fp32's range.
+template <class T>
+constexpr float kHeld = std::is_same<T, f16>::value ? 13.0f : 0.0f;  // both as exponents
+template <class T>
+constexpr float kPast = std::is_same<T, f16>::value ? 2.0f : 8.0f;
+
 // Two tiles to a turn, since each is at another place in LDS; the second of the
 // last turn may be past the end, where a wave passes it over like any tile it
 // does not see. (Leaving the loop between the two cost 36 register moves a tile,
@@ -415,7 +431,7 @@ __global__ __launch_bounds__(NW * kWave, (sizeof(T) == 4 && DP > 64 ? 1 : 2)) vo
 #pragma unroll
       for (int r = 0; r < 16; ++r) now = fmaxf(now, p[t][r]);
     now = both_halves_max(now) * c;
-    if (ballot(now > top + 8.0f)) {
+    if (ballot(now > top + kPast<T>)) {
       const float higher = fmaxf(now, top), keep = higher == top ? 1.0f : __builtin_amdgcn_exp2f(top - higher);
       top = higher;
       sum *= keep;
@@ -424,7 +440,7 @@ __global__ __launch_bounds__(NW * kWave, (sizeof(T) == 4 && DP > 64 ? 1 : 2)) vo
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[t][r] *= keep;
     }
-    const float off = top == -INFINITY ? 0.0f : top;
+    const float off = top == -INFINITY ? 0.0f : top - kHeld<T>;
 #pragma unroll
     for (int t = 0; t < BN / 32; ++t)
 #pragma unroll
@@ -455,6 +471,7 @@ __global__ __launch_bounds__(NW * kWave, (sizeof(T) == 4 && DP > 64 ? 1 : 2)) vo
   }
   sum = rows.live ? both_halves_sum(sum) : 0.0f;
   if (!rows.there) return;
+  top -= kHeld<T>;  // what sum and o are relative to
   if (parts > 1) {
     const uint64_t row = (uint64_t)id * (NW * 32) + threadIdx.x / kWave * 32 + lane_id() % 32;
     if (lane_id() < 32) reinterpret_cast<float2*>(part)[row] = make_float2(top, sum);
