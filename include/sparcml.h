@@ -652,7 +652,12 @@ sparcml_status sparcml_head_norm_rotate_backward(const sparcml_head_norm_args* a
  *               NULL where that is 0
  * Nothing written may overlap anything else. With 16-bit types the products'
  * probabilities and ds are rounded to the type, their sums are fp32; with fp32
- * nothing is rounded further. What some query of a sequence sees, and the queries
+ * nothing is rounded further. fp16 has few digits below 1: a probability loses
+ * some below 2^-27 of its row's largest and is 0 below 2^-38 of it (for dv below
+ * 2^-28 and 2^-39), ds below 2^-28 and 2^-39 of |dout| |v|. There |v| is the largest
+ * of the values that a query of the sequence and the key and value head sees,
+ * |dout| the query's own for dq, and the largest of those queries for dk: dk of a
+ * key that only queries of far smaller dout see has fewer digits. What some query of a sequence sees, and the queries
  * that see something and their dout, have to be finite: a NaN or an infinity in
  * one of them may reach all its sequence's results, also those it has no part
  * in. It touches no other sequence.

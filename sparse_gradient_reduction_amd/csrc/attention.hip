@@ -562,10 +562,13 @@ __global__ __launch_bounds__(kJoinThreads) void k_attention_join(Args a, Packing
 // ---- backward -------------------------------------------------------------------
 // fp16 has 40 binary digits from its smallest to its largest value, fewer than
 // probabilities of long rows and ds of small gradients take. So p is held 2^14
-// times as large, and ds, which is at most 2 p |dout| |v|, 2^14 f times, f the
-// power of two that brings the largest |dout| |v| of a key and value head of a
-// sequence to 1/2 .. 1: at most 2^15, and no other digits are lost than those of
-// values 2^-25 times as large. bf16 has fp32's range, f and both factors are 1.
+// times as large, and ds, which is at most 2 p |dout| |v|, 2^14 f times, f a
+// power of two that brings |dout| |v| to 1/2 .. 1: at most 2^15, and digits of a
+// ds are lost below 2^-28 |dout| |v| and all of it below 2^-39. |v| is the largest
+// of the key and value head's in a sequence; |dout| is the row's own for dq, so
+// that rows of any size keep their digits, and for dk, whose sums run over the
+// rows, the largest, too: keys that only rows of far smaller dout see lose
+// digits of their dk. bf16 has fp32's range, f and both factors are 1.
 template <class T>
 constexpr float kBoost = sizeof(T) == 2 && std::is_same<T, f16>::value ? 14.0f : 0.0f;  // as an exponent
 
@@ -608,19 +611,16 @@ __global__ __launch_bounds__(4 * kWave) void k_attention_norms(Args a, float* no
     }
   }
 }
-// f of a sequence's key and value head
-template <class T>
-__device__ __forceinline__ float factor_of(const float* norms, uint32_t bg) {
-  if constexpr (kBoost<T> == 0.0f) {
-    return 1.0f;
-  } else {
-    const float* v = norms + bg * 2 * kNormParts + lane_id();
-    const float most = sqrtf(wave_max(v[0])) * sqrtf(wave_max(v[kNormParts]));
-    if (!(most > 0.0f) || most == INFINITY) return 1.0f;
-    int e;
-    frexpf(most, &e);
-    return ldexpf(1.0f, -e);
-  }
+// The largest norm of a row of dout (which = 0) or v (1) of a sequence's key and value head.
+__device__ __forceinline__ float largest_norm(const float* norms, uint32_t bg, int which) {
+  return sqrtf(wave_max(norms[(bg * 2 + which) * kNormParts + lane_id()]));
+}
+// the power of two that brings `most` to 1/2 .. 1
+__device__ __forceinline__ float factor_of(float most) {
+  if (!(most > 0.0f) || most == INFINITY) return 1.0f;
+  int e;
+  frexpf(most, &e);
+  return ldexpf(1.0f, -e);
 }
 
 // ---- backward: dq ---------------------------------------------------------------
@@ -662,8 +662,16 @@ __global__ __launch_bounds__(NW * kWave, (sizeof(T) == 4 && DP > 64 ? 1 : 2)) vo
       stats[where + (uint64_t)a.batch * a.heads * a.queries] = -delta;
     }
   }
-  const float f = factor_of<T>(norms, bg);
-  delta *= f;
+  float f = 1.0f;
+  if constexpr (kBoost<T> != 0.0f) {
+    float size = 0.0f;
+#pragma unroll
+    for (int x = 0; x < TL::STEPS; ++x)
+#pragma unroll
+      for (int e = 0; e < TL::PACK; ++e) size = fmaf(to_f32((T)d[x][e]), to_f32((T)d[x][e]), size);
+    f = factor_of(sqrtf(both_halves_sum(size)) * largest_norm(norms, bg, 1));
+    delta *= f;
+  }
   Acc o[DP / 32] = {};
 
   const Packing one{1, BN, 1};
@@ -771,7 +779,8 @@ __global__ __launch_bounds__(NW * kWave, (DP > 64 ? 1 : 2)) void k_attention_dkv
   const bool seen = j >= s.first_seen() && j < s.m;
   load_row<T, TL, DIRECT>(k, a.k, b, j, g, seen, a.dim);
   load_row<T, TL, DIRECT>(v, a.v, b, j, g, seen, a.dim);
-  const float f = factor_of<T>(norms, bg);
+  float f = 1.0f;
+  if constexpr (kBoost<T> != 0.0f) f = factor_of(largest_norm(norms, bg, 0) * largest_norm(norms, bg, 1));
   Acc dk[DP / 32] = {}, dv[DP / 32] = {};
 
   // queries first .. last see one of the workgroup's keys

@@ -1,5 +1,5 @@
-"""fp16 attention whose results are made of small probabilities: fp16 has few
-binary digits below 1."""
+"""fp16 attention whose results are made of small probabilities, or of gradients
+of unequal size: fp16 has few binary digits below 1."""
 import math
 
 import pytest
@@ -7,7 +7,7 @@ import torch
 
 import sparse_gradient_reduction_amd as sg
 from tests import attention_util as au
-from tests.operator_util import assert_within
+from tests.operator_util import assert_within, half_step
 from tests.test_gpu_attention import check_forward, make
 
 pytestmark = pytest.mark.gpu
@@ -75,3 +75,40 @@ def test_random_scores(sharp):
     got = sg.attention(q.cuda(), k.cuda(), v.cuda())
     check_forward(got, q, k, v)
     check_small(got, q, k, v)
+
+
+def assert_rounded(got, ref, tol, name):
+    """assert_within, with values from 65520 on (half a step past fp16's largest, 65504) rounded to infinity."""
+    got, limit = got.double().cpu(), 65520
+    past, may_be = ref.abs() - tol >= limit, (ref.abs() + tol >= limit) & (got.abs() == math.inf)
+    assert torch.equal(got[past], math.inf * ref[past].sign())
+    assert torch.equal(got[may_be].sign(), ref[may_be].sign())
+    rest = ~(past | may_be)
+    assert_within(got[rest], ref[rest], tol[rest], name)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("keys", [200, 3000])
+def test_gradients_of_rows_of_unequal_size(causal, keys):
+    """A row's dq has the digits that its own dout leaves, whatever other rows'
+    are; the queries' dout falls from 2^12 to 2^-12. With the ds of a row below
+    2^15 and its steps 2^-25 at worst (half of fp16's smallest), dq is off by
+    2^-36 |dout| max |v| a key, |dout| that row's own."""
+    n, d, scale = 90, 64, 0.125
+    q, k, v, dout = make(torch.float16, 1, n, keys, 2, 1, d, seed=32)
+    v = (v.float() * 500).half()
+    dout = (dout.float() * 2.0 ** torch.linspace(12, -12, n).view(1, -1, 1, 1)).half()
+    gq, gk, gv, gd = (x.cuda() for x in (q, k, v, dout))
+    out, lse = sg.attention(gq, gk, gv, causal=causal, scale=scale)
+    got = sg.attention_backward(gd, gq, gk, gv, out, lse, causal=causal, scale=scale)
+    for x, (ref, tol), name in zip(got, au.backward(dout, q, k, v, out.cpu(), lse.cpu(), causal=causal, scale=scale), ("dq", "dk", "dv")):
+        assert_rounded(x, ref, tol, name)
+    for h in range(2):
+        x = [y.double() for y in (dout[0, :, h], q[0, :, h], k[0, :, 0], v[0, :, 0], out[0, :, h].cpu(), lse[0, h].cpu())]
+        see = au.sees(n, keys, n, keys, causal, None)
+        r = au.head_backward(*x, see, scale, torch.float16)
+        own = x[0].norm(dim=1, keepdim=True)
+        spare = 2.0 ** -36 * (own.max() - own) * x[3].norm(dim=1).max()  # of the other rows' size
+        tol = r[3] - scale * (see * spare) @ x[2].abs() + half_step(torch.float16, r[0])
+        assert bool((tol > 0).all())
+        assert_rounded(got[0][0, :, h], r[0], tol, "dq")
