@@ -373,6 +373,8 @@ constexpr int kJoinThreads = 256;
 template <class T>
 constexpr float kHeld = std::is_same<T, f16>::value ? 13.0f : 0.0f;  // both as exponents
 template <class T>
+constexpr float kBack = kHeld<T> == 0.0f ? 1.0f : 0x1p-13f;  // 2^-kHeld: takes it off sums exactly
+template <class T>
 constexpr float kPast = std::is_same<T, f16>::value ? 2.0f : 8.0f;
 
 // Two tiles to a turn, since each is at another place in LDS; the second of the
@@ -469,16 +471,15 @@ __global__ __launch_bounds__(NW * kWave, (sizeof(T) == 4 && DP > 64 ? 1 : 2)) vo
     pass(j, k0, v0, k1, v1);
     pass(j + BN, k1, v1, k0, v0);
   }
-  sum = rows.live ? both_halves_sum(sum) : 0.0f;
+  sum = rows.live ? both_halves_sum(sum) * kBack<T> : 0.0f;
   if (!rows.there) return;
-  top -= kHeld<T>;  // what sum and o are relative to
   if (parts > 1) {
     const uint64_t row = (uint64_t)id * (NW * 32) + threadIdx.x / kWave * 32 + lane_id() % 32;
     if (lane_id() < 32) reinterpret_cast<float2*>(part)[row] = make_float2(top, sum);
-    store_part<DP>(o, 1.0f, part + (uint64_t)gridDim.x * (NW * 32) * 2 + row * DP);
+    store_part<DP>(o, kBack<T>, part + (uint64_t)gridDim.x * (NW * 32) * 2 + row * DP);
     return;
   }
-  store_row<T, DP>(o, sum == 0.0f ? 0.0f : 1.0f / sum, at<T>(a.out, b, rows.i, rows.head), a.dim);
+  store_row<T, DP>(o, sum == 0.0f ? 0.0f : kBack<T> / sum, at<T>(a.out, b, rows.i, rows.head), a.dim);
   if (lane_id() < 32) a.lse[((uint64_t)b * a.heads + rows.head) * a.queries + rows.i] = sum == 0.0f ? -INFINITY : top * kLn2 + logf(sum);
 }
 

@@ -77,6 +77,16 @@ def test_random_scores(sharp):
     check_small(got, q, k, v)
 
 
+@pytest.mark.parametrize("keys", [1, 64, 1024, 16384])
+def test_equal_scores_have_an_exact_sum(keys):
+    """Scores of 0 over 2^n keys: lse is the logarithm of 2^n, rounded as fp32's is (and 0 for one key)."""
+    q, k = torch.zeros(1, 3, 1, 64, dtype=torch.float16, device="cuda"), torch.ones(1, keys, 1, 64, dtype=torch.float16, device="cuda")
+    out, lse = sg.attention(q, k, k)
+    _, lse32 = sg.attention(q.float(), k.float(), k.float())
+    assert bool((out == 1).all()) and torch.equal(lse, lse32)
+    assert abs(float(lse[0, 0, 0]) - math.log(keys)) <= 4 * 2.0 ** -24 * math.log(keys)
+
+
 def assert_rounded(got, ref, tol, name):
     """assert_within, with values from 65520 on (half a step past fp16's largest, 65504) rounded to infinity."""
     got, limit = got.double().cpu(), 65520
