@@ -636,7 +636,7 @@ sparcml_status sparcml_head_norm_rotate_backward(const sparcml_head_norm_args* a
  *   dim         1 .. 128
  *   before, after  UINT32_MAX (or any that reach past the keys): all of them;
  *               after = 0: causal
- *   scale       finite, >= 1e-30
+ *   scale       1e-30 .. 1e30
  *   q_lengths, k_lengths  device, [batch] int32, n and m of each sequence,
  *               taken as 0 and as queries or keys where they lie outside;
  *               NULL: all of them

@@ -1033,8 +1033,8 @@ def _attention_checks(q, k, v, causal, window, scale, q_lengths, k_lengths):
         raise ValueError(f"{heads} heads do not share {groups} groups of keys and values in equal parts")
     if scale is None:
         scale = cols ** -0.5
-    elif not 1e-30 <= scale < math.inf:
-        raise ValueError("scale must be finite and at least 1e-30")
+    elif not 1e-30 <= scale <= 1e30:
+        raise ValueError("scale must lie between 1e-30 and 1e30")
     n = m = 0
     if q_lengths is not None:
         n = _lengths(q_lengths, batch, dev, "q_lengths")

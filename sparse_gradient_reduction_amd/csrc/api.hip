@@ -482,8 +482,12 @@ static bool attention_sizes_ok(const sparcml_attention_args& a) {
   return a.dim > 0 && a.dim <= sparcml::kAttentionDim && (bh == 0 || most < (1ull << 24) / bh);
 }
 
+// The kernels multiply the scale by log2 e and, for fp16, by up to 2^26, and
+// divide by it: all of that stays finite.
+static bool attention_scale_ok(float scale) { return scale >= 1e-30f && scale <= 1e30f; }
+
 static bool attention_args_ok(const sparcml_attention_args& a, bool backward) {
-  if (!attention_sizes_ok(a) || !std::isfinite(a.scale) || !(a.scale >= 1e-30f)) return false;
+  if (!attention_sizes_ok(a) || !attention_scale_ok(a.scale)) return false;
   if ((a.q_lengths && (reinterpret_cast<uintptr_t>(a.q_lengths) & 3u)) ||
       (a.k_lengths && (reinterpret_cast<uintptr_t>(a.k_lengths) & 3u)))
     return false;

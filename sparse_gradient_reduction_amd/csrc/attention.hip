@@ -724,7 +724,7 @@ __global__ __launch_bounds__(NW * kWave, (sizeof(T) == 4 && DP > 64 ? 1 : 2)) vo
     pass(j + BN, k1, v1, k0, v0);
   }
   if (!rows.there) return;
-  const float by = a.scale / f * exp2f(-kBoost<T>);
+  const float by = a.scale * (exp2f(-kBoost<T>) / f);
   if (parts == 1) store_row<T, DP>(o, by, at<T>(a.dq, b, rows.i, rows.head), a.dim);
   else store_part<DP>(o, by, part + ((uint64_t)id * (NW * 32) + threadIdx.x / kWave * 32 + lane_id() % 32) * DP);
 }
@@ -926,7 +926,7 @@ __global__ __launch_bounds__(NW * kWave, (DP > 64 ? 1 : 2)) void k_attention_dkv
     }
   }
   if (!there) return;
-  const float byk = a.scale / f * exp2f(-kBoost<T>), byv = exp2f(-kBoost<T>);
+  const float byk = a.scale * (exp2f(-kBoost<T>) / f), byv = exp2f(-kBoost<T>);
   if (parts == 1) {
     store_row<T, DP>(dk, byk, at<T>(a.dk, b, j, g), a.dim);
     store_row<T, DP>(dv, byv, at<T>(a.dv, b, j, g), a.dim);
