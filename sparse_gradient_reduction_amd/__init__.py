@@ -887,9 +887,9 @@ def _on(device, call, *args) -> int:
 
 
 def _token_heads(t: torch.Tensor, name: str):
-    """sparcml_heads of [..., heads, D] whose tokens are evenly spaced."""
-    if t.dim() == 3:
-        return t.data_ptr(), 0, t.stride(0), t.stride(1)
+    """sparcml_heads of [..., heads, D] whose tokens are evenly spaced (where there are none, any)."""
+    if t.dim() == 3 or t.numel() == 0:
+        return t.data_ptr(), 0, t.stride(-3), t.stride(-2)
     step, size = 0, 1  # of the tokens' dimensions from the inside out
     for d in range(t.dim() - 3, -1, -1):
         n = t.shape[d]
