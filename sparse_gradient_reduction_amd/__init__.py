@@ -782,6 +782,8 @@ def _node_rows(t: Optional[torch.Tensor], nodes: int, cols: int, like: torch.Ten
         return like.new_empty((nodes, cols), dtype=torch.float32), cols
     if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_cuda:
         raise TypeError(f"{name} must be a float32 tensor on a GPU")
+    if t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}")
     if tuple(t.shape) != (nodes, cols) or (cols > 1 and t.stride(1) != 1) or (nodes > 1 and t.stride(0) < cols):
         raise ValueError(f"{name} must be [{nodes}, {cols}] with contiguous rows that do not overlap")
     return t, max(t.stride(0), cols)
