@@ -720,6 +720,8 @@ def _workspace(t: Optional[torch.Tensor], need: int, like: torch.Tensor) -> torc
     if t is None:
         return like.new_empty(need, dtype=torch.uint8)
     _check_dev(t, torch.uint8, "workspace")
+    if t.device != like.device:
+        raise ValueError(f"workspace must be on {like.device}")
     return t
 
 
@@ -1071,8 +1073,6 @@ def _call_workspace(t: Optional[torch.Tensor], need: int, like: torch.Tensor):
     if t is None and need == 0:
         return 0, 0, None
     t = _workspace(t, need, like)
-    if t.device != like.device:
-        raise ValueError(f"workspace must be on {like.device}")
     return t.data_ptr(), t.numel(), t
 
 
