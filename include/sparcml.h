@@ -591,8 +591,9 @@ typedef struct {
  *               (nodes, tokens, dim) bytes, 256-byte aligned; content does not
  *               matter
  * q_out and k_out may be q and k (the backward's also dq and dk) with the same
- * strides; apart from that nothing written may overlap anything else. A NaN or
- * an infinity in a head touches no other head's results.
+ * strides; apart from that nothing written may overlap anything else. Sums are
+ * fp32, that of a head's squares too: it has to stay below 2^128. A NaN or an
+ * infinity in a head touches no other head's results.
  * ---------------------------------------------------------------------- */
 typedef struct {
   uint32_t type, nodes, heads, groups, dim, rotated, interleaved;

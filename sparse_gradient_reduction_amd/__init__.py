@@ -957,9 +957,11 @@ def head_norm_rotate(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.
     or fp16; views of one projection, say): x / sqrt(mean(x^2) + eps) * weight,
     with fp32 weights of D elements, then turns pair i of its first
     2 * len(frequencies) elements by position * frequencies[i] (int32 positions of
-    q.shape[:-2], fp64 frequencies; none: nothing turns). Pair i is elements i and
-    i + len(frequencies), or 2 i and 2 i + 1 where `interleaved`. Returns (q_out,
-    k_out), which may be q and k themselves."""
+    q.shape[:-2], fp64 frequencies; none: nothing turns, whatever the positions).
+    Pair i is elements i and i + len(frequencies), or 2 i and 2 i + 1 where
+    `interleaved`. Tokens of several dimensions have to be evenly spaced in memory,
+    as those of a contiguous tensor's heads are. Returns (q_out, k_out), which may
+    be q and k themselves and overlap nothing else."""
     t, tokens, heads, groups, cols, rotated = _head_norm_checks(q, k, q_weight, k_weight, positions, frequencies)
     q_out, k_out = _output_heads(q_out, q, "q_out"), _output_heads(k_out, k, "k_out")
     args = _HEAD_NORM_ARGS.pack(t, 1, heads, groups, cols, rotated, interleaved, eps, tokens, *_token_heads(q, "q"),
@@ -990,7 +992,8 @@ def head_norm_rotate_backward(dq: torch.Tensor, dk: torch.Tensor, q: torch.Tenso
     `q` and `k` its inputs: (like q, like k, dq_weight [nodes, D], dk_weight
     [nodes, D], both fp32). The tokens belong to `nodes` nodes in equal parts, one
     after the other. q_out and k_out may be dq and dk (or q and k); dq_weight and
-    dk_weight may be columns of the [P, N] gradients."""
+    dk_weight may be columns of the [P, N] gradients. Apart from that nothing that
+    is written may overlap anything else."""
     t, tokens, heads, groups, cols, rotated = _head_norm_checks(q, k, q_weight, k_weight, positions, frequencies)
     if not (_alike(q, q.stride(), dq) and _alike(k, k.stride(), dk)):
         _head_tensor(dq, q.dtype, q.shape, q.device, "dq")
@@ -1096,7 +1099,9 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = 
     than `window` away from i + m - n where that is given. `q_lengths`, `k_lengths`
     [batch] int32 are each sequence's own n and m: what lies behind is not read,
     rows of out there are 0 and lse -inf, as where a query sees nothing. scale:
-    1 / sqrt(D) if none is given."""
+    1 / sqrt(D) if none is given, else 1e-30 to 1e30. With 16-bit types the
+    probabilities are rounded to the type for their product with v, sums are fp32.
+    out and lse overlap nothing else."""
     head = _attention_checks(q, k, v, causal, window, scale, q_lengths, k_lengths)
     out = _output_heads(out, q, "out")
     if lse is None:
@@ -1133,7 +1138,10 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     head. They may be given, of any strides (the parts of a projection's gradient,
     say). Behind a sequence's lengths, and for queries that see nothing, they are
     0. Nothing of queries times keys is stored: the probabilities are computed
-    again, tile by tile."""
+    again, tile by tile, and with 16-bit types rounded to the type like their
+    gradients. With fp16 a dk has fewer digits where only queries see its key whose
+    dout is far below the others' (2^-16 and less). The gradients overlap nothing
+    else, nor one another."""
     head = _attention_checks(q, k, v, causal, window, scale, q_lengths, k_lengths)
     if not _alike(q, q.stride(), dout, out):
         _head_tensor(dout, q.dtype, q.shape, q.device, "dout")

@@ -109,7 +109,8 @@ struct Mma<float> {
 // order takes a row's lowest bits to the chunk's highest for the latter and the
 // next ones below for the former; with rows of 2 to the 256 bytes, the lowest
 // bit is in the place already. fp32's columns are 32 neighbours of 2 rows,
-// rows 4 apart; its rows are two to a bank, as its products take 8 times as long.
+// rows 4 apart; its rows are two to a bank, as its matrix instructions take 16
+// times as long for as many products.
 template <class T, int DP, int ROWS_>
 struct Tile {
   typedef Mma<T> M;
@@ -359,17 +360,19 @@ constexpr int keys_of() { return sizeof(T) == 2 ? kKeys : kKeys / 2; }
 constexpr int kJoinThreads = 256;
 
 // ---- forward --------------------------------------------------------------------
-// The probabilities go to the second product in the type, 2^kHeld times as
-// large as they are below the running maximum, which is moved on where a score
-// passes it by a factor of 2^kPast. fp16 has 40 binary digits from its smallest
-// to its largest value: held at 2^13 and 2^2 past that, at most 2^15, those of
-// 2^-27 of the maximum have all their digits and those of 2^-38 are lost (held
-// at 1, 2^-14 and 2^-25: a row whose result is made of many such keys beside a
-// large one of value 0 lost its result). The larger kPast, the fewer rescalings:
-// 2^2 instead of 2^8 takes nothing that shows at 4 x 4096 tokens (585 and 592
-// us, where bf16's unchanged code gave 555 and 563) and up to 4 of 100 where ways
-// are short (5 x 1001 padded tokens, a window of 300: 16.6 and 17.2 us). bf16 has
-// fp32's range.
+// The probabilities go to the second product in the type, since 4-byte operands
+// would take 16 times as long: each is rounded by half a step at most, their sum
+// is taken before that. With bf16 the result is then off by 2.1e-3 of its norm
+// at 4 x 4096 tokens, where its own rounding leaves 1.6e-3.
+//
+// They are held 2^kHeld times as large below the running maximum, which is moved
+// on where a score passes it by a factor of 2^kPast. fp16 has 40 binary digits
+// from its smallest to its largest value: at 2^13 and 2^2 past that, at most
+// 2^15, those of 2^-27 of the maximum have all their digits and those of 2^-38
+// are lost (at 1, 2^-14 and 2^-25: a row whose result is made of many such keys
+// beside a large one of value 0 lost its result). The larger kPast, the fewer
+// rescalings: at 2^7 and 2^8 past that, 4 x 4096 tokens of 32 heads of 128 take
+// 597 us for 600, 65 queries of 16384 keys 20.6 for 21.2. bf16 has fp32's range.
 template <class T>
 constexpr float kHeld = std::is_same<T, f16>::value ? 13.0f : 0.0f;  // both as exponents
 template <class T>
@@ -380,10 +383,9 @@ constexpr float kPast = std::is_same<T, f16>::value ? 2.0f : 8.0f;
 // Two tiles to a turn, since each is at another place in LDS; the second of the
 // last turn may be past the end, where a wave passes it over like any tile it
 // does not see. (Leaving the loop between the two cost 36 register moves a tile,
-// 4 x 4096 tokens of 32 heads of 128, bf16, 629 us instead of 590.) Of the time
-// there, 930 TFLOP/s, the matrix instructions take half; the rest is the
-// softmax's, 7 vector instructions to each of them, which two waves to a SIMD
-// hide in part.
+// a fifteenth of the time.) 4 x 4096 tokens of 32 heads of 128, bf16: 567 us, 970
+// TFLOP/s. The matrix cores are busy half the time; the rest is the softmax's, 6
+// vector instructions to each matrix one, which two waves to a SIMD hide in part.
 template <class T, int DP, int NW, bool DIRECT>
 __global__ __launch_bounds__(NW * kWave, (sizeof(T) == 4 && DP > 64 ? 1 : 2)) void k_attention(Args a, Packing pk, uint32_t tiles,
                                                                          uint32_t parts, float* part) {
@@ -628,8 +630,9 @@ __device__ __forceinline__ float factor_of(float most) {
 // For dk and dv, what their products take off goes to `stats` ([batch][heads]
 // [queries] each): each row's lse in base 2 less the probabilities' exponent, or
 // +inf where they are 0, with 16-bit types as a score, before its scaling; and
-// its sum of dout * out. 4 x 4096 tokens of 32 heads of 128: 772 us, 1070
-// TFLOP/s, more than half of it matrix instructions.
+// its sum of dout * out. ds is rounded to the type for its product with k, like
+// the forward pass's probabilities and for the same reason. 4 x 4096 tokens of
+// 32 heads of 128: 765 us, 1080 TFLOP/s, matrix cores busy 59 of 100 of it.
 template <class T, int DP, int NW, bool DIRECT>
 __global__ __launch_bounds__(NW * kWave, (sizeof(T) == 4 && DP > 64 ? 1 : 2)) void k_attention_dq(Args a, Packing pk, uint32_t tiles, float* stats,
                                                                             const float* norms, uint32_t parts, float* part) {
@@ -754,7 +757,11 @@ __global__ __launch_bounds__(kJoinThreads) void k_attention_join_dq(Args a, Pack
 // workgroup's. It holds k, v, dk and dv, with 128-element heads 192 registers, so
 // that there is one wave to a SIMD (the second one's spills took 2800 us instead
 // of 1960 for the gradients of 4 x 4096 tokens of 32 heads of 128) and nothing
-// hides the vector instructions between the products, nor the reads from LDS.
+// hides the vector instructions between the products, nor the reads from LDS:
+// matrix cores busy 42 of 100 of the time, 870 TFLOP/s of its own four products.
+// s and dout v^T are computed here and for dq: sharing them would take sums in
+// memory that several workgroups add to, in an order that changes results.
+// p is rounded to the type for its product with dout, ds for that with q.
 // The mask is applied in the middle of the one way through a tile's products:
 // a way of its own for masked tiles had the results moved to other registers at
 // its end, 2150 us instead of 1960.
@@ -1019,11 +1026,12 @@ struct Plan {
 
   // Few workgroups with long ways are split so that all compute units are
   // full: two workgroups each, one of those that hold 128-element heads' dk and
-  // dv (5 sequences of 1001, 80-element heads, in 3 parts: gradients 82 us, in
-  // one 77). Parts have `shortest` tiles at least, and a way that has fewer than
+  // dv (5 sequences of 1001, 80-element heads, in 3 parts: gradients 80 us, in
+  // one 74). Parts have `shortest` tiles at least, and a way that has fewer than
   // `least` is not worth the kernel that joins it: 512 tokens of 16 heads of 64
-  // take 12 us, in parts of 4 tiles 20; an fp32 tile takes about 6 times as long,
-  // and 128 queries of 512 keys 14 us in parts of 2, else 18.
+  // take 12 us, in parts of 4 tiles 17; an fp32 tile takes about 6 times as long,
+  // and 128 queries of 512 keys 17 us in parts of 2, in one 44. The rule knows the
+  // sizes alone: workgroups past a sequence's length count, too.
   static uint32_t parts_of(const Args& a, uint64_t workgroups, uint64_t way, uint64_t full) {
     const uint64_t shortest = a.type == SPARCML_F32 ? 2 : 4, least = a.type == SPARCML_F32 ? 4 : 16;
     if (workgroups == 0 || workgroups * 2 > full || way < least) return 1;

@@ -13,10 +13,12 @@
 // results are rounded once, at the store.
 //
 // Both are bound by memory, large calls by its rate (65536 tokens of 32 + 8 heads
-// of 128, bf16: forward 255 us, 5.3 TB/s, backward 390 us, 5.2 TB/s; a large copy
-// reaches 4.95), small ones by the launch (8 tokens: 4 us of a call's 12). What is
-// read and written is touched once and goes past the caches, which takes 4 of 100
-// off. A head's D elements are held by L lanes, two packs
+// of 128, bf16: forward 247 us, 5.4 TB/s, backward 383 us, 5.3 TB/s; a large copy
+// reaches 4.95), small ones by the launch (8 tokens: 4.6 us of a call's 12.6).
+// With one or two heads a token the angles, in 64 bits, count too (3 nodes of
+// 275557 tokens, 1 + 1 heads of 80: gradients 342 us, without turning 238, 161 by
+// the bytes). What is read and written is touched once and goes past the caches,
+// which takes 4 of 100 off. A head's D elements are held by L lanes, two packs
 // of V elements each, chosen so that a pair is in one lane (halves: the packs
 // are as far apart as the pair's elements; interleaved: the packs are next to
 // each other). A wave takes a token with all its heads, or several tokens where
@@ -149,8 +151,8 @@ struct Turn {
 
 // How a wave's S::H groups of lanes are dealt: to `tokens` tokens, `heads` groups
 // each, a power of two that takes a token's heads at once where there are as
-// many (a call of 58454 tokens of 2 query and 2 key heads of 64 takes 26 us so,
-// with all groups to one token's heads 55).
+// many (a call of 58454 tokens of 2 query and 2 key heads of 64 takes 23 us so,
+// with all groups to one token's heads 53).
 template <class S>
 struct Dealt {
   uint32_t heads, tokens, token, head;  // token, head: the lane's first
@@ -325,7 +327,9 @@ hipError_t with_slots(const sparcml_head_norm_args& g, F&& f) {
 // Workgroups of a node, 8 to a CU in all, each of whose waves has `least` tokens
 // at least: backward 4, since a workgroup's sums of its weights' gradients take
 // as long as a token's heads do (a call of 64 nodes of 98 tokens, 32 + 4 heads of
-// 32, takes 33 us so, with 1 token 42, with 2 38, with 8 42).
+// 32, takes 30 us so, with 1 token 42, with 2 35, with 8 40; where the chip is not
+// full anyway, 3 nodes of 1001 tokens, 6 + 2 fp32 heads of 80, kernels 21 us, with
+// 1 token 17, which the call hides: 24.6 and 24.4).
 constexpr uint32_t kLeastTokens = 4;
 uint32_t chunks_of(uint32_t nodes, uint64_t tokens, uint32_t least) {
   const uint64_t most = (2048 + nodes - 1) / nodes, wanted = (tokens + kWaves * least - 1) / (kWaves * least);
